@@ -11,7 +11,10 @@
  *   - the FP8xFP4 expert FFN, the single-GPU compute share of the fused MoE layer
  *     (news page "DeepSeek 发布 DeepGEMM 重大更新：Mega MoE 融合算子与 FP4 精度支持",
  *      sections Mega MoE and FP4 精度支持: linear1 -> SwiGLU -> linear2 -> combine,
- *      FP4 weights with UE8M0 scales packed four per int32).
+ *      FP4 weights with UE8M0 scales packed four per int32);
+ *   - the operators that make those operands and use them at four bits: quantisation
+ *     to MXFP4, the MXFP4 x MXFP4 dense GEMM, and RMS norm with the residual's
+ *     addition and a quantised output, with its backward pass.
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers to dense row-major arrays (last index
@@ -369,6 +372,109 @@ int dg_m_grouped_fp8_fp4_gemm_nt_masked(const uint8_t* a, const int32_t* a_sf, c
 int dg_k_grouped_fp8_gemm_tn_contiguous(const uint8_t* a, const float* sfa, const uint8_t* b, const float* sfb,
                                         const int32_t* ks, uint16_t* d, int m, int n, int k, int num_groups,
                                         void* stream);
+
+/*
+ * Quantisation to MXFP4: blocks of 32 consecutive values share a power-of-two
+ * scale 2^e and hold E2M1 codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6).
+ *   e    = the smallest integer with 6 * 2^e >= max |x| over the block, at least
+ *          -127; 0 where the block is all zeros
+ *   code = E2M1 nearest to x * 2^-e, ties to the even code; no value saturates
+ * A block that holds a NaN or an infinity gets the exponent byte 255 (NaN) and
+ * codes 0: its products are NaN.  A zero keeps its sign.
+ *
+ *   x      [num_groups, m, k]            bf16 (DG_BF16) or fp32 (DG_F32)
+ * blocks along k (both or neither; q is the A or B operand of the GEMMs below,
+ * and with sf the weights of the FP8 x FP4 entry points):
+ *   q      [num_groups, m, k/2]          E2M1 pairs; element 2i in the low nibble of byte i
+ *   sf     [num_groups, k/128, m]        int32, four UE8M0 exponents per word (byte i of word
+ *                                        [g][kb][r]: values 128kb+32i..+32 of row r), the
+ *                                        K-block-major layout dg_transform_fp4_weight_sf writes
+ * blocks along m, of the transposed operand (both or neither), which a product
+ * that sums over m reads; mp = 128 * ceil(m/128), rows m .. mp-1 count as zeros:
+ *   qt     [num_groups, k, mp/2]         E2M1 pairs along m
+ *   sft    [num_groups, mp/128, k]       int32
+ *   values [num_groups, m, k]            bf16, optional: what q and sf stand for, code * 2^e,
+ *                                        exactly (a NaN block: NaN), for a forward pass that
+ *                                        trains through the rounding
+ * At least one of q, qt and values is given; x is read once.
+ * Requirements: num_groups, m, k > 0; k % 128 == 0 and num_groups * m, m + 127 at
+ *   most 2^31 - 1 (else DG_ERR_UNSUPPORTED).  Outputs must not overlap x or each other.
+ */
+typedef enum dg_dtype { DG_BF16 = 0, DG_F32 = 1 } dg_dtype;
+int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t* sf, uint8_t* qt, int32_t* sft,
+                      uint16_t* values, int num_groups, int m, int k, void* stream);
+
+/*
+ * MXFP4 x MXFP4 dense NT GEMM: d[i][j] = bf16( c[i][j] + sum_k A[i][k] * B[j][k] ),
+ * A[i][k] = e2m1(a[i][k]) * 2^(a_sf exponent of (i, k/32)) and B likewise.  The matrix
+ * cores apply both scales; the sum is fp32.
+ *   a     [m, k/2]      E2M1 pairs; a_sf [k/128, m] int32 (as dg_quantize_mxfp4's q and sf)
+ *   b     [n, k/2]      E2M1 pairs; b_sf [k/128, n] int32
+ *   c     [m, n]        bf16, or NULL for C = 0 (16-byte aligned)
+ *   d     [m, n]        bf16 output (may alias c only if identical)
+ *   workspace, workspace_bytes
+ *         device scratch of at least dg_mxfp4_gemm_workspace_bytes(m, n, k, 0) bytes,
+ *         16-byte aligned; may be NULL when that is 0.
+ * The products of a linear layer's training step are all of this form, on the
+ * operands that dg_quantize_mxfp4 makes from x [T, K], w [N, K] and dy [T, N]:
+ * y = q(x) . q(w)^T, dx = q(dy) . qt(w)^T, dw = qt(dy) . qt(x)^T.
+ * An exponent byte 255 gives NaN results.
+ * Requirements: m, n, k > 0; k % 128 == 0; n % 16 == 0; m*k/2, n*k/2, 2*m*n and the scales'
+ *   bytes m*k/32 and n*k/32 at most 2^31, else DG_ERR_UNSUPPORTED.
+ */
+int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
+                     const uint16_t* c, uint16_t* d, int m, int n, int k, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace dg_mxfp4_gemm_nt needs for these sizes (0: none; 0 also for
+ * invalid sizes, whose calls fail with their own status).  num_cus as in
+ * dg_fp8_gemm_workspace_bytes. */
+size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
+
+/*
+ * RMS norm with the residual's addition and a quantised output, the step in front
+ * of a layer's GEMM.  Per row:
+ *   h = bf16(x + residual)                 (residual NULL: h = x)
+ *   r = 1 / sqrt(mean(h^2) + eps)          fp32
+ *   y = h * r * weight                     fp32, not rounded before it is quantised
+ * and y is quantised in the format the GEMM behind it reads:
+ *   DG_QUANT_E4M3_F32    q [m, k] e4m3, sf [k/128, m] fp32: s = max|y| / 448 per 1x128 block (at
+ *                        least 2^-126; 1 where the block is all zeros), code = e4m3(y / s): A of
+ *                        dg_fp8_gemm_nt and the other fp32-scale forms
+ *   DG_QUANT_E4M3_UE8M0  q [m, k] e4m3, sf [m, ceil(k/512)] int32: the smallest power of two
+ *                        with 448 * 2^e >= max|y| per 1x128 block (2^0 for zeros and for the
+ *                        unused bytes of the last word): A of the _ue8m0 forms, x of the FFN
+ *   DG_QUANT_MXFP4       q [m, k/2], sf [k/128, m] int32 as dg_quantize_mxfp4: A of dg_mxfp4_gemm_nt
+ * A block of y with a NaN or an infinity gets a NaN scale; its codes are NaN (e4m3)
+ * or 0 (E2M1).  Squares are summed in fp32: a row whose sum of squares passes
+ * fp32's range gives r = 0.
+ *   x, residual [m, k]  bf16; weight [k] bf16
+ *   h           [m, k]  bf16 output, or NULL; may be x or residual itself (in place)
+ *   rstd        [m]     fp32 output r, or NULL (the backward pass needs it)
+ * Requirements: m, k > 0, eps > 0 and finite; k % 128 == 0 and k <= 32768 (else
+ *   DG_ERR_UNSUPPORTED); 16-byte aligned tensors (sf and rstd: 4).
+ */
+typedef enum dg_quant_format { DG_QUANT_E4M3_F32 = 0, DG_QUANT_E4M3_UE8M0 = 1, DG_QUANT_MXFP4 = 2 } dg_quant_format;
+int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h, void* q,
+                    void* sf, int format, float* rstd, int m, int k, float eps, void* stream);
+
+/*
+ * Its backward pass; the gradient passes straight through the quantisation.  With
+ * n = h * r and g = dy * weight:
+ *   dx[i]      = bf16( dh[i] + r * (g[i] - n[i] * mean(g * n)) )   the gradient of x and of residual alike
+ *   dweight[i] = sum over rows of dy[i] * n[i]                     fp32, summed in a fixed order
+ *   dy      [m, k] bf16, the gradient of y; dh [m, k] bf16, the gradient that arrives at h from
+ *           the residual stream, or NULL
+ *   h       [m, k] bf16, weight [k] bf16, rstd [m] fp32 from the forward pass
+ *   dx      [m, k] bf16 (may be dy or dh itself); dweight [k] fp32
+ *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned
+ * Requirements: as dg_add_rms_norm's.
+ */
+int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                             const float* rstd, uint16_t* dx, float* dweight, int m, int k, void* workspace,
+                             size_t workspace_bytes, void* stream);
+/* Bytes of that workspace (0 for invalid sizes).  Host-only. */
+size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k);
 
 /* Row alignment of each group in the contiguous layout (usage guide, 工具函数). Returns 128. */
 int dg_get_mk_alignment_for_contiguous_layout(void);

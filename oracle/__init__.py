@@ -18,10 +18,12 @@ Modules
 ``ref``      the four reference operations: dense NT GEMM, M-grouped contiguous,
              M-grouped masked, and the FP8xFP4 expert FFN, plus per-element
              evaluators for spot checks at full size.
+``mx``       MXFP4 quantisation and GEMM, RMS norm forward and backward (pinned in
+             ``tests/test_oracle_mx.py``).
 
 Pins: every function here is checked against something other than itself in
 ``tests/test_oracle.py`` (library decoders, exact rational brute force, closed
 forms, exact power-of-two cases, invariants).  No function is "parity unpinned".
 """
 
-from . import formats, ref  # noqa: F401
+from . import formats, mx, ref  # noqa: F401

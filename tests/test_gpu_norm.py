@@ -1,0 +1,317 @@
+"""RMS norm with the residual's addition and a quantised output, and its backward pass, against the float64 oracle.
+
+Tolerances.  The sum of k squares (positive terms) in fp32, added over at most k/64 values per thread and 16 steps
+between threads, is off by (k/64 + 16) 2^-24 of itself; r = 1/sqrt by half of that and 4 roundings of 2^-24; y = h r w
+and its scale by two more each.  D below is the sum, relative to y.  A code is one nearest to a value within D of the
+exact y, so its value is no further from y than the nearest point of the grid is, by 2 D |y| (the move of y counts on
+both sides), and a block's scale follows an amax within D of the exact one.
+y is an fp32 value: below 2^-126 its two products are each off by half the subnormal step, 2^-150, besides, so a value
+of at most 2^-150 may be 0 (and its block all zeros) and every bound on y has 2^-149 added.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx as X
+from oracle.formats import bf16_bits_to_f64, decode_e4m3, f64_to_bf16_bits
+from tests.helpers import bits
+from tests.test_gpu_mxfp4 import guarded
+
+pytestmark = pytest.mark.gpu
+
+F32, UE8M0, MX = 0, 1, 2
+
+
+def rel(k):
+    return ((k / 64 + 16) / 2 + 8) * 2.0 ** -24
+
+
+def bf(seed, *shape, scale=1.0):
+    return f64_to_bf16_bits(np.random.default_rng(seed).standard_normal(shape) * scale)
+
+
+def dev(b):
+    return None if b is None else torch.from_numpy(b.view(np.int16).copy()).cuda().view(torch.bfloat16)
+
+
+def run_norm(dgm, x, res, w, fmt, eps=1e-6, want_h=True, inplace=None):
+    m, k = x.shape
+    tx, tr, tw = dev(x), dev(res), dev(w)
+    q, cq = guarded((m, k // 2 if fmt == MX else k), torch.uint8)
+    sf, cs = guarded((m, (k + 511) // 512) if fmt == UE8M0 else (k // 128, m), torch.float32 if fmt == F32 else torch.int32)
+    rstd, cr = guarded((m,), torch.float32)
+    h, ch = guarded((m, k), torch.bfloat16) if want_h else (None, lambda: None)
+    if inplace:
+        h = {"x": tx, "residual": tr}[inplace]
+    dgm.dg_add_rms_norm(tx, tr, tw, h, q, sf, eps, fmt, rstd)
+    torch.cuda.synchronize()
+    for c in (cq, cs, cr, ch):
+        c()
+    return q.cpu().numpy(), sf.cpu().numpy(), None if h is None else bits(h), rstd.cpu().numpy().astype(np.float64)
+
+
+def block_scales(sf, fmt, m, k):
+    """The scales per block [m, k/128] (or k/32) in float64."""
+    if fmt == F32:
+        return sf.T.astype(np.float64)
+    if fmt == MX:
+        return X.unpack_ue8m0_int32(np.ascontiguousarray(sf.T))
+    s = X.unpack_ue8m0_int32(sf)
+    assert (s[:, k // 128:] == 1).all(), "unused bytes of the last word"
+    return s[:, :k // 128]
+
+
+def check_norm(got, x, res, w, fmt, eps=1e-6):
+    q, sf, hb, rstd = got
+    m, k = x.shape
+    h, r, y = X.add_rms_norm(x, res, w, eps)
+    y = np.where(np.abs(y) <= 2.0 ** -150, 0.0, y)
+    if hb is not None:
+        assert np.array_equal(hb, f64_to_bf16_bits(h)), "h"
+    d = rel(k)
+    assert (np.abs(rstd - r) <= d * r).all(), "rstd"
+    blk = 32 if fmt == MX else 128
+    s = block_scales(sf, fmt, m, k)
+    amax = np.abs(y).reshape(m, k // blk, blk).max(axis=2)
+    if fmt == F32:
+        want = np.where(amax > 0, np.maximum(amax / 448, 2.0 ** -126), 1.0)
+        assert (np.abs(s - want) <= d * want).all(), "scales"
+        unit = s
+    else:
+        qmax = 6.0 if fmt == MX else 448.0
+        e = np.log2(s)
+        assert (e == np.round(e)).all()
+        zero = amax == 0
+        assert (s[zero] == 1).all()
+        assert (qmax * s >= amax * (1 - d))[~zero].all(), "a scale too small"
+        assert ((qmax * s / 2 < amax * (1 + d)) | (e == -127))[~zero].all(), "a scale too large"
+        unit = s
+    unit = np.repeat(unit, blk, axis=1)
+    grid = X.E2M1_GRID if fmt == MX else X.E4M3_GRID
+    v = (X.unpack_e2m1(q) if fmt == MX else decode_e4m3(q)) * unit
+    a = np.minimum(np.abs(y) / unit, grid[-1])
+    best = np.abs(grid[X.nearest_code(a, grid)] * unit - np.abs(y))
+    bad = ~(np.abs(v - y) <= best + 2 * (d * np.abs(y) + 2.0 ** -149))
+    assert not bad.any(), f"{bad.sum()} codes, first at {np.argwhere(bad)[0]}: {v[bad][0]} for {y[bad][0]}"
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+@pytest.mark.parametrize("m,k", [(1, 128), (3, 7168), (9, 640), (130, 2048), (33, 5120), (2, 16384), (5, 32768),
+                                 (700, 1536), (2100, 384)])
+def test_norm_shapes(dg, m, k, fmt):
+    x, res, w = bf(m, m, k, scale=2.0), bf(k, m, k), f64_to_bf16_bits(1 + 0.3 * np.random.default_rng(1).standard_normal(k))
+    r = res if (m + k // 128) % 3 else None
+    check_norm(run_norm(dg, x, r, w, fmt), x, r, w, fmt)
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+def test_norm_edges(dg, fmt):
+    """Rows of zeros, of tiny values (eps decides), with one large value; weights that are 0 over a block, and that
+    make amax subnormal; a row whose sum cancels."""
+    m, k = 8, 768
+    x, res, w = bf(3, m, k), bf(4, m, k), bf(5, k)
+    x[0], res[0] = 0, 0
+    x[1] = f64_to_bf16_bits(np.full(k, 2.0 ** -130))
+    res[1] = 0
+    x[2, 5] = f64_to_bf16_bits(np.float64(3e4))
+    res[3] = x[3] ^ 0x8000                                  # h = 0
+    w[128:256] = 0
+    w[256:384] = f64_to_bf16_bits(np.full(128, 2.0 ** -128))
+    check_norm(run_norm(dg, x, res, w, fmt), x, res, w, fmt)
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_norm_nonfinite(dg, fmt, value):
+    """A NaN makes its whole row NaN; an infinity its own block (r = 0 makes the others 0); other rows are unharmed."""
+    m, k = 5, 512
+    x, w = bf(6, m, k), f64_to_bf16_bits(np.ones(k))
+    x[2, 200] = f64_to_bf16_bits(np.float64(value)) if not np.isnan(value) else 0x7fc0
+    q, sf, _, rstd = run_norm(dg, x, None, w, fmt)
+    blk = 32 if fmt == MX else 128
+    s = block_scales(sf, fmt, m, k)
+    nan_block = np.zeros((m, k // blk), dtype=bool)
+    nan_block[2, :] = np.isnan(value)
+    nan_block[2, 200 // blk] = True
+    assert np.array_equal(np.isnan(s), nan_block)
+    v = X.unpack_e2m1(q) if fmt == MX else decode_e4m3(q)
+    if fmt != MX:
+        assert np.isnan(v[2, 200])
+    keep = [0, 1, 3, 4]
+    sub = (q[keep], (sf[keep] if fmt == UE8M0 else np.ascontiguousarray(sf[:, keep])), None, rstd[keep])
+    check_norm(sub, x[keep], None, w, fmt)
+
+
+@pytest.mark.parametrize("inplace", ["x", "residual"])
+def test_norm_in_place(dg, inplace):
+    x, res, w = bf(7, 40, 1024), bf(8, 40, 1024), bf(9, 1024)
+    check_norm(run_norm(dg, x, res, w, F32, inplace=inplace), x, res, w, F32)
+
+
+def test_norm_without_h(dg):
+    x, res, w = bf(7, 12, 1024), bf(8, 12, 1024), bf(9, 1024)
+    check_norm(run_norm(dg, x, res, w, UE8M0, want_h=False), x, res, w, UE8M0)
+
+
+def test_norm_large_batch_same_rows(dg):
+    """A row's outputs do not depend on the batch it is in (the row counts cross the kernel's variants)."""
+    k = 1536
+    x, res, w = bf(10, 5000, k), bf(11, 5000, k), bf(12, k)
+    big = run_norm(dg, x, res, w, MX)
+    for m in (1, 40, 1300):
+        part = run_norm(dg, x[:m], res[:m], w, MX)
+        v = [X.dequant_mxfp4(part[0], part[1]), X.dequant_mxfp4(big[0][:m], np.ascontiguousarray(big[1][:, :m]))]
+        assert np.array_equal(part[2], big[2][:m])
+        # (the row sum's order may differ between the variants: only codes at a border may)
+        assert (v[0] != v[1]).mean() <= 1e-3
+    check_norm(big, x, res, w, MX)
+
+
+def run_back(dgm, dy, dh, h, w, rstd, into=None):
+    m, k = dy.shape
+    t = dict(dy=dev(dy), dh=dev(dh), h=dev(h), w=dev(w), r=torch.from_numpy(rstd.astype(np.float32)).cuda())
+    dx, cx = guarded((m, k), torch.bfloat16) if into is None else (t[into], lambda: None)
+    dw, cw = guarded((k,), torch.float32)
+    ws, cws = guarded((dgm.dg_add_rms_norm_backward_workspace_bytes(m, k),), torch.uint8)
+    dgm.dg_add_rms_norm_backward(t["dy"], t["dh"], t["h"], t["w"], t["r"], dx, dw, ws)
+    torch.cuda.synchronize()
+    for c in (cx, cw, cws):
+        c()
+    return bits(dx), dw.cpu().numpy().astype(np.float64)
+
+
+def back_inputs(m, k, with_dh, seed=0):
+    h, w = bf(seed, m, k, scale=1.5), f64_to_bf16_bits(1 + 0.3 * np.random.default_rng(seed + 1).standard_normal(k))
+    dy, dh = bf(seed + 2, m, k, scale=0.1), bf(seed + 3, m, k, scale=0.1) if with_dh else None
+    r = 1 / np.sqrt(np.mean(bf16_bits_to_f64(h) ** 2, axis=1) + 1e-6)
+    return dy, dh, h, w, r.astype(np.float32)
+
+
+def check_back(got, dy, dh, h, w, rstd):
+    """dx: the bf16 rounding, 2^-8 of it, and fp32: the mean of k products within (k/64 + 16) 2^-24 of the mean of
+    their magnitudes, and 8 roundings of each term.  dweight: m products added in any order, (m + 4) 2^-24 of their
+    magnitudes' sum."""
+    m, k = dy.shape
+    f = [bf16_bits_to_f64(v) for v in (dy, h, w)]
+    d = None if dh is None else bf16_bits_to_f64(dh)
+    r = rstd.astype(np.float64)
+    dx, dw = X.add_rms_norm_backward(f[0], d, f[1], f[2], r)
+    n, g = f[1] * r[:, None], f[0] * f[2]
+    terms = r[:, None] * (np.abs(g) + np.abs(n) * np.mean(np.abs(g * n), axis=1, keepdims=True)) + (0 if d is None else np.abs(d))
+    bound = 2.0 ** -8 * np.abs(dx) + (k / 64 + 24) * 2.0 ** -24 * (1 + 2.0 ** -8) * terms
+    err = np.abs(bf16_bits_to_f64(got[0]) - dx)
+    assert (err <= bound).all(), f"dx: {(err > bound).sum()}, worst {np.max(err / np.maximum(bound, 1e-300))} of the bound"
+    bound = (m + 4) * 2.0 ** -24 * np.sum(np.abs(f[0] * n), axis=0)
+    assert (np.abs(got[1] - dw) <= bound).all(), "dweight"
+
+
+@pytest.mark.parametrize("with_dh", [False, True])
+@pytest.mark.parametrize("m,k", [(1, 128), (2, 7168), (130, 2048), (37, 640), (600, 1536), (1500, 384), (3, 32768),
+                                 (520, 5120), (9, 16384)])
+def test_backward_shapes(dg, m, k, with_dh):
+    a = back_inputs(m, k, with_dh, seed=m + k)
+    check_back(run_back(dg, *a), *a)
+
+
+@pytest.mark.parametrize("into", ["dy", "dh"])
+def test_backward_in_place(dg, into):
+    a = back_inputs(70, 1024, True)
+    want = run_back(dg, *a)
+    got = run_back(dg, *a, into=into)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+def test_backward_nonfinite_rows_stay_apart(dg):
+    """A NaN gradient makes its row of dx and its column of dweight NaN, and no other row of dx."""
+    dy, dh, h, w, r = back_inputs(300, 512, True)
+    dy[17, 100] = 0x7fc0
+    dx, dw = run_back(dg, dy, dh, h, w, r)
+    nan = np.isnan(bf16_bits_to_f64(dx))
+    assert nan[17].all() and not np.delete(nan, 17, axis=0).any()
+    assert np.isnan(dw[100]) and np.isfinite(np.delete(dw, 100)).all()
+
+
+def test_backward_against_differences_of_the_forward(dg):
+    """dx along a direction against the difference of the norm's own forward: with r and the scales of the F32 format
+    the unquantised y is not returned, so the forward is the oracle's, at the kernel's h and eps."""
+    m, k, eps = 3, 256, 1e-6
+    dy, _, h, w, r = back_inputs(m, k, False, seed=40)
+    dx = bf16_bits_to_f64(run_back(dg, dy, None, h, w, r)[0])
+    hv, wv, gv = (bf16_bits_to_f64(v) for v in (h, w, dy))
+    u = np.random.default_rng(3).standard_normal((m, k))
+
+    def loss(hh):
+        return np.sum(gv * hh / np.sqrt(np.mean(hh * hh, axis=1, keepdims=True) + eps) * wv, axis=1)
+    t = 1e-4                                               # central: error ~ t^2
+    diff = (loss(hv + t * u) - loss(hv - t * u)) / (2 * t)
+    got = np.sum(dx * u, axis=1)
+    # dx is rounded to bf16 (2^-8 of each term); r is fp32; the third derivative's share is t^2 ~ 1e-8 of the terms
+    assert (np.abs(got - diff) <= (2.0 ** -8 + 1e-6) * np.sum(np.abs(dx * u), axis=1)).all()
+
+
+def test_backward_repeats_and_graph_replays(dg):
+    m, k = 333, 7168
+    a = back_inputs(m, k, True, seed=50)
+    t = [dev(v) for v in a[:4]] + [torch.from_numpy(a[4]).cuda()]
+    want = dg.add_rms_norm_backward(*t)
+    dx, dw = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = torch.empty(dg.dg_add_rms_norm_backward_workspace_bytes(m, k), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dg.dg_add_rms_norm_backward(*t, dx, dw, ws)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.dg_add_rms_norm_backward(*t, dx, dw, ws)
+    for i in range(4):
+        for v in (dx, dw):
+            v.fill_(float("nan"))
+        ws.fill_(255 - i)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]), f"replay {i}"
+
+
+def test_a_block_of_calls_and_its_graph(dg):
+    """Norm -> MXFP4 GEMM -> norm -> FP8 GEMM with UE8M0 scales, as a layer runs them, eagerly against the oracle's
+    products on the kernels' own operands, and captured in a graph whose replays follow changed inputs."""
+    import synth
+    from oracle import ref as R
+    m, k, n = 70, 512, 768
+    x, res, w1, w2 = bf(60, m, k), bf(61, m, k), bf(62, k), bf(63, n)
+    tx, tr, tw1, tw2 = dev(x), dev(res), dev(w1), dev(w2)
+    wq, wsf = dg.quantize_mxfp4(torch.randn(n, k, device="cuda"))
+    b = synth.gen_dense_ue8m0(16, 256, n, seed=1, with_c=False)
+    b2, sfb2 = b["b"].cuda(), b["sfb"].cuda()
+
+    def block():
+        q, sf, h, _ = dg.add_rms_norm(tx, tr, tw1, 1e-6, dg.QUANT_MXFP4)
+        y = dg.mxfp4_gemm_nt(q, sf, wq, wsf)
+        q2, sf2, _, _ = dg.add_rms_norm(y, None, tw2, 1e-6, dg.QUANT_E4M3_UE8M0)
+        d = torch.empty(m, 256, dtype=torch.bfloat16, device="cuda")
+        dg.dg_fp8_gemm_nt_ue8m0(q2, sf2, b2, sfb2, None, d)
+        return q, sf, h, y, q2, sf2, d
+
+    q, sf, h, y, q2, sf2, d = block()
+    n_ = lambda t: t.cpu().numpy()                                                      # noqa: E731
+    check_norm((n_(q), n_(sf), bits(h), 1 / np.sqrt(np.mean(bf16_bits_to_f64(bits(h)) ** 2, axis=1) + 1e-6)), x, res, w1, MX)
+    ref = X.mxfp4_gemm_nt(n_(q), n_(sf), n_(wq), n_(wsf))
+    a_, b_ = X.dequant_mxfp4(n_(q), n_(sf)), X.dequant_mxfp4(n_(wq), n_(wsf))
+    assert (np.abs(bf16_bits_to_f64(bits(y)) - ref) <= 2.0 ** -8 * np.abs(ref) + (k / 8 + 1) * 2.0 ** -22 * (np.abs(a_) @ np.abs(b_).T)).all()
+    yb = bits(y)
+    check_norm((n_(q2), n_(sf2), None, 1 / np.sqrt(np.mean(bf16_bits_to_f64(yb) ** 2, axis=1) + 1e-6)), yb, None, w2, UE8M0)
+    ref = R.fp8_gemm_nt_ue8m0(n_(q2), n_(sf2), n_(b2), n_(sfb2))
+    from tests.helpers import check_parity
+    check_parity(bits(d), ref, what="block")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = block()
+    for i in range(3):
+        tx.copy_(dev(bf(70 + i, m, k)))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, block()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), f"replay {i}"
