@@ -454,23 +454,26 @@ _X_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
 QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4 = 0, 1, 2
 
 
-def _call(name, t, *args):
-    """The C entry point on tensor t's device and torch's current stream there."""
-    f = getattr(lib(), name)
-    dev = t.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(name, dev, *args):
+    """The C entry point on device dev and torch's current stream there.  (A decode step makes many calls of a few
+    microseconds: these wrappers read the raw stream and device index, and pass addresses as plain integers.)"""
+    f = getattr(_lib or load_library(), name)
+    index = dev.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         raise DgError(name, st)
 
 
-def _arg(t, dtypes, shape, like, name):
+def _arg(t, dtypes, shape, dev, name):
     """Checks one tensor argument (None passes) and returns its address."""
     if t is None:
         return None
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.device == dev and t.is_cuda:
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
@@ -479,28 +482,28 @@ def _arg(t, dtypes, shape, like, name):
         raise ValueError(f"{name}: must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, expected {dev}")
 
 
 _U8S, _I32S, _F32S = (_U8,), (torch.int32,), (torch.float32,)
+
+
+def _matrix_dims(x):
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: expected [m, k] or [G, m, k], got {tuple(x.shape)}")
+    return x.shape if x.dim() == 3 else (1, *x.shape)
 
 
 def dg_quantize_mxfp4(x, q=None, sf=None, qt=None, sft=None, values=None):
     """x [m, k] or [G, m, k] (bf16 or fp32) -> MXFP4 (see include/dg.h).  Blocks along k: q [.., m, k/2] uint8 and
     sf [.., k/128, m] int32; blocks along m, transposed: qt [.., k, mp/2] and sft [.., mp/128, k], mp = m rounded up
     to 128; values [.., m, k] bf16: what q and sf stand for.  Outputs that are None are not computed."""
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x: expected [m, k] or [G, m, k], got {tuple(x.shape)}")
-    lead = x.shape[:-2]
-    m, k = x.shape[-2:]
-    mb = (m + 127) // 128
-    xp = _arg(x, _X_TYPES, x.shape, x, "x")
-    _call("dg_quantize_mxfp4", x, xp, _X_TYPES[x.dtype], _arg(q, _U8S, (*lead, m, k // 2), x, "q"),
-          _arg(sf, _I32S, (*lead, k // 128, m), x, "sf"), _arg(qt, _U8S, (*lead, k, mb * 64), x, "qt"),
-          _arg(sft, _I32S, (*lead, mb, k), x, "sft"), _arg(values, _BF, x.shape, x, "values"),
-          lead[0] if lead else 1, m, k)
+    G, m, k = _matrix_dims(x)
+    lead, mb, dev = x.shape[:-2], (m + 127) // 128, x.device
+    xp = _arg(x, _X_TYPES, x.shape, dev, "x")
+    _call("dg_quantize_mxfp4", dev, xp, _X_TYPES[x.dtype], _arg(q, _U8S, (*lead, m, k // 2), dev, "q"),
+          _arg(sf, _I32S, (*lead, k // 128, m), dev, "sf"), _arg(qt, _U8S, (*lead, k, mb * 64), dev, "qt"),
+          _arg(sft, _I32S, (*lead, mb, k), dev, "sft"), _arg(values, _BF, x.shape, dev, "values"), G, m, k)
 
 
 def dg_mxfp4_gemm_workspace_bytes(m, n, k, num_cus=0):
@@ -511,18 +514,21 @@ def dg_mxfp4_gemm_workspace_bytes(m, n, k, num_cus=0):
 def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
     """d = c + a . b^T, both operands MXFP4: a [M, K/2] uint8, a_sf [K/128, M] int32, b [N, K/2], b_sf [K/128, N].
     workspace: optional uint8 device tensor (allocated here when needed and not given)."""
-    m, k = a.shape[0], 2 * a.shape[1]
-    n = b.shape[0]
+    m, kh = a.shape
+    n, k, dev = b.shape[0], 2 * kh, a.device
     kb = k // 128
-    args = (_arg(a, _U8S, (m, k // 2), a, "a"), _arg(a_sf, _I32S, (kb, m), a, "a_sf"),
-            _arg(b, _U8S, (n, k // 2), a, "b"), _arg(b_sf, _I32S, (kb, n), a, "b_sf"),
-            _arg(c, _BF, (m, n), a, "c"), _arg(d, _BF, (m, n), a, "d"), m, n, k)
+    ap = _arg(a, _U8S, (m, kh), dev, "a")
     if workspace is None:
-        need = lib().dg_mxfp4_gemm_workspace_bytes(m, n, k, 0)
-        if need:
-            workspace = torch.empty(need, dtype=_U8, device=a.device)
-    nbytes = 0 if workspace is None else workspace.numel()
-    _call("dg_mxfp4_gemm_nt", a, *args, _arg(workspace, _U8S, (nbytes,), a, "workspace"), nbytes)
+        nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=_U8, device=dev)
+            wp = workspace.data_ptr()
+    else:
+        nbytes = workspace.numel()
+        wp = _arg(workspace, _U8S, (nbytes,), dev, "workspace")
+    _call("dg_mxfp4_gemm_nt", dev, ap, _arg(a_sf, _I32S, (kb, m), dev, "a_sf"), _arg(b, _U8S, (n, kh), dev, "b"),
+          _arg(b_sf, _I32S, (kb, n), dev, "b_sf"), _arg(c, _BF, (m, n), dev, "c"), _arg(d, _BF, (m, n), dev, "d"),
+          m, n, k, wp, nbytes)
     return d
 
 
@@ -533,13 +539,13 @@ def dg_add_rms_norm(x, residual, weight, h, q, sf, eps, quant_format, rstd=None)
     m, k = x.shape
     if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
         raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
-    mx = quant_format == QUANT_MXFP4
+    shape, dev = (m, k), x.device
     sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
-    _call("dg_add_rms_norm", x, _arg(x, _BF, (m, k), x, "x"), _arg(residual, _BF, (m, k), x, "residual"),
-          _arg(weight, _BF, (k,), x, "weight"), _arg(h, _BF, (m, k), x, "h"),
-          _arg(q, _U8S, (m, k // 2 if mx else k), x, "q"),
-          _arg(sf, _F32S if quant_format == QUANT_E4M3_F32 else _I32S, sf_shape, x, "sf"), quant_format,
-          _arg(rstd, _F32S, (m,), x, "rstd"), m, k, eps)
+    _call("dg_add_rms_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
+          _arg(weight, _BF, (k,), dev, "weight"), _arg(h, _BF, shape, dev, "h"),
+          _arg(q, _U8S, (m, k // 2) if quant_format == QUANT_MXFP4 else shape, dev, "q"),
+          _arg(sf, _F32S if quant_format == QUANT_E4M3_F32 else _I32S, sf_shape, dev, "sf"), quant_format,
+          _arg(rstd, _F32S, (m,), dev, "rstd"), m, k, eps)
 
 
 def dg_add_rms_norm_backward_workspace_bytes(m, k):
@@ -550,10 +556,11 @@ def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace):
     """dx [m, k] bf16 and dweight [k] fp32 from dy, dh (or None), h [m, k] bf16, weight [k] bf16 and the forward
     pass's rstd [m] (see include/dg.h)."""
     m, k = dy.shape
-    _call("dg_add_rms_norm_backward", dy, _arg(dy, _BF, (m, k), dy, "dy"), _arg(dh, _BF, (m, k), dy, "dh"),
-          _arg(h, _BF, (m, k), dy, "h"), _arg(weight, _BF, (k,), dy, "weight"), _arg(rstd, _F32S, (m,), dy, "rstd"),
-          _arg(dx, _BF, (m, k), dy, "dx"), _arg(dweight, _F32S, (k,), dy, "dweight"), m, k,
-          _arg(workspace, _U8S, (workspace.numel(),), dy, "workspace"), workspace.numel())
+    shape, dev = (m, k), dy.device
+    _call("dg_add_rms_norm_backward", dev, _arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"),
+          _arg(h, _BF, shape, dev, "h"), _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"),
+          _arg(dx, _BF, shape, dev, "dx"), _arg(dweight, _F32S, (k,), dev, "dweight"), m, k,
+          _arg(workspace, _U8S, (workspace.numel(),), dev, "workspace"), workspace.numel())
 
 
 def dg_get_mk_alignment_for_contiguous_layout():
@@ -633,25 +640,30 @@ def fp8_fp4_expert_ffn(x, x_sf, topk_idx, topk_w, w1, w1_sf, w2, w2_sf, expert_o
     return dg_fp8_fp4_expert_ffn(x, x_sf, topk_idx, topk_w, w1, w1_sf, w2, w2_sf, y, expert_offset, workspace)
 
 
+# (The outputs made here need no checks: these call the C entry points themselves.)
+
 def quantize_mxfp4(x, transposed=False, values=False):
     """MXFP4 of x [m, k] or [G, m, k] (bf16 or fp32): (q, sf), the operand whose products sum over k; with transposed,
     (q, sf, qt, sft), qt and sft the transposed operand, whose products sum over m; with values, also the bf16 values
     that q and sf stand for, as the last item."""
-    lead = x.shape[:-2]
-    m, k = x.shape[-2:]
-    q = torch.empty((*lead, m, k // 2), dtype=_U8, device=x.device)
-    sf = torch.empty((*lead, k // 128, m), dtype=torch.int32, device=x.device)
+    G, m, k = _matrix_dims(x)
+    lead, dev = x.shape[:-2], x.device
+    xp = _arg(x, _X_TYPES, x.shape, dev, "x")
+    q = torch.empty((*lead, m, k // 2), dtype=_U8, device=dev)
+    sf = torch.empty((*lead, k // 128, m), dtype=torch.int32, device=dev)
     out = (q, sf)
-    qt = sft = v = None
+    qtp = sftp = vp = None
     if transposed:
         mb = (m + 127) // 128
-        qt = torch.empty((*lead, k, mb * 64), dtype=_U8, device=x.device)
-        sft = torch.empty((*lead, mb, k), dtype=torch.int32, device=x.device)
+        qt = torch.empty((*lead, k, mb * 64), dtype=_U8, device=dev)
+        sft = torch.empty((*lead, mb, k), dtype=torch.int32, device=dev)
+        qtp, sftp = qt.data_ptr(), sft.data_ptr()
         out += (qt, sft)
     if values:
-        v = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        v = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        vp = v.data_ptr()
         out += (v,)
-    dg_quantize_mxfp4(x, q, sf, qt, sft, v)
+    _call("dg_quantize_mxfp4", dev, xp, _X_TYPES[x.dtype], q.data_ptr(), sf.data_ptr(), qtp, sftp, vp, G, m, k)
     return out
 
 
@@ -665,26 +677,35 @@ def add_rms_norm(x, residual, weight, eps=1e-6, quant_format=QUANT_E4M3_F32):
     """(q, sf, h, rstd): the quantised norm of h = x + residual (residual None: h is x itself), with h and
     rstd = 1 / rms(h) for the residual stream and the backward pass."""
     m, k = x.shape
-    dev = x.device
-    q = torch.empty((m, k // 2 if quant_format == QUANT_MXFP4 else k), dtype=_U8, device=dev)
+    shape, dev = (m, k), x.device
+    xp, rp = _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual")
+    wp = _arg(weight, _BF, (k,), dev, "weight")
+    q = torch.empty((m, k // 2) if quant_format == QUANT_MXFP4 else shape, dtype=_U8, device=dev)
     if quant_format == QUANT_E4M3_UE8M0:
         sf = torch.empty((m, _kw(k)), dtype=torch.int32, device=dev)
     else:
         sf = torch.empty((k // 128, m), dtype=torch.float32 if quant_format == QUANT_E4M3_F32 else torch.int32,
                          device=dev)
-    h = None if residual is None else torch.empty_like(x)
     rstd = torch.empty(m, dtype=torch.float32, device=dev)
-    dg_add_rms_norm(x, residual, weight, h, q, sf, eps, quant_format, rstd)
-    return q, sf, x if h is None else h, rstd
+    h, hp = x, None
+    if residual is not None:
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
+    _call("dg_add_rms_norm", dev, xp, rp, wp, hp, q.data_ptr(), sf.data_ptr(), quant_format, rstd.data_ptr(), m, k, eps)
+    return q, sf, h, rstd
 
 
 def add_rms_norm_backward(dy, dh, h, weight, rstd):
     """(dx, dweight) of add_rms_norm: dx bf16 is the gradient of x and of residual alike, dweight fp32."""
     m, k = dy.shape
+    shape, dev = (m, k), dy.device
+    ins = (_arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"), _arg(h, _BF, shape, dev, "h"),
+           _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"))
     dx = torch.empty_like(dy)
-    dweight = torch.empty(k, dtype=torch.float32, device=dy.device)
-    ws = torch.empty(lib().dg_add_rms_norm_backward_workspace_bytes(m, k), dtype=_U8, device=dy.device)
-    dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, ws)
+    dweight = torch.empty(k, dtype=torch.float32, device=dev)
+    nbytes = (_lib or load_library()).dg_add_rms_norm_backward_workspace_bytes(m, k)
+    ws = torch.empty(nbytes, dtype=_U8, device=dev)
+    _call("dg_add_rms_norm_backward", dev, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, ws.data_ptr(), nbytes)
     return dx, dweight
 
 

@@ -7,7 +7,24 @@
 // its row: 16 bytes, and byte g of the row's scale word.  Blocks are computed
 // transposed (B's rows as the instruction's first operand), so a lane's four results
 // are four consecutive columns of one row of D.
+//
+// Tile kernel (persistent, eight waves, two per SIMD):
+//   * a stage is 256 values of K, so a tile row is one 128-byte line; A, B and their
+//     scale words come through a ring of R LDS slots by LDS-DMA loads;
+//   * a wave multiplies K block kb while it reads the fragments of kb + 1: A's into a
+//     second register set, B's into the registers of the column block that has just
+//     had its last use;
+//   * one barrier per stage, inside its second K block, after the first two column
+//     blocks: by then the wave's reads of the slot are back without a wait.  It frees
+//     the slot for stage s + R and certifies stage s + 1;
+//   * the stage copies run on into the next tile, so its first stage is there when
+//     the tile ends; D goes from the registers to memory, 16 bytes a lane: the columns
+//     of B's fragments are permuted so that a lane's two neighbouring column blocks
+//     are eight adjacent columns;
+//   * K may be split (few tiles, or a small last round): slices write fp32 partial
+//     tiles to the workspace, which the split-K reduce adds in slice order.
 #include <algorithm>
+#include <cstdlib>
 
 #include "../../include/dg.h"
 #include "dg_device.hpp"
@@ -22,7 +39,12 @@ struct Mxfp4Params {
   const int32_t* b_sf;
   const uint16_t* c;
   uint16_t* d;
+  float* ws;
   int m, n, k;
+  int tiles_m, tiles_n, group_m;
+  int splits, kb_per_split;   // K slices of a split tile, K blocks per slice (even)
+  int full_tiles;             // tiles [0, full_tiles) run whole, the others are split
+  int units;                  // whole tiles and slices
 };
 
 __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, uint32_t sa, const v4i& b, uint32_t sb, const v4f& c) {
@@ -30,95 +52,620 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, uint32_t sa, const v4i& 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, FMT_E2M1, FMT_E2M1, 0, (int)sa, 0, (int)sb);
 }
 
-// One wave per workgroup computes 64 x 64 of D with fragments read from memory.
-// Rows past the end of A or B are read from the last row; their results are not stored.
-__global__ void __launch_bounds__(64) mxfp4_gemm_kernel(Mxfp4Params p) {
-  constexpr int T = 4;
-  const int lane = threadIdx.x, lrow = lane & 15, lgrp = lane >> 4;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int kb_n = p.k >> 7;
-  const uint8_t* ap[T];
-  const uint8_t* bp[T];
-  int ar[T], br[T];
-#pragma unroll
-  for (int i = 0; i < T; ++i) {
-    ar[i] = min(m0 + i * 16 + lrow, p.m - 1);
-    br[i] = min(n0 + i * 16 + lrow, p.n - 1);
-    ap[i] = p.a + (size_t)ar[i] * (p.k / 2) + lgrp * 16;
-    bp[i] = p.b + (size_t)br[i] * (p.k / 2) + lgrp * 16;
-  }
-  v4f acc[T][T];
-#pragma unroll
-  for (int i = 0; i < T; ++i)
-#pragma unroll
-    for (int j = 0; j < T; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < kb_n; ++kb) {
-    v4i af[T], bf[T];
-    uint32_t sa[T], sb[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      af[i] = *reinterpret_cast<const v4i*>(ap[i] + (size_t)kb * 64);
-      bf[i] = *reinterpret_cast<const v4i*>(bp[i] + (size_t)kb * 64);
-      sa[i] = (uint32_t)p.a_sf[(size_t)kb * p.m + ar[i]] >> (8 * lgrp) & 255u;
-      sb[i] = (uint32_t)p.b_sf[(size_t)kb * p.n + br[i]] >> (8 * lgrp) & 255u;
+// WM x WN waves of MT x NT blocks of 16 x 16; R ring slots.
+template <int MT_, int NT_, int WM_, int WN_, int R_>
+struct MxTile {
+  static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, R = R_;
+  static constexpr int NW = WM * WN, THREADS = NW * 64;
+  static constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
+  static constexpr int OFF_B = BM * 128, OFF_SA = OFF_B + BN * 128, OFF_SB = OFF_SA + BM * 8;
+  static constexpr int STAGE = OFF_SB + BN * 8, LDS = R * STAGE;
+  static constexpr int RA = BM / 8 / NW, RB = BN / 8 / NW;   // 1-KB copies (8 rows) per wave and stage
+  static constexpr int LPS = RA + RB + 2;                    // copies per wave and stage, with the scales'
+  static constexpr int NSA = BM / 32, NSB = BN / 32;         // 64-word scale copies of a stage
+  static constexpr int NSTORE = MT * NT / 2;                 // 16-byte stores of D per lane
+  static constexpr int BAR = NT > 2 ? 2 : 1;                 // column blocks ahead of the barrier
+  static_assert(NW == 8 && NSA <= NW && NSB <= NW && NW % NSA == 0 && NW % NSB == 0, "scale copies");
+  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024, "tile shape");
+};
+
+// chunk swizzle of a B row: the 16 rows that one fragment read touches (8a + b, a, b
+// = 0..3, plus 4 in odd column blocks) fall on distinct 16-byte bank groups
+__device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) & 6); }
+
+// The value x, opaque to the compiler: lane-dependent terms that only a change of tile
+// needs are formed there, not held in registers through the K loop.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p) {
+  constexpr int MT = T::MT, NT = T::NT, R = T::R;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_m = wave / T::WN, wave_n = wave % T::WN;
+  const int lrow = lane & 15, lgrp = lane >> 4;
+  const int M = p.m, N = p.n;
+  const uint32_t Kh = (uint32_t)p.k >> 1;   // bytes of an operand row
+  const int KB = p.k >> 7;
+
+  const int G = gridDim.x;
+  int vb = blockIdx.x;
+  if ((G & 7) == 0) vb = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
+  if (vb >= p.units) return;
+
+  struct Unit {
+    int m0, n0, kb0, nkb, part;
+  };
+  auto decode = [&](int t) -> Unit {
+    Unit w{0, 0, 0, KB, -1};
+    if (t >= p.full_tiles) {
+      const int u = t - p.full_tiles;
+      w.kb0 = (u % p.splits) * p.kb_per_split;
+      w.nkb = min(p.kb_per_split, KB - w.kb0);
+      w.part = u;
+      t = p.full_tiles + u / p.splits;
     }
+    int tm, tn;
+    raster_tile(t, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    w.m0 = tm * T::BM;
+    w.n0 = tn * T::BN;
+    return w;
+  };
+
+  const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
+  const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
+  const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
+  const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
+
+  // The copy cursor: the unit and stage copied next.  Copy j of a wave fills rows
+  // 8 (RA wave + j) .. + 7 of the A tile: lane l position l % 8 of row (..) + l / 8,
+  // which holds chunk (l % 8) ^ swizzle(row); the swizzle's part that depends on j is
+  // uniform.  Rows past M lie past the buffer and read zeros, and so does the second
+  // K block of a stage at an odd end of K: a zero code under a finite scale adds nothing.
+  int cu = vb, cs = 0, c_kb0 = 0, c_nkb = 0;
+  uint32_t slot_w = 0;   // the slot copied into next
+  uint32_t a_row = 0, b_row = 0, sa_off = 0, sb_off = 0;
+  const uint32_t a_bc = (uint32_t)((lane & 7) ^ (lane >> 3)) << 4;
+  const uint32_t b_bc = (uint32_t)((lane & 7) ^ ((lane >> 4) & 1)) << 4;
+  auto cursor_to = [&](const Unit& w) {
+    c_kb0 = w.kb0;
+    c_nkb = w.nkb;
+    cs = 0;
+    const int ln = opaque(lane);
+    a_row = (uint32_t)(w.m0 + wave * T::RA * 8 + (ln >> 3)) * Kh;
+    b_row = (uint32_t)(w.n0 + wave * T::RB * 8 + (ln >> 3)) * Kh;
+    // scale words: position q of a K block's words holds the row that puts the words
+    // of a lane's MT row blocks (NT column blocks) side by side
+    {
+      const int q = (wave % T::NSA % (T::BM / 64)) * 64 + ln;
+      const int i = q % (MT * 16), row = w.m0 + q - i + (i % MT) * 16 + i / MT;
+      sa_off = row < M ? (uint32_t)row * 4u : kBufferOutOfRange;
+    }
+    {
+      const int q = (wave % T::NSB % (T::BN / 64)) * 64 + ln;
+      const int i = q % (NT * 16), nt = i % NT, r = i / NT;
+      const int row = w.n0 + q - i + (nt >> 1) * 32 + (r >> 2) * 8 + (nt & 1) * 4 + (r & 3);
+      sb_off = row < N ? (uint32_t)row * 4u : kBufferOutOfRange;
+    }
+  };
+  // copy idx of the cursor's stage
+  auto issue = [&](auto idx_tag) {
+    constexpr int idx = decltype(idx_tag)::value;
+    const int kb = c_kb0 + 2 * cs;
+    const uint32_t kofs = (uint32_t)kb * 64u;
+    const bool odd_end = 2 * cs + 1 >= c_nkb;   // the stage's second K block is past the end
+    const uint32_t hi = odd_end ? 64u : 0u;     // chunks 4-7 are it
+    if constexpr (idx < T::RA) {
+      const uint32_t t = a_bc ^ (uint32_t)(((wave * T::RA + idx) & 1) << 4);
+      buf16_to_lds(rsA, (a_row + (uint32_t)(idx * 8) * Kh + t) | (t & hi) << 25, kofs,
+                   smem + slot_w + (wave * T::RA + idx) * 1024);
+    } else if constexpr (idx < T::RA + T::RB) {
+      constexpr int j = idx - T::RA;
+      const uint32_t t = b_bc ^ (uint32_t)(((wave * T::RB + j) & 3) << 5);
+      buf16_to_lds(rsB, (b_row + (uint32_t)(j * 8) * Kh + t) | (t & hi) << 25, kofs,
+                   smem + slot_w + T::OFF_B + (wave * T::RB + j) * 1024);
+    } else if constexpr (idx == T::RA + T::RB) {
+      const int i = wave % T::NSA, half = i / (T::BM / 64);
+      const bool none = half && odd_end;
+      buf4_to_lds(rsSA, none ? kBufferOutOfRange : sa_off, none ? 0u : (uint32_t)(kb + half) * (uint32_t)M * 4u,
+                  smem + slot_w + T::OFF_SA + i * 256);
+    } else {
+      const int i = wave % T::NSB, half = i / (T::BN / 64);
+      const bool none = half && odd_end;
+      buf4_to_lds(rsSB, none ? kBufferOutOfRange : sb_off, none ? 0u : (uint32_t)(kb + half) * (uint32_t)N * 4u,
+                  smem + slot_w + T::OFF_SB + i * 256);
+    }
+  };
+  // to the next stage, of the next unit if this one has no more (past the last unit
+  // the last unit is copied again; nothing reads it)
+  auto advance = [&]() {
+    slot_w = slot_w + T::STAGE == T::LDS ? 0u : slot_w + T::STAGE;
+    ++cs;
+    if (2 * cs >= c_nkb) {
+      if (cu + G < p.units) cu += G;
+      cursor_to(decode(cu));
+    }
+  };
+
+  // fragment addresses within a slot; K block 1 of a stage is chunks 4-7
+  const uint32_t a_rd = (uint32_t)(wave_m * MT * 16 + lrow) * 128u + (uint32_t)((lgrp ^ swz(lrow)) << 4);
+  const int brow = (lrow >> 2) * 8 + (lrow & 3);   // (+ 4 in odd column blocks, + 32 per pair: the same swizzle)
+  const uint32_t b_rd =
+      T::OFF_B + (uint32_t)(wave_n * NT * 16 + brow) * 128u + (uint32_t)((lgrp ^ swz_b(brow)) << 4);
+  const uint32_t sa_rd = T::OFF_SA + (uint32_t)(wave_m * MT * 16 + lrow * MT) * 4u;
+  const uint32_t sb_rd = T::OFF_SB + (uint32_t)(wave_n * NT * 16 + lrow * NT) * 4u;
+  const int sh = 8 * lgrp;
+
+  v4i af[2][MT], bf[NT];
+  uint32_t sa[2][MT], sb[NT];   // scale words; the byte is taken at use
+  // Reads of K block H of the slot at byte offset rd, in two sets of parts.
+  auto read_a = [&](uint32_t rd, auto half_tag, auto mt_tag) {
+    constexpr int H = decltype(half_tag)::value, mt = decltype(mt_tag)::value;
+    af[H][mt] = *reinterpret_cast<const v4i*>(smem + rd + (a_rd ^ (H * 64u)) + mt * 2048);
+  };
+  auto read_sa = [&](uint32_t rd, auto half_tag) {
+    constexpr int H = decltype(half_tag)::value;
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int mt = 0; mt < MT; ++mt)
+      sa[H][mt] = *reinterpret_cast<const uint32_t*>(smem + rd + sa_rd + H * (T::BM * 4) + mt * 4);
+  };
+  // what column block nt's registers take over after their last use: its fragment,
+  // and after the last of a half of the column blocks that half's scale words
+  auto read_b = [&](uint32_t rd, auto half_tag, auto nt_tag) {
+    constexpr int H = decltype(half_tag)::value, nt = decltype(nt_tag)::value, NH = NT / 2;
+    bf[nt] = *reinterpret_cast<const v4i*>(smem + rd + (b_rd ^ (H * 64u)) + (nt >> 1) * 4096 + (nt & 1) * 512);
+    if constexpr (nt % NH == NH - 1) {
 #pragma unroll
-      for (int j = 0; j < T; ++j) acc[i][j] = mfma_mxfp4(bf[j], sb[j], af[i], sa[i], acc[i][j]);
+      for (int e = nt - NH + 1; e <= nt; ++e)
+        sb[e] = *reinterpret_cast<const uint32_t*>(smem + rd + sb_rd + H * (T::BN * 4) + e * 4);
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+
+  // prologue: R stages in flight, the first one's fragments
+  cursor_to(decode(cu));
+  static_for<R>([&](auto r) {
+    static_for<T::LPS>([&](auto i) { issue(i); });
+    if constexpr (decltype(r)::value + 1 < R) advance();
+  });
+  wait_vmcnt<0>();
+  block_barrier();
+  uint32_t rd = 0;
+  read_sa(0u, I0{});
+  static_for<MT>([&](auto mt) { read_a(0u, I0{}, mt); });
+  static_for<NT>([&](auto nt) { read_b(0u, I0{}, nt); });
+
+  v4f acc[MT][NT];
+  // One stage.  FIRST: the first of a unit, whose predecessor's stores were issued after
+  // the copies of the stage waited for (the first unit of all waited in the prologue).
+  auto stage = [&](auto first_tag) {
+    constexpr bool FIRST = decltype(first_tag)::value;
+    advance();   // (ahead of the matrix instructions: its branch must not split them)
+    const uint32_t nx = rd + T::STAGE == T::LDS ? 0u : rd + T::STAGE;
+    // first K block: read the second one's fragments
+    static_for<NT>([&](auto nt_tag) {
+      constexpr int nt = decltype(nt_tag)::value;
+      const uint32_t sbv = sb[nt] >> sh;
+      static_for<MT>([&](auto mt_tag) {
+        constexpr int mt = decltype(mt_tag)::value;
+        if constexpr (nt == 0) sa[0][mt] >>= sh;
+        acc[mt][nt] = mfma_mxfp4(bf[nt], sbv, af[0][mt], sa[0][mt], acc[mt][nt]);
+      });
+      read_b(rd, I1{}, nt_tag);
+      if constexpr (nt == 0) read_sa(rd, I1{});
+      if constexpr (nt < MT) read_a(rd, I1{}, nt_tag);
+      if constexpr (nt == NT - 1 && MT > NT)
+        static_for<(MT > NT ? MT - NT : 0)>([&](auto e) { read_a(rd, I1{}, std::integral_constant<int, NT + decltype(e)::value>{}); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // second K block: after BAR column blocks the barrier, then the next stage's
+    // fragments and the copies into this slot
+    static_for<NT>([&](auto nt_tag) {
+      constexpr int nt = decltype(nt_tag)::value;
+      const uint32_t sbv = sb[nt] >> sh;
+      static_for<MT>([&](auto mt_tag) {
+        constexpr int mt = decltype(mt_tag)::value;
+        if constexpr (nt == 0) sa[1][mt] >>= sh;
+        acc[mt][nt] = mfma_mxfp4(bf[nt], sbv, af[1][mt], sa[1][mt], acc[mt][nt]);
+      });
+      if constexpr (nt == T::BAR - 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_lgkmcnt0();
+        wait_vmcnt<(R - 2) * T::LPS + (FIRST ? T::NSTORE : 0)>();
+        block_barrier();
+        read_sa(nx, I0{});
+        static_for<T::BAR>([&](auto e) {
+          read_b(nx, I0{}, e);
+          if constexpr (decltype(e)::value < MT) read_a(nx, I0{}, e);
+        });
+      } else if constexpr (nt >= T::BAR) {
+        read_b(nx, I0{}, nt_tag);
+        if constexpr (nt < MT) read_a(nx, I0{}, nt_tag);
+      }
+      if constexpr (nt == NT - 1 && MT > NT)
+        static_for<(MT > NT ? MT - NT : 0)>([&](auto e) { read_a(nx, I0{}, std::integral_constant<int, NT + decltype(e)::value>{}); });
+      if constexpr (nt >= T::BAR - 1) {
+        // the copies, spread over the column blocks from the barrier on
+        constexpr int parts = NT - T::BAR + 1, q = nt - (T::BAR - 1);
+        constexpr int lo = T::LPS * q / parts, hi = T::LPS * (q + 1) / parts;
+        static_for<hi - lo>([&](auto e) { issue(std::integral_constant<int, lo + decltype(e)::value>{}); });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    rd = nx;
+  };
+
+  for (int u = vb; u < p.units; u += G) {
+    const Unit cur = decode(u);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    const int S = (cur.nkb + 1) >> 1;
+    stage(std::true_type{});
+#pragma clang loop unroll(disable)
+    for (int s = 1; s < S; ++s) stage(std::false_type{});
+
+    if (cur.part >= 0) {
+      // fp32 partial tile of this slice: ws[part][BM][BN]
+      const v4i rsW = make_buffer_rsrc(p.ws + (size_t)cur.part * (T::BM * T::BN), (uint32_t)(T::BM * T::BN * 4));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = wave_m * MT * 16 + mt * 16 + lrow;
+          const int col = wave_n * NT * 16 + (nt >> 1) * 32 + lgrp * 8 + (nt & 1) * 4;
+          const v4i w = {__float_as_int(acc[mt][nt][0]), __float_as_int(acc[mt][nt][1]),
+                         __float_as_int(acc[mt][nt][2]), __float_as_int(acc[mt][nt][3])};
+          dg_raw_buffer_store_v4i32(w, rsW, (int)((uint32_t)(row * T::BN + col) * 4u), 0, 0);
+        }
+    } else {
+      const v4i rsD = make_buffer_rsrc(p.d, (uint32_t)M * (uint32_t)N * 2u);
+      const v4i rsC = make_buffer_rsrc(p.c, p.c ? (uint32_t)M * (uint32_t)N * 2u : 0u);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + lrow;
+#pragma unroll
+        for (int np = 0; np < NT / 2; ++np) {
+          const int col = cur.n0 + wave_n * NT * 16 + np * 32 + lgrp * 8;
+          const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u : kBufferOutOfRange;
+          v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
+          if (p.c) {
+            const v4i cv = dg_raw_buffer_load_v4i32(rsC, (int)off, 0, 0);
+            const uint32_t cw[4] = {(uint32_t)cv.x, (uint32_t)cv.y, (uint32_t)cv.z, (uint32_t)cv.w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              lo[2 * e] += __uint_as_float(cw[e] << 16);
+              lo[2 * e + 1] += __uint_as_float(cw[e] & 0xffff0000u);
+              hi[2 * e] += __uint_as_float(cw[2 + e] << 16);
+              hi[2 * e + 1] += __uint_as_float(cw[2 + e] & 0xffff0000u);
+            }
+          }
+          const v4i w = {(int)pack_bf16x2_rne(lo[0], lo[1]), (int)pack_bf16x2_rne(lo[2], lo[3]),
+                         (int)pack_bf16x2_rne(hi[0], hi[1]), (int)pack_bf16x2_rne(hi[2], hi[3])};
+          dg_raw_buffer_store_v4i32(w, rsD, (int)off, 0, 0);
+        }
+      }
+    }
+  }
+  wait_vmcnt<0>();   // the copies past the last stage: LDS is not given back before they have landed
+}
+
+// id, MT, NT, WM, WN, ring slots
+#define DG_MXFP4_TILES(X) \
+  X(0, 4, 8, 4, 2, 2)     \
+  X(1, 4, 4, 2, 4, 3)     \
+  X(2, 2, 4, 4, 2, 4)     \
+  X(3, 2, 2, 2, 4, 6)
+
+struct Mxfp4TileInfo {
+  int bm, bn, lds, threads;
+};
+static const Mxfp4TileInfo kMxTiles[] = {
+#define X(id, MT, NT, WM, WN, R) \
+  {MxTile<MT, NT, WM, WN, R>::BM, MxTile<MT, NT, WM, WN, R>::BN, MxTile<MT, NT, WM, WN, R>::LDS, MxTile<MT, NT, WM, WN, R>::THREADS},
+    DG_MXFP4_TILES(X)
+#undef X
+};
+
+static hipError_t launch_mxfp4_tile(const Mxfp4Params& p, int id, int grid, hipStream_t stream) {
+  switch (id) {
+#define X(i, MT, NT, WM, WN, R)                                                                          \
+  case i: {                                                                                              \
+    using T = MxTile<MT, NT, WM, WN, R>;                                                                 \
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T>), \
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);  \
+    if (attr != hipSuccess) return attr;                                                                 \
+    hipLaunchKernelGGL(mxfp4_tile_kernel<T>, dim3(grid), dim3(T::THREADS), T::LDS, stream, p);           \
+    return hipGetLastError();                                                                            \
+  }
+    DG_MXFP4_TILES(X)
+#undef X
+  }
+  return hipErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (decode): the product streams B once, bound by how much of it is in
+// flight, and by the launch.  A workgroup takes 16 NT columns and all rows of A (MT
+// blocks of 16); its waves split K between them, pair of K blocks by pair (a 128-byte
+// line of each row), with fragments and scale words loaded straight into registers, P
+// pairs ahead.  The waves' sums meet in LDS, added in wave order, so no second launch
+// and no workspace is needed.
+// ---------------------------------------------------------------------------
+extern "C" __device__ int dg_raw_buffer_load_i32_mx(v4i rsrc, int voffset, int soffset,
+                                                    int aux) __asm("llvm.amdgcn.raw.buffer.load.i32");
+
+template <int MT, int NT, int NW, int P>
+__global__ void __launch_bounds__(NW * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
+  __shared__ v4f red[NW][NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4, sh = 8 * lgrp;
+  const int M = p.m, N = p.n;
+  const uint32_t Kh = (uint32_t)p.k >> 1;
+  const int KB = p.k >> 7, PAIRS = (KB + 1) >> 1;
+  const int n0 = blockIdx.x * (16 * NT);
+  const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
+  const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
+  const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
+  const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
+  // per-lane offsets; a row past the end reads zeros (and its results are not stored)
+  uint32_t a_off[MT], b_off[NT], sa_off[MT], sb_off[NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = i * 16 + lrow;
+    a_off[i] = r < M ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
+    sa_off[i] = r < M ? (uint32_t)r * 4u : kBufferOutOfRange;
   }
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const int row = m0 + i * 16 + lrow;
+  for (int i = 0; i < NT; ++i) {
+    const int r = n0 + i * 16 + lrow;
+    b_off[i] = r < N ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
+    sb_off[i] = r < N ? (uint32_t)r * 4u : kBufferOutOfRange;
+  }
+  v4i af[P][2][MT], bf[P][2][NT];
+  uint32_t sa[P][2][MT], sb[P][2][NT];
+  // pair j of this wave (pair j NW + wave of K); K blocks past the end read zeros
+  auto load = [&](int j, auto set_tag) {
+    constexpr int S = decltype(set_tag)::value;
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int col = n0 + j * 16 + 4 * lgrp;
-      if (row >= p.m || col >= p.n) continue;
-      const size_t at = (size_t)row * p.n + col;
-      v4f v = acc[i][j];
-      if (p.c) {
+    for (int h = 0; h < 2; ++h) {
+      const int kb = (j * NW + wave) * 2 + h;
+      const bool in = kb < KB;
+      const int ko = in ? kb * 64 : 0;
+      const uint32_t none = in ? 0u : kBufferOutOfRange;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.c[at + e]);
+      for (int i = 0; i < NT; ++i) {
+        bf[S][h][i] = dg_raw_buffer_load_v4i32(rsB, (int)(b_off[i] | none), ko, 0);
+        sb[S][h][i] = (uint32_t)dg_raw_buffer_load_i32_mx(rsSB, (int)(sb_off[i] | none), in ? kb * N * 4 : 0, 0);
       }
-      *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        af[S][h][i] = dg_raw_buffer_load_v4i32(rsA, (int)(a_off[i] | none), ko, 0);
+        sa[S][h][i] = (uint32_t)dg_raw_buffer_load_i32_mx(rsSA, (int)(sa_off[i] | none), in ? kb * M * 4 : 0, 0);
+      }
+    }
+  };
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int mine = (PAIRS - wave + NW - 1) / NW;   // (0 for a wave past the last pair)
+  static_for<P>([&](auto s) { load(decltype(s)::value, s); });
+  for (int j = 0; j < mine; j += P) {
+    static_for<P>([&](auto s) {
+      constexpr int S = decltype(s)::value;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            acc[mt][nt] = mfma_mxfp4(bf[S][h][nt], sb[S][h][nt] >> sh, af[S][h][mt], sa[S][h][mt] >> sh, acc[mt][nt]);
+      load(j + P + S, s);
+    });
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    if (mt > 0) __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) red[wave][nt][lane] = acc[mt][nt];
+    __syncthreads();
+    for (int e = threadIdx.x; e < NT * 64; e += NW * 64) {
+      v4f v = red[0][e >> 6][e & 63];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) v += red[w][e >> 6][e & 63];
+      const int row = mt * 16 + (e & 15), col = n0 + (e >> 6) * 16 + 4 * ((e & 63) >> 4);
+      if (row < M && col < N) {
+        const size_t at = (size_t)row * N + col;
+        if (p.c) {
+          const uint2 cv = *reinterpret_cast<const uint2*>(p.c + at);
+          v[0] += __uint_as_float(cv.x << 16);
+          v[1] += __uint_as_float(cv.x & 0xffff0000u);
+          v[2] += __uint_as_float(cv.y << 16);
+          v[3] += __uint_as_float(cv.y & 0xffff0000u);
+        }
+        *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
+      }
     }
   }
 }
+
+// id, MT, NT, waves, pairs in flight per wave
+#define DG_MXFP4_SKINNY(X) \
+  X(0, 1, 1, 8, 4)         \
+  X(1, 2, 1, 8, 4)         \
+  X(2, 4, 1, 8, 2)         \
+  X(3, 8, 1, 8, 1)         \
+  X(4, 1, 2, 8, 4)         \
+  X(5, 2, 2, 8, 2)         \
+  X(6, 4, 2, 8, 2)         \
+  X(7, 8, 2, 8, 1)         \
+  X(8, 1, 1, 16, 2)        \
+  X(9, 4, 1, 16, 1)        \
+  X(10, 1, 1, 4, 4)        \
+  X(11, 4, 1, 4, 2)        \
+  X(12, 4, 2, 4, 2)
+
+static int skinny_rows(int id) {
+  switch (id) {
+#define X(i, MT, NT, NW, P) case i: return MT * 16;
+    DG_MXFP4_SKINNY(X)
+#undef X
+  }
+  return 0;
+}
+
+static hipError_t launch_mxfp4_skinny(const Mxfp4Params& p, int id, hipStream_t stream) {
+  switch (id) {
+#define X(i, MT, NT, NW, P)                                                                                  \
+  case i:                                                                                                    \
+    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, NT, NW, P>), dim3((p.n + 16 * NT - 1) / (16 * NT)), dim3(NW * 64), 0, \
+                       stream, p);                                                                           \
+    return hipGetLastError();
+    DG_MXFP4_SKINNY(X)
+#undef X
+  }
+  return hipErrorInvalidValue;
+}
+
+struct Mxfp4Plan {
+  int skinny, tile, tiles_m, tiles_n, splits, kb_per_split, full_tiles, units, grid;
+  size_t ws_bytes;
+};
+
+static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
+  Mxfp4Plan pl{};
+  const Mxfp4TileInfo t = kMxTiles[id];
+  pl.skinny = -1;
+  pl.tile = id;
+  pl.tiles_m = (m + t.bm - 1) / t.bm;
+  pl.tiles_n = (n + t.bn - 1) / t.bn;
+  const long long tiles = (long long)pl.tiles_m * pl.tiles_n;
+  const int kb = k / 128;
+  long long full = tiles;
+  pl.splits = split_rule(tiles, cus, kb, &full);
+  pl.kb_per_split = kb;
+  if (pl.splits > 1) {
+    pl.kb_per_split = ((kb + pl.splits - 1) / pl.splits + 1) & ~1;   // whole stages
+    pl.splits = (kb + pl.kb_per_split - 1) / pl.kb_per_split;
+    if (pl.splits < 2) {
+      pl.splits = 1;
+      pl.kb_per_split = kb;
+      full = tiles;
+    }
+  }
+  pl.full_tiles = (int)full;
+  pl.units = (int)(full + (tiles - full) * pl.splits);
+  pl.ws_bytes = (size_t)(tiles - full) * (pl.splits > 1 ? pl.splits : 0) * t.bm * t.bn * 4;
+  pl.grid = std::min(pl.units, cus);
+  return pl;
+}
+
+// The tile with the least estimated time: rounds of units, each its stages at the
+// tile's measured pace (microseconds per 256 values of K, all CUs busy: 4096 rows,
+// K = 7168 and 16384) and a fixed share per unit (pipeline fill, D), and for a split
+// the partials' round trip and a second launch.
+static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
+  constexpr double kStage[] = {1.90, 1.30, 0.78, 0.52}, kUnit[] = {3.5, 1.6, 0.8, 0.6};
+  constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
+  int force = -1;
+  if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
+  Mxfp4Plan best{};
+  double best_t = 1e30;
+  for (int id = 0; id < kTiles; ++id) {
+    if (force >= 0 && force < kTiles && id != force) continue;
+    const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
+    const int stages = (pl.kb_per_split + 1) / 2, whole = (k / 128 + 1) / 2;
+    double t;
+    if (pl.splits > 1) {
+      t = (double)(pl.full_tiles / cus) * (whole * kStage[id] + kUnit[id]) + stages * kStage[id] + kUnit[id] + 4.0 +
+          2.0 * (double)pl.ws_bytes / 4.0e6;
+    } else {
+      t = (double)((pl.units + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
+    }
+    if (t < best_t - 1e-9) {
+      best_t = t;
+      best = pl;
+    }
+  }
+  // Few rows: where the tiles would be split along K, the streaming kernel needs no
+  // second launch.
+  int sk = -1;
+  if (best.splits > 1 && best.full_tiles == 0) sk = m <= 16 ? 10 : m <= 32 ? 1 : m <= 64 && k <= 8192 ? 11 : -1;
+  if (force >= 0) sk = force >= 100 && skinny_rows(force - 100) >= m ? force - 100 : -1;
+  if (sk >= 0) {
+    best.skinny = sk;
+    best.ws_bytes = 0;
+  }
+  return best;
+}
+
+static bool mxfp4_sizes_fit(int m, int n, int k) {
+  const long long lim = 1LL << 31;
+  return k % 128 == 0 && n % 16 == 0 && (long long)m * (k / 2) <= lim && (long long)n * (k / 2) <= lim &&
+         (long long)m * n * 2 <= lim && (long long)m * (k / 32) <= lim && (long long)n * (k / 32) <= lim;
+}
+
+static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
 }  // namespace dg
 
 using namespace dg;
 
-static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
-
 extern "C" {
 
 size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus) {
-  (void)m; (void)n; (void)k; (void)num_cus;
-  return 0;
+  try {
+    if (m <= 0 || n <= 0 || k <= 0 || !mxfp4_sizes_fit(m, n, k)) return 0;
+    if (num_cus <= 0) num_cus = dg_get_num_cus();
+    if (num_cus <= 0) return 0;
+    return plan_mxfp4(m, n, k, num_cus).ws_bytes;
+  } catch (...) {
+    return 0;
+  }
 }
 
 int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
                      const uint16_t* c, uint16_t* d, int m, int n, int k, void* workspace, size_t workspace_bytes,
                      void* stream) {
   try {
-    (void)workspace; (void)workspace_bytes;
     if (!a || !a_sf || !b || !b_sf || !d) return DG_ERR_INVALID_ARG;
     if (m <= 0 || n <= 0 || k <= 0) return DG_ERR_INVALID_ARG;
     if (misaligned(a, 16) || misaligned(b, 16) || misaligned(c, 16) || misaligned(d, 16) || misaligned(a_sf, 4) ||
         misaligned(b_sf, 4))
       return DG_ERR_INVALID_ARG;
-    const long long lim = 1LL << 31;
-    if (k % 128 != 0 || n % 16 != 0 || (long long)m * (k / 2) > lim || (long long)n * (k / 2) > lim ||
-        (long long)m * n * 2 > lim || (long long)m * (k / 32) > lim || (long long)n * (k / 32) > lim)
-      return DG_ERR_UNSUPPORTED;
-    if ((m + 63) / 64 > 65535) return DG_ERR_UNSUPPORTED;
+    if (!mxfp4_sizes_fit(m, n, k)) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    Mxfp4Params p{a, a_sf, b, b_sf, c, d, m, n, k};
-    hipLaunchKernelGGL(mxfp4_gemm_kernel, dim3((n + 63) / 64, (m + 63) / 64), dim3(64), 0,
-                       reinterpret_cast<hipStream_t>(stream), p);
-    return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
+    int cus = dg_get_num_cus();
+    if (cus <= 0) cus = di.num_cus;
+    const Mxfp4Plan pl = plan_mxfp4(m, n, k, cus);
+    if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes || misaligned(workspace, 16)))
+      return DG_ERR_INVALID_ARG;
+    Mxfp4Params p{a, a_sf, b, b_sf, c, d, static_cast<float*>(workspace), m, n, k,
+                  pl.tiles_m, pl.tiles_n, 8, pl.splits, pl.kb_per_split, pl.full_tiles, pl.units};
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = pl.skinny >= 0 ? launch_mxfp4_skinny(p, pl.skinny, hs) : launch_mxfp4_tile(p, pl.tile, pl.grid, hs);
+    if (e == hipSuccess && pl.ws_bytes) {
+      const Mxfp4TileInfo t = kMxTiles[pl.tile];
+      Fp8GemmParams rp{};
+      rp.ws = p.ws; rp.c = c; rp.d = d; rp.m = m; rp.n = n; rp.k = k; rp.num_groups = 1;
+      rp.tiles_m = pl.tiles_m; rp.tiles_n = pl.tiles_n; rp.group_m = p.group_m;
+      GemmPlan rpl{};
+      rpl.block_m = t.bm; rpl.block_n = t.bn; rpl.num_tiles = pl.tiles_m * pl.tiles_n;
+      rpl.full_tiles = pl.full_tiles; rpl.splits = pl.splits;
+      e = launch_splitk_reduce(rp, rpl, cus, hs);
+    }
+    return e == hipSuccess ? DG_OK : DG_ERR_HIP;
   } catch (...) {
     return DG_ERR_HIP;
   }
