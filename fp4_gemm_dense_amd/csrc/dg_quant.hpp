@@ -42,11 +42,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float scale) {
   return w;
 }
 __device__ __forceinline__ uint32_t e2m1x8(const v4i& v, float scale) {   // eight bf16
+  // (named copies: a bit cast of a vector's element reads the vector's first one)
+  const int a = v.x, b = v.y, c = v.z, d = v.w;
   uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, v.x), scale, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, v.y), scale, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, v.z), scale, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, v.w), scale, 3);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, a), scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, b), scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, c), scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(qbf2, d), scale, 3);
   return w;
 }
 
@@ -65,6 +67,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
+
+// Two bf16 side by side: their magnitudes, and the larger ones of two pairs (as integers
+// the patterns order like the magnitudes).
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ us2 us2abs(int w) { return __builtin_bit_cast(us2, w & 0x7fff7fff); }
+__device__ __forceinline__ us2 us2max(us2 a, us2 b) { return __builtin_elementwise_max(a, b); }
 
 // Largest of v over the lane's aligned group of 4 / 16 lanes; every lane gets it.
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }

@@ -26,51 +26,106 @@ struct QuantParams {
   int groups, m, k;
 };
 
-// Eight consecutive values of x from element i, and the largest magnitude's bits.
-struct Vec8 {
-  float v[8];
-  uint32_t amax;
+// Eight consecutive values of a row as they are in memory.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  v4i p;
+  __device__ __forceinline__ void zero() { p = v4i{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const uint16_t* x) { p = *reinterpret_cast<const v4i*>(x); }
+  __device__ __forceinline__ void to_lds(uint16_t* l) const { *reinterpret_cast<v4i*>(l) = p; }
+  // bit pattern of the largest magnitude, as fp32
+  __device__ __forceinline__ uint32_t amax() const {
+    const us2 a = us2max(us2max(us2abs(p.x), us2abs(p.y)), us2max(us2abs(p.z), us2abs(p.w)));
+    return umax(a.x, a.y) << 16;
+  }
+  __device__ __forceinline__ uint32_t codes(float scale) const { return e2m1x8(p, scale); }
+};
+template <>
+struct Vec8<float> {
+  v4f a, b;
+  __device__ __forceinline__ void zero() { a = b = v4f{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void load(const float* x) {
+    a = *reinterpret_cast<const v4f*>(x);
+    b = *reinterpret_cast<const v4f*>(x + 4);
+  }
+  __device__ __forceinline__ void to_lds(float* l) const {
+    *reinterpret_cast<v4f*>(l) = a;
+    *reinterpret_cast<v4f*>(l + 4) = b;
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = umax(m, umax(abs_bits(a[j]), abs_bits(b[j])));
+    return m;
+  }
+  __device__ __forceinline__ uint32_t codes(float scale) const {
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return e2m1x8(v, scale);
+  }
+};
+
+// The row direction of one vector: its 4-lane block's codes, and the scale word of its
+// 16-lane K block (all lanes of the 16 take part).
+struct RowCodes {
+  uint32_t w, word;
+  float scale;
 };
 template <typename T>
-__device__ __forceinline__ void load8(const T* x, size_t i, Vec8& o) {
-  if constexpr (sizeof(T) == 2) {
-    unpack_bf16x8(*reinterpret_cast<const v4i*>(x + i), o.v);
-  } else {
-    const v4f a = *reinterpret_cast<const v4f*>(x + i), b = *reinterpret_cast<const v4f*>(x + i + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o.v[j] = a[j];
-      o.v[4 + j] = b[j];
-    }
-  }
-  o.amax = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o.amax = umax(o.amax, abs_bits(o.v[j]));
+__device__ __forceinline__ RowCodes quantize_row8(const Vec8<T>& v) {
+  const uint32_t byte = ue8m0_byte<false>(group_max<4>(v.amax()));
+  RowCodes r;
+  r.scale = ue8m0_value(byte);
+  r.w = byte == 255u ? 0u : v.codes(r.scale);
+  r.word = scale_word(byte);
+  return r;
 }
 
-// Blocks along k: a lane holds 8 values, 4 lanes a block, 16 lanes a 128-wide K block.
+// Blocks along k.  A workgroup takes 16 rows x 512 columns: a wave reads 512 values of
+// each of its four rows (all four loads in flight), 16 lanes a K block, and the 16
+// rows' scale words leave through LDS as 64-byte runs (K-block-major).
+constexpr int QR_ROWS = 16, QR_COLS = 512;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantParams p) {
+  __shared__ uint32_t words[QR_COLS / 128][QR_ROWS];
   const T* x = static_cast<const T*>(p.x);
-  const size_t total = (size_t)p.groups * p.m * (p.k / 8);   // a multiple of 16
-  const uint32_t per_row = (uint32_t)p.k / 8;
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
-    Vec8 t;
-    load8(x, i * 8, t);
-    const uint32_t byte = ue8m0_byte<false>(group_max<4>(t.amax));
-    const float scale = ue8m0_value(byte);
-    const uint32_t w = byte == 255u ? 0u : e2m1x8(t.v, scale);
-    if (p.q) {
-      reinterpret_cast<uint32_t*>(p.q)[i] = w;
-      const uint32_t word = scale_word(byte);
-      if ((threadIdx.x & 15) == 0) {
-        const size_t row = i / per_row;
-        const uint32_t kb = (uint32_t)(i - row * per_row) >> 4;
-        const size_t g = row / p.m, r = row - g * p.m;
-        p.sf[(g * (p.k / 128) + kb) * p.m + r] = (int32_t)word;
-      }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int kb_n = p.k >> 7;
+  const uint32_t cb = (uint32_t)(p.k + QR_COLS - 1) / QR_COLS, rb = (uint32_t)(p.m + QR_ROWS - 1) / QR_ROWS;
+  const long long total = (long long)cb * rb * p.groups;
+  for (long long t = blockIdx.x; t < total; t += gridDim.x) {
+    const uint32_t row_block = (uint32_t)(t / cb), c0 = (uint32_t)(t - (long long)row_block * cb) * QR_COLS;
+    const uint32_t g = row_block / rb, r0 = (row_block - g * rb) * QR_ROWS;
+    const uint32_t col = c0 + lane * 8;
+    const bool in = col < (uint32_t)p.k;
+    Vec8<T> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t r = r0 + i * 4 + wave;
+      if (in && r < (uint32_t)p.m) v[i].load(x + ((size_t)g * p.m + r) * p.k + col);
+      else v[i].zero();
     }
-    if (p.values) reinterpret_cast<v4i*>(p.values)[i] = e2m1x8_to_bf16(w, scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t r = r0 + i * 4 + wave;
+      const RowCodes o = quantize_row8(v[i]);
+      if (in && r < (uint32_t)p.m) {
+        const size_t at = (((size_t)g * p.m + r) * p.k + col) >> 3;
+        if (p.q) reinterpret_cast<uint32_t*>(p.q)[at] = o.w;
+        if (p.values) reinterpret_cast<v4i*>(p.values)[at] = e2m1x8_to_bf16(o.w, o.scale);
+      }
+      if ((lane & 15) == 0) words[lane >> 4][i * 4 + wave] = o.word;
+    }
+    if (p.sf) {   // (uniform)
+      __syncthreads();
+      if (tid < 64) {
+        const uint32_t kb = (c0 >> 7) + (tid >> 4), r = r0 + (tid & 15);
+        if (kb < (uint32_t)kb_n && r < (uint32_t)p.m)
+          p.sf[((size_t)g * kb_n + kb) * p.m + r] = (int32_t)words[tid >> 4][tid & 15];
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -79,74 +134,99 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantParams p) {
 // from there: a thread holds two columns of one block of 32 rows.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_tiles_kernel(QuantParams p) {
-  __shared__ T tile[128][128];
-  __shared__ uint32_t bytes[128];
+  __shared__ __attribute__((aligned(16))) T tile[128][128];
+  __shared__ uint32_t words[128];
+  __shared__ __attribute__((aligned(4))) uint8_t bytes[128][4];
   const T* x = static_cast<const T*>(p.x);
   const int tid = threadIdx.x;
-  const int kb_n = p.k / 128, mb_n = (p.m + 127) / 128;
+  const uint32_t kb_n = (uint32_t)p.k >> 7, mb_n = (uint32_t)(p.m + 127) >> 7;
   const size_t mp = (size_t)mb_n * 128;
   const long long total = (long long)p.groups * mb_n * kb_n;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-    const int kb = (int)(t % kb_n);
-    const long long gm = t / kb_n;
-    const int mb = (int)(gm % mb_n);
-    const size_t g = (size_t)(gm / mb_n);
-    if (tid < 128) bytes[tid] = 0;
-    for (int s = 0; s < 8; ++s) {
-      const int r = s * 16 + (tid >> 4), c = (tid & 15) * 8;
-      const int row = mb * 128 + r;
-      Vec8 v;
+    const uint32_t gm = (uint32_t)(t / kb_n), kb = (uint32_t)(t - (long long)gm * kb_n);
+    const uint32_t g = gm / mb_n, mb = gm - g * mb_n;
+    const int rr = tid >> 4, c = (tid & 15) * 8;
+    const T* src = x + ((size_t)g * p.m + mb * 128u) * p.k + kb * 128u + c;
+    const int rows = min(128, p.m - (int)(mb * 128u));
+    Vec8<T> v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v.v[j] = 0.f;
-      v.amax = 0;
-      const size_t at = (g * p.m + row) * (size_t)p.k + (size_t)kb * 128 + c;
-      const bool in = row < p.m;
-      if (in) load8(x, at, v);
-      T* dst = &tile[r][c];
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<v4i*>(dst) = in ? *reinterpret_cast<const v4i*>(x + at) : v4i{0, 0, 0, 0};
-      } else {
-        *reinterpret_cast<v4f*>(dst) = v4f{v.v[0], v.v[1], v.v[2], v.v[3]};
-        *reinterpret_cast<v4f*>(dst + 4) = v4f{v.v[4], v.v[5], v.v[6], v.v[7]};
+    for (int s = 0; s < 8; ++s) {
+      const int r = s * 16 + rr;
+      if (r < rows) v[s].load(src + (size_t)r * p.k);
+      else v[s].zero();
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int r = s * 16 + rr;
+      v[s].to_lds(&tile[r][c]);
+      if (p.q || p.values) {   // (uniform)
+        const RowCodes o = quantize_row8(v[s]);
+        if (r < rows) {
+          const size_t at = (((size_t)g * p.m + mb * 128u + r) * p.k + kb * 128u + c) >> 3;
+          if (p.q) reinterpret_cast<uint32_t*>(p.q)[at] = o.w;
+          if (p.values) reinterpret_cast<v4i*>(p.values)[at] = e2m1x8_to_bf16(o.w, o.scale);
+        }
+        if ((tid & 15) == 0) words[r] = o.word;
       }
-      const uint32_t byte = ue8m0_byte<false>(group_max<4>(v.amax));
-      const float scale = ue8m0_value(byte);
-      const uint32_t w = byte == 255u ? 0u : e2m1x8(v.v, scale);
-      const uint32_t word = scale_word(byte);
-      if (in && p.q) {
-        reinterpret_cast<uint32_t*>(p.q)[at / 8] = w;
-        if ((tid & 15) == 0) p.sf[(g * kb_n + kb) * p.m + row] = (int32_t)word;
-      }
-      if (in && p.values) reinterpret_cast<v4i*>(p.values)[at / 8] = e2m1x8_to_bf16(w, scale);
     }
     __syncthreads();
-    const int c = (tid & 63) * 2, b = tid >> 6;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[32];
-      uint32_t amax = 0;
+    if (p.sf && tid < rows) p.sf[((size_t)g * kb_n + kb) * p.m + mb * 128u + tid] = (int32_t)words[tid];
+    const int c2 = (tid & 63) * 2, b = tid >> 6;
+    v4i w[2];
+    uint32_t byte[2];
+    if constexpr (sizeof(T) == 2) {
+      uint32_t e[32];   // rows b*32 .. of columns c2 (low half) and c2 + 1
+      us2 am = us2{0, 0};
 #pragma unroll
       for (int r = 0; r < 32; ++r) {
-        if constexpr (sizeof(T) == 2) v[r] = bf16_to_f32((uint16_t)tile[b * 32 + r][c + h]);
-        else v[r] = tile[b * 32 + r][c + h];
-        amax = umax(amax, abs_bits(v[r]));
+        e[r] = *reinterpret_cast<const uint32_t*>(&tile[b * 32 + r][c2]);
+        am = us2max(am, us2abs((int)e[r]));
       }
-      const uint32_t byte = ue8m0_byte<false>(amax);
-      const float scale = ue8m0_value(byte);
-      v4i w;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float e[8];
+      for (int h = 0; h < 2; ++h) {
+        byte[h] = ue8m0_byte<false>((uint32_t)(h ? am.y : am.x) << 16);
+        const float scale = ue8m0_value(byte[h]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = v[8 * q + j];
-        w[q] = byte == 255u ? 0 : (int)e2m1x8(e, scale);
+        for (int q = 0; q < 4; ++q) {
+          v4i pr;   // eight rows of the column
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            pr[j] = (int)__builtin_amdgcn_perm(e[8 * q + 2 * j + 1], e[8 * q + 2 * j], h ? 0x07060302u : 0x05040100u);
+          w[h][q] = byte[h] == 255u ? 0 : (int)e2m1x8(pr, scale);
+        }
       }
-      const size_t col = g * p.k + (size_t)kb * 128 + c + h;
-      *reinterpret_cast<v4i*>(p.qt + col * (mp / 2) + (size_t)mb * 64 + b * 16) = w;
-      atomicOr(&bytes[c + h], byte << (8 * b));
+    } else {
+      float e[2][32];
+      uint32_t am[2] = {0, 0};
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const float2 f = *reinterpret_cast<const float2*>(&tile[b * 32 + r][c2]);
+        e[0][r] = f.x;
+        e[1][r] = f.y;
+        am[0] = umax(am[0], abs_bits(f.x));
+        am[1] = umax(am[1], abs_bits(f.y));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        byte[h] = ue8m0_byte<false>(am[h]);
+        const float scale = ue8m0_value(byte[h]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = e[h][8 * q + j];
+          w[h][q] = byte[h] == 255u ? 0 : (int)e2m1x8(o, scale);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t col = (size_t)g * p.k + kb * 128u + c2 + h;
+      *reinterpret_cast<v4i*>(p.qt + col * (mp / 2) + (size_t)mb * 64 + b * 16) = w[h];
+      bytes[c2 + h][b] = (uint8_t)byte[h];
     }
     __syncthreads();
-    if (tid < 128) p.sft[(g * mb_n + mb) * p.k + (size_t)kb * 128 + tid] = (int32_t)bytes[tid];
+    if (tid < 128) p.sft[((size_t)g * mb_n + mb) * p.k + kb * 128u + tid] = *reinterpret_cast<const int32_t*>(bytes[tid]);
     __syncthreads();
   }
 }
@@ -181,8 +261,8 @@ extern "C" int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t*
       else
         hipLaunchKernelGGL(quantize_tiles_kernel<float>, dim3(grid), dim3(256), 0, hs, p);
     } else {
-      const long long blocks = ((long long)num_groups * m * (k / 8) + 255) / 256;
-      const int grid = (int)std::min<long long>(blocks, (long long)cus * 8);
+      const long long tiles = (long long)num_groups * ((m + QR_ROWS - 1) / QR_ROWS) * ((k + QR_COLS - 1) / QR_COLS);
+      const int grid = (int)std::min<long long>(tiles, (long long)cus * 64);
       if (x_type == DG_BF16)
         hipLaunchKernelGGL(quantize_rows_kernel<uint16_t>, dim3(grid), dim3(256), 0, hs, p);
       else
