@@ -43,8 +43,8 @@ static NormShape norm_shape(int k) {
 }
 constexpr int NORM_MAX_K = 32768, NORM_MAX_WAVES = 16;
 
-// Sum of v over the workgroup, in a fixed order; every thread gets it.  red: two
-// buffers used in turn, so that one barrier per sum is enough.
+// Sum of v over the workgroup, in a fixed order; every thread gets it.  One barrier: a
+// caller that sums again passes another buffer.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
@@ -57,112 +57,89 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
-// RC rows in a row per workgroup: with K-block-major scales the workgroup keeps their
-// scales in LDS and writes runs of RC words.
-template <int FMT, int V, int RC>
+// One row per workgroup.  (Measured against 2, 4 and 8 rows per workgroup, with the
+// next row loaded ahead and the K-block-major scales leaving in longer runs, and
+// against 2 to 8 persistent workgroups per CU: one row was the fastest at 8192 x 7168
+// in every format, 70-75 us against 73-84.)
+template <int FMT, int V>
 __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormParams p) {
-  __shared__ float red[2][NORM_MAX_WAVES];
-  __shared__ uint32_t scales[FMT != DG_QUANT_E4M3_UE8M0 && RC > 1 ? (V * 512 / 16) * RC : 1];
+  __shared__ float red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3, kb_n = p.k >> 7;
-  v4i wv[V];
+  const int row = blockIdx.x;
+  const size_t base = (size_t)row * nv;
+  v4i hv[V], rv[V], wv[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int j = i * nt + tid;
-    wv[i] = j < nv ? reinterpret_cast<const v4i*>(p.weight)[j] : v4i{0, 0, 0, 0};
-  }
-  for (int r0 = blockIdx.x * RC; r0 < p.m; r0 += gridDim.x * RC) {
-    const int rows = min(RC, p.m - r0);
-    for (int rr = 0; rr < rows; ++rr) {
-      const int row = r0 + rr;
-      const size_t base = (size_t)row * nv;
-      v4i hv[V], rv[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = i * nt + tid;
-        hv[i] = rv[i] = v4i{0, 0, 0, 0};
-        if (j < nv) {
-          hv[i] = reinterpret_cast<const v4i*>(p.x)[base + j];
-          if (p.residual) rv[i] = reinterpret_cast<const v4i*>(p.residual)[base + j];
-        }
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = i * nt + tid;
-        float a[8];
-        unpack_bf16x8(hv[i], a);
-        if (p.residual) {
-          float b[8];
-          unpack_bf16x8(rv[i], b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) a[e] += b[e];
-          hv[i] = pack_bf16x8(a);
-          unpack_bf16x8(hv[i], a);
-        }
-        if (p.h && j < nv) reinterpret_cast<v4i*>(p.h)[base + j] = hv[i];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
-      }
-      const float r = 1.0f / sqrtf(block_sum(ss, red[rr & 1]) / (float)p.k + p.eps);
-      if (p.rstd && tid == 0) p.rstd[row] = r;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int j = i * nt + tid;   // (j >= nv: whole groups of 16 lanes; their vectors are zeros)
-        const bool in = j < nv;
-        float y[8], w[8];
-        unpack_bf16x8(hv[i], y);
-        unpack_bf16x8(wv[i], w);
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = y[e] * r * w[e];
-          amax = umax(amax, abs_bits(y[e]));
-        }
-        const int kb = j >> 4;
-        if constexpr (FMT == DG_QUANT_MXFP4) {
-          const uint32_t byte = ue8m0_byte<false>(group_max<4>(amax));
-          const uint32_t word = scale_word(byte);
-          if (in) {
-            static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
-            if ((tid & 15) == 0) {
-              if constexpr (RC > 1) scales[kb * RC + rr] = word;
-              else static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
-            }
-          }
-        } else {
-          amax = group_max<16>(amax);
-          float inv;
-          if constexpr (FMT == DG_QUANT_E4M3_F32) {
-            float s = __uint_as_float(amax) / 448.0f;
-            s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(s, 0x1p-126f));
-            inv = 1.0f / s;
-            if (in && (tid & 15) == 0) {
-              if constexpr (RC > 1) scales[kb * RC + rr] = __float_as_uint(s);
-              else static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
-            }
-          } else {
-            // the wave's four blocks make one word (past the end: 2^0)
-            const uint32_t byte = in ? ue8m0_byte<true>(amax) : 127u;
-            inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);   // 2^(127 - byte)
-            uint32_t word = byte << (8 * ((tid >> 4) & 3));
-            word |= (uint32_t)__shfl_xor((int)word, 16, 64);
-            word |= (uint32_t)__shfl_xor((int)word, 32, 64);
-            if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
-          }
-          if (in)
-            static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                                   (int)e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
-        }
-      }
+    hv[i] = rv[i] = wv[i] = v4i{0, 0, 0, 0};
+    if (j < nv) {
+      hv[i] = reinterpret_cast<const v4i*>(p.x)[base + j];
+      if (p.residual) rv[i] = reinterpret_cast<const v4i*>(p.residual)[base + j];
+      wv[i] = reinterpret_cast<const v4i*>(p.weight)[j];
     }
-    if constexpr (FMT != DG_QUANT_E4M3_UE8M0 && RC > 1) {
-      __syncthreads();
-      for (int e = tid; e < kb_n * RC; e += nt) {
-        const int kb = e / RC, rr = e % RC;
-        if (rr < rows) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + r0 + rr] = scales[e];
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = i * nt + tid;
+    float a[8];
+    unpack_bf16x8(hv[i], a);
+    if (p.residual) {
+      float b[8];
+      unpack_bf16x8(rv[i], b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] += b[e];
+      hv[i] = pack_bf16x8(a);
+      unpack_bf16x8(hv[i], a);
+    }
+    if (p.h && j < nv) reinterpret_cast<v4i*>(p.h)[base + j] = hv[i];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+  }
+  const float r = 1.0f / sqrtf(block_sum(ss, red) / (float)p.k + p.eps);
+  if (p.rstd && tid == 0) p.rstd[row] = r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = i * nt + tid;   // (j >= nv: whole groups of 16 lanes; their vectors are zeros)
+    const bool in = j < nv;
+    float y[8], w[8];
+    unpack_bf16x8(hv[i], y);
+    unpack_bf16x8(wv[i], w);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = y[e] * r * w[e];
+      amax = umax(amax, abs_bits(y[e]));
+    }
+    const int kb = j >> 4;
+    if constexpr (FMT == DG_QUANT_MXFP4) {
+      const uint32_t byte = ue8m0_byte<false>(group_max<4>(amax));
+      const uint32_t word = scale_word(byte);
+      if (in) {
+        static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
+        if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
       }
-      __syncthreads();
+    } else {
+      amax = group_max<16>(amax);
+      float inv;
+      if constexpr (FMT == DG_QUANT_E4M3_F32) {
+        float s = __uint_as_float(amax) / 448.0f;
+        s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(s, 0x1p-126f));
+        inv = 1.0f / s;
+        if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
+      } else {
+        // the wave's four blocks make one word (past the end: 2^0)
+        const uint32_t byte = in ? ue8m0_byte<true>(amax) : 127u;
+        inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);   // 2^(127 - byte)
+        uint32_t word = byte << (8 * ((tid >> 4) & 3));
+        word |= (uint32_t)__shfl_xor((int)word, 16, 64);
+        word |= (uint32_t)__shfl_xor((int)word, 32, 64);
+        if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
+      }
+      if (in)
+        static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                               (int)e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
     }
   }
 }
@@ -180,8 +157,9 @@ struct NormBackParams {
 
 // A workgroup takes rows blockIdx.x, + gridDim.x, ...; a thread keeps its columns'
 // share of dweight in registers over them and writes one partial row at the end.  The
-// next row's vectors are loaded before this row's sum is waited for (up to 512 threads;
-// with 1024 a thread has 128 registers, too few for two rows).
+// next row's dy and h are loaded before this row's sum is waited for.  With more than
+// 512 threads a thread has 128 registers, too few for two rows (or even one): dy and h
+// are then read again for dx.
 template <int V, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_backward_kernel(NormBackParams p) {
   __shared__ float red[2][NORM_MAX_WAVES];
@@ -189,71 +167,68 @@ __global__ void __launch_bounds__(THREADS) rms_norm_backward_kernel(NormBackPara
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3;
   const float inv_k = 1.0f / (float)p.k;
+  const v4i none = {0, 0, 0, 0};
+  auto at = [&](const uint16_t* t, int row, int i) -> v4i {
+    const int j = i * nt + tid;
+    return j < nv ? reinterpret_cast<const v4i*>(t)[(size_t)row * nv + j] : none;
+  };
   float dw[V][8];
-  v4i wv[V], dyv[V], hv[V], dhv[V];
-  float r = 0.f;
+  v4i wv[V], dyn[V], hn[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int j = i * nt + tid;
-    wv[i] = j < nv ? reinterpret_cast<const v4i*>(p.weight)[j] : v4i{0, 0, 0, 0};
+    wv[i] = at(p.weight, 0, i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   }
-  auto load = [&](int row) {
-    const size_t base = (size_t)row * nv;
-    r = p.rstd[row];
+  int row = blockIdx.x, turn = 0;
+  float rn = 0.f;
+  auto load_next = [&](int r) {
+    rn = p.rstd[r];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int j = i * nt + tid;
-      dyv[i] = hv[i] = dhv[i] = v4i{0, 0, 0, 0};
-      if (j < nv) {
-        dyv[i] = reinterpret_cast<const v4i*>(p.dy)[base + j];
-        hv[i] = reinterpret_cast<const v4i*>(p.h)[base + j];
-        if (p.dh) dhv[i] = reinterpret_cast<const v4i*>(p.dh)[base + j];
-      }
+      dyn[i] = at(p.dy, r, i);
+      hn[i] = at(p.h, r, i);
     }
   };
-  int row = blockIdx.x, turn = 0;
-  if (row < p.m) load(row);
-  while (row < p.m) {
+  if (AHEAD && row < p.m) load_next(row);
+  for (; row < p.m; row += gridDim.x) {
     v4i dyc[V], hc[V], dhc[V];
-    const float rc = r;
     float dot = 0.f;
+    const float r = AHEAD ? rn : p.rstd[row];
+    if (AHEAD && p.dh) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) dhc[i] = at(p.dh, row, i);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      dyc[i] = dyv[i];
-      hc[i] = hv[i];
-      dhc[i] = dhv[i];
+      dyc[i] = AHEAD ? dyn[i] : at(p.dy, row, i);
+      hc[i] = AHEAD ? hn[i] : at(p.h, row, i);
       float a[8], n[8], w[8];
       unpack_bf16x8(dyc[i], a);
       unpack_bf16x8(hc[i], n);
       unpack_bf16x8(wv[i], w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[e] *= rc;
+        n[e] *= r;
         dw[i][e] = fmaf(a[e], n[e], dw[i][e]);
         dot = fmaf(a[e] * w[e], n[e], dot);
       }
     }
-    const int next = row + gridDim.x;
-    if (AHEAD && next < p.m) load(next);
+    if (AHEAD && row + (int)gridDim.x < p.m) load_next(row + gridDim.x);
     const float mean = block_sum(dot, red[turn]) * inv_k;
     turn ^= 1;
-    const size_t base = (size_t)row * nv;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int j = i * nt + tid;
       float a[8], n[8], w[8], d[8];
-      unpack_bf16x8(dyc[i], a);
-      unpack_bf16x8(hc[i], n);
+      unpack_bf16x8(AHEAD ? dyc[i] : at(p.dy, row, i), a);
+      unpack_bf16x8(AHEAD ? hc[i] : at(p.h, row, i), n);
       unpack_bf16x8(wv[i], w);
-      unpack_bf16x8(dhc[i], d);
+      unpack_bf16x8(p.dh ? (AHEAD ? dhc[i] : at(p.dh, row, i)) : none, d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] += rc * (a[e] * w[e] - n[e] * rc * mean);
-      if (j < nv) reinterpret_cast<v4i*>(p.dx)[base + j] = pack_bf16x8(d);
+      for (int e = 0; e < 8; ++e) d[e] += r * (a[e] * w[e] - n[e] * r * mean);
+      if (j < nv) reinterpret_cast<v4i*>(p.dx)[(size_t)row * nv + j] = pack_bf16x8(d);
     }
-    if (!AHEAD && next < p.m) load(next);
-    row = next;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -265,55 +240,48 @@ __global__ void __launch_bounds__(THREADS) rms_norm_backward_kernel(NormBackPara
   }
 }
 
-// dweight from the partial rows: a workgroup sums 64 columns, 16 threads (4 columns
-// each) across and 16 down, each every 16th row; their sums meet in LDS in order.
+// dweight from the partial rows: a workgroup sums 32 columns, 8 threads (4 columns
+// each) across and 32 down, each every 32nd row; their sums meet in LDS in order.
 __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, float* dweight, int parts, int k) {
-  __shared__ v4f sums[16][16];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const float* src = part + (size_t)blockIdx.x * 64 + cx * 4;
+  __shared__ v4f sums[32][8];
+  const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
+  const float* src = part + (size_t)blockIdx.x * 32 + cx * 4;
   v4f s = {0.f, 0.f, 0.f, 0.f};
-  int i = ry;
-  for (; i + 7 * 16 < parts; i += 8 * 16) {
+  for (int i = ry; i < parts; i += 8 * 32) {
     v4f t[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) t[u] = *reinterpret_cast<const v4f*>(src + (size_t)(i + u * 16) * k);
+    for (int u = 0; u < 8; ++u)
+      t[u] = i + u * 32 < parts ? *reinterpret_cast<const v4f*>(src + (size_t)(i + u * 32) * k) : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += t[u];
   }
-  for (; i < parts; i += 16) s += *reinterpret_cast<const v4f*>(src + (size_t)i * k);
   sums[ry][cx] = s;
   __syncthreads();
-  if (threadIdx.x < 16) {
+  if (threadIdx.x < 8) {
     v4f t = sums[0][threadIdx.x];
 #pragma unroll
-    for (int y = 1; y < 16; ++y) t += sums[y][threadIdx.x];
-    *reinterpret_cast<v4f*>(dweight + (size_t)blockIdx.x * 64 + threadIdx.x * 4) = t;
+    for (int y = 1; y < 32; ++y) t += sums[y][threadIdx.x];
+    *reinterpret_cast<v4f*>(dweight + (size_t)blockIdx.x * 32 + threadIdx.x * 4) = t;
   }
 }
 
-// Workgroups of the backward kernel, each with one partial row of dweight: about 4096
-// waves, a function of the sizes alone, so that the order of the sums is, too.
-static int norm_parts(int m, int k) { return std::min(m, 4096 / (norm_shape(k).threads / 64)); }
-
-// Rows per workgroup: several only when there are enough rows to fill the chip with them
-template <int FMT, int V>
-static hipError_t launch_norm_v(const NormParams& p, int threads, int cus, hipStream_t hs) {
-  if (FMT != DG_QUANT_E4M3_UE8M0 && V <= 2 && p.m >= 8 * 4 * cus)
-    hipLaunchKernelGGL((add_rms_norm_kernel<FMT, V, (V <= 2 ? 8 : 1)>), dim3(std::min((p.m + 7) / 8, cus * 32)), dim3(threads), 0,
-                       hs, p);
-  else
-    hipLaunchKernelGGL((add_rms_norm_kernel<FMT, V, 1>), dim3(std::min(p.m, cus * 32)), dim3(threads), 0, hs, p);
-  return hipGetLastError();
+// Workgroups of the backward kernel, each with one partial row of dweight: one of up to
+// eight waves per CU of the whole chip, or up to four smaller ones (more would write and
+// read more partial rows than they overlap: 4096 x 7168 takes 49 us with 256, 54 with
+// 512, 60 with 1024; 8192 x 512 takes 25, 17 and 14).  A function of the sizes alone, so
+// that the order of the sums is, too.
+static int norm_parts(int m, int k) {
+  const int waves = norm_shape(k).threads / 64;
+  return std::min(m, 256 * std::max(1, std::min(4, 8 / waves)));
 }
 
 template <int FMT>
-static hipError_t launch_norm(const NormParams& p, int cus, hipStream_t hs) {
+static hipError_t launch_norm(const NormParams& p, hipStream_t hs) {
   const NormShape s = norm_shape(p.k);
-  switch (s.v) {
-    case 1: return launch_norm_v<FMT, 1>(p, s.threads, cus, hs);
-    case 2: return launch_norm_v<FMT, 2>(p, s.threads, cus, hs);
-    default: return launch_norm_v<FMT, 4>(p, s.threads, cus, hs);
-  }
+  if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  else hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 4>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  return hipGetLastError();
 }
 
 static hipError_t launch_norm_backward(const NormBackParams& p, int grid, hipStream_t hs) {
@@ -346,13 +314,11 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
     if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    int cus = dg_get_num_cus();
-    if (cus <= 0) cus = di.num_cus;
     NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const hipError_t e = format == DG_QUANT_E4M3_F32     ? launch_norm<DG_QUANT_E4M3_F32>(p, cus, hs)
-                         : format == DG_QUANT_E4M3_UE8M0 ? launch_norm<DG_QUANT_E4M3_UE8M0>(p, cus, hs)
-                                                         : launch_norm<DG_QUANT_MXFP4>(p, cus, hs);
+    const hipError_t e = format == DG_QUANT_E4M3_F32     ? launch_norm<DG_QUANT_E4M3_F32>(p, hs)
+                         : format == DG_QUANT_E4M3_UE8M0 ? launch_norm<DG_QUANT_E4M3_UE8M0>(p, hs)
+                                                         : launch_norm<DG_QUANT_MXFP4>(p, hs);
     return e == hipSuccess ? DG_OK : DG_ERR_HIP;
   } catch (...) {
     return DG_ERR_HIP;
@@ -382,7 +348,7 @@ int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = launch_norm_backward(p, parts, hs);
     if (e != hipSuccess) return DG_ERR_HIP;
-    hipLaunchKernelGGL(norm_dweight_kernel, dim3(k / 64), dim3(256), 0, hs, p.part, dweight, parts, k);
+    hipLaunchKernelGGL(norm_dweight_kernel, dim3(k / 32), dim3(256), 0, hs, p.part, dweight, parts, k);
     return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
   } catch (...) {
     return DG_ERR_HIP;

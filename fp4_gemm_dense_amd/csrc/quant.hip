@@ -219,13 +219,22 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(QuantParams p) {
         }
       }
     }
+    // the codes leave through LDS (the tile is read): four lanes write the 64 bytes of a
+    // column, where each lane writing its own would send 16-byte pieces of 64 lines
+    __syncthreads();
+    uint8_t* stage = reinterpret_cast<uint8_t*>(tile);   // [128 columns][64 bytes, + 16 against bank conflicts]
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const size_t col = (size_t)g * p.k + kb * 128u + c2 + h;
-      *reinterpret_cast<v4i*>(p.qt + col * (mp / 2) + (size_t)mb * 64 + b * 16) = w[h];
+      *reinterpret_cast<v4i*>(stage + (c2 + h) * 80 + b * 16) = w[h];
       bytes[c2 + h][b] = (uint8_t)byte[h];
     }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int col = i * 64 + (tid >> 2);
+      *reinterpret_cast<v4i*>(p.qt + ((size_t)g * p.k + kb * 128u + col) * (mp / 2) + (size_t)mb * 64 + (tid & 3) * 16) =
+          *reinterpret_cast<const v4i*>(stage + col * 80 + (tid & 3) * 16);
+    }
     if (tid < 128) p.sft[((size_t)g * mb_n + mb) * p.k + kb * 128u + tid] = *reinterpret_cast<const int32_t*>(bytes[tid]);
     __syncthreads();
   }
