@@ -52,25 +52,36 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, uint32_t sa, const v4i& 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, FMT_E2M1, FMT_E2M1, 0, (int)sa, 0, (int)sb);
 }
 
+#ifndef MXBAR
+#define MXBAR(NT) 1
+#define MXLATE(NT, LPS) (NT == 8 ? 2 : NT == 4 ? 4 : 1)
+#endif
 // WM x WN waves of MT x NT blocks of 16 x 16; R ring slots.
 template <int MT_, int NT_, int WM_, int WN_, int R_>
 struct MxTile {
   static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, R = R_;
   static constexpr int NW = WM * WN, THREADS = NW * 64;
   static constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
-  static constexpr int OFF_B = BM * 128, OFF_SA = OFF_B + BN * 128, OFF_SB = OFF_SA + BM * 8;
-  static constexpr int STAGE = OFF_SB + BN * 8, LDS = R * STAGE;
+  // a stage: A rows, B rows, then the scale words of both K blocks ([2][BM], [2][BN]) in
+  // whole 1-KB copies
+  static constexpr int NSA = (BM * 8 + 1023) / 1024, NSB = (BN * 8 + 1023) / 1024;
+  static constexpr int OFF_B = BM * 128, OFF_SA = OFF_B + BN * 128, OFF_SB = OFF_SA + NSA * 1024;
+  static constexpr int STAGE = OFF_SB + NSB * 1024, LDS = R * STAGE;
   static constexpr int RA = BM / 8 / NW, RB = BN / 8 / NW;   // 1-KB copies (8 rows) per wave and stage
-  static constexpr int LPS = RA + RB + 2;                    // copies per wave and stage, with the scales'
-  static constexpr int NSA = BM / 32, NSB = BN / 32;         // 64-word scale copies of a stage
+  static constexpr int LPS = RA + RB + 1;                    // copies per wave and stage, with one of scales
   static constexpr int NSTORE = MT * NT / 2;                 // 16-byte stores of D per lane
-  static constexpr int BAR = NT > 2 ? 2 : 1;                 // column blocks ahead of the barrier
-  static_assert(NW == 8 && NSA <= NW && NSB <= NW && NW % NSA == 0 && NW % NSB == 0, "scale copies");
+  static constexpr int BAR = MXBAR(NT);   // column blocks ahead of the barrier
+  static constexpr int LATE = MXLATE(NT, LPS);   // copies of a stage issued in the next stage's first K block
+  static_assert(NW == 8 && NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
   static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024, "tile shape");
 };
 
-// chunk swizzle of a B row: the 16 rows that one fragment read touches (8a + b, a, b
-// = 0..3, plus 4 in odd column blocks) fall on distinct 16-byte bank groups
+// Chunk swizzles of an A and a B row.  A 16-byte LDS read serves lanes {0-3, 12-15,
+// 20-27}, {4-11, 16-19, 28-31} and the same of the upper 32 together (measured: two
+// lanes of one set on the same banks cost a cycle), over 64 banks, two rows.  With
+// these the 16 lanes of a set meet 16 different 16-byte bank groups: A's fragment reads
+// rows 0-15 by lane, B's rows 8a + b (a, b = 0..3; plus 4 in odd column blocks).
+__device__ __forceinline__ int swz_a(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) & 6); }
 
 // The value x, opaque to the compiler: lane-dependent terms that only a change of tile
@@ -118,67 +129,87 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
 
   const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
   const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
-  const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
-  const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
-
   // The copy cursor: the unit and stage copied next.  Copy j of a wave fills rows
   // 8 (RA wave + j) .. + 7 of the A tile: lane l position l % 8 of row (..) + l / 8,
-  // which holds chunk (l % 8) ^ swizzle(row); the swizzle's part that depends on j is
-  // uniform.  Rows past M lie past the buffer and read zeros, and so does the second
+  // which holds chunk (l % 8) ^ swizzle(row).  Rows past M lie past the buffer and read zeros, and so does the second
   // K block of a stage at an odd end of K: a zero code under a finite scale adds nothing.
   int cu = vb, cs = 0, c_kb0 = 0, c_nkb = 0;
   uint32_t slot_w = 0;   // the slot copied into next
-  uint32_t a_row = 0, b_row = 0, sa_off = 0, sb_off = 0;
-  const uint32_t a_bc = (uint32_t)((lane & 7) ^ (lane >> 3)) << 4;
-  const uint32_t b_bc = (uint32_t)((lane & 7) ^ ((lane >> 4) & 1)) << 4;
+  uint32_t off[T::LPS];
+  // per-lane offset of copy idx within its buffer, from tile row 0's bytes; chunks 4-7
+  // (bit 6 of the chunk's offset) are the stage's second K block
+  auto chunk_a = [&](int ln, int j) -> uint32_t {
+    return (uint32_t)((ln & 7) ^ swz_a((wave * T::RA + j) * 8 + (ln >> 3))) << 4;
+  };
+  auto chunk_b = [&](int ln, int j) -> uint32_t {
+    return (uint32_t)((ln & 7) ^ swz_b((wave * T::RB + j) * 8 + (ln >> 3))) << 4;
+  };
+  // this wave's scale copy: 1 KB of A's words or of B's
+  const int sc = wave % (T::NSA + T::NSB);
+  const bool sc_b = sc >= T::NSA;
+  const v4i rsS = make_buffer_rsrc(sc_b ? p.b_sf : p.a_sf, (uint32_t)KB * (uint32_t)(sc_b ? N : M) * 4u);
+  const uint32_t s_stride = (uint32_t)(sc_b ? N : M) * 4u;   // bytes of one K block's words
+  const uint32_t s_dst = sc_b ? T::OFF_SB + (sc - T::NSA) * 1024 : T::OFF_SA + sc * 1024;
+  auto scale_offset = [&](int ln, int m0, int n0, bool odd_end) -> uint32_t {
+    const int bt = sc_b ? T::BN : T::BM, rows = sc_b ? N : M, r0 = sc_b ? n0 : m0;
+    const int q = (sc_b ? sc - T::NSA : sc) * 256 + ln * 4, half = q / bt, row = r0 + q % bt;
+    // (rows past the end, lanes past the two K blocks, a second K block past the end)
+    return row < rows && half < (odd_end ? 1 : 2) ? (uint32_t)half * s_stride + (uint32_t)row * 4u : kBufferOutOfRange;
+  };
+  int c_m0 = 0, c_n0 = 0;
   auto cursor_to = [&](const Unit& w) {
+    c_m0 = w.m0;
+    c_n0 = w.n0;
     c_kb0 = w.kb0;
     c_nkb = w.nkb;
     cs = 0;
     const int ln = opaque(lane);
-    a_row = (uint32_t)(w.m0 + wave * T::RA * 8 + (ln >> 3)) * Kh;
-    b_row = (uint32_t)(w.n0 + wave * T::RB * 8 + (ln >> 3)) * Kh;
-    // scale words: position q of a K block's words holds the row that puts the words
-    // of a lane's MT row blocks (NT column blocks) side by side
-    {
-      const int q = (wave % T::NSA % (T::BM / 64)) * 64 + ln;
-      const int i = q % (MT * 16), row = w.m0 + q - i + (i % MT) * 16 + i / MT;
-      sa_off = row < M ? (uint32_t)row * 4u : kBufferOutOfRange;
-    }
-    {
-      const int q = (wave % T::NSB % (T::BN / 64)) * 64 + ln;
-      const int i = q % (NT * 16), nt = i % NT, r = i / NT;
-      const int row = w.n0 + q - i + (nt >> 1) * 32 + (r >> 2) * 8 + (nt & 1) * 4 + (r & 3);
-      sb_off = row < N ? (uint32_t)row * 4u : kBufferOutOfRange;
+#pragma unroll
+    for (int j = 0; j < T::RA; ++j)
+      off[j] = (uint32_t)(w.m0 + (wave * T::RA + j) * 8 + (ln >> 3)) * Kh + chunk_a(ln, j);
+#pragma unroll
+    for (int j = 0; j < T::RB; ++j)
+      off[T::RA + j] = (uint32_t)(w.n0 + (wave * T::RB + j) * 8 + (ln >> 3)) * Kh + chunk_b(ln, j);
+    // scale words: copy sc of the stage, four words (rows) of one K block per lane
+    off[T::RA + T::RB] = scale_offset(ln, w.m0, w.n0, false);
+  };
+  // the cursor's stage is a unit's last and has one K block only: its second one is
+  // out of range (the offsets are formed anew for the next unit)
+  auto cursor_odd_end = [&]() {
+    const int ln = opaque(lane);
+#pragma unroll
+    for (int j = 0; j < T::RA; ++j) off[j] |= (chunk_a(ln, j) & 64u) << 25;
+#pragma unroll
+    for (int j = 0; j < T::RB; ++j) off[T::RA + j] |= (chunk_b(ln, j) & 64u) << 25;
+    off[T::RA + T::RB] = scale_offset(ln, c_m0, c_n0, true);
+  };
+  // copy idx of a stage: per-lane offset o, first K block kb, slot
+  auto issue_at = [&](auto idx_tag, uint32_t o, int kb, uint32_t slot) {
+    constexpr int idx = decltype(idx_tag)::value;
+    if constexpr (idx < T::RA) {
+      buf16_to_lds(rsA, o, (uint32_t)kb * 64u, smem + slot + (wave * T::RA + idx) * 1024);
+    } else if constexpr (idx < T::RA + T::RB) {
+      buf16_to_lds(rsB, o, (uint32_t)kb * 64u, smem + slot + T::OFF_B + (wave * T::RB + idx - T::RA) * 1024);
+    } else {
+      // (the K block in the lane's offset: a lane's last words may lie past the end, and
+      // the range check of each then needs no scalar offset)
+      buf16_to_lds(rsS, o == kBufferOutOfRange ? o : o + (uint32_t)kb * s_stride, 0u, smem + slot + s_dst);
     }
   };
   // copy idx of the cursor's stage
-  auto issue = [&](auto idx_tag) {
-    constexpr int idx = decltype(idx_tag)::value;
-    const int kb = c_kb0 + 2 * cs;
-    const uint32_t kofs = (uint32_t)kb * 64u;
-    const bool odd_end = 2 * cs + 1 >= c_nkb;   // the stage's second K block is past the end
-    const uint32_t hi = odd_end ? 64u : 0u;     // chunks 4-7 are it
-    if constexpr (idx < T::RA) {
-      const uint32_t t = a_bc ^ (uint32_t)(((wave * T::RA + idx) & 1) << 4);
-      buf16_to_lds(rsA, (a_row + (uint32_t)(idx * 8) * Kh + t) | (t & hi) << 25, kofs,
-                   smem + slot_w + (wave * T::RA + idx) * 1024);
-    } else if constexpr (idx < T::RA + T::RB) {
-      constexpr int j = idx - T::RA;
-      const uint32_t t = b_bc ^ (uint32_t)(((wave * T::RB + j) & 3) << 5);
-      buf16_to_lds(rsB, (b_row + (uint32_t)(j * 8) * Kh + t) | (t & hi) << 25, kofs,
-                   smem + slot_w + T::OFF_B + (wave * T::RB + j) * 1024);
-    } else if constexpr (idx == T::RA + T::RB) {
-      const int i = wave % T::NSA, half = i / (T::BM / 64);
-      const bool none = half && odd_end;
-      buf4_to_lds(rsSA, none ? kBufferOutOfRange : sa_off, none ? 0u : (uint32_t)(kb + half) * (uint32_t)M * 4u,
-                  smem + slot_w + T::OFF_SA + i * 256);
-    } else {
-      const int i = wave % T::NSB, half = i / (T::BN / 64);
-      const bool none = half && odd_end;
-      buf4_to_lds(rsSB, none ? kBufferOutOfRange : sb_off, none ? 0u : (uint32_t)(kb + half) * (uint32_t)N * 4u,
-                  smem + slot_w + T::OFF_SB + i * 256);
-    }
+  auto issue = [&](auto idx_tag) { issue_at(idx_tag, off[decltype(idx_tag)::value], c_kb0 + 2 * cs, slot_w); };
+  // the last LATE copies of a stage are issued in the next one, from these
+  uint32_t late_off[T::LATE > 0 ? T::LATE : 1], late_slot = 0;
+  int late_kb = 0;
+  auto keep_late = [&]() {
+#pragma unroll
+    for (int i = 0; i < T::LATE; ++i) late_off[i] = off[T::LPS - T::LATE + i];
+    late_kb = c_kb0 + 2 * cs;
+    late_slot = slot_w;
+  };
+  auto issue_late = [&](auto i_tag) {
+    constexpr int i = decltype(i_tag)::value;
+    issue_at(std::integral_constant<int, T::LPS - T::LATE + i>{}, late_off[i], late_kb, late_slot);
   };
   // to the next stage, of the next unit if this one has no more (past the last unit
   // the last unit is copied again; nothing reads it)
@@ -189,15 +220,16 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if (cu + G < p.units) cu += G;
       cursor_to(decode(cu));
     }
+    if (2 * cs + 1 == c_nkb) cursor_odd_end();
   };
 
   // fragment addresses within a slot; K block 1 of a stage is chunks 4-7
-  const uint32_t a_rd = (uint32_t)(wave_m * MT * 16 + lrow) * 128u + (uint32_t)((lgrp ^ swz(lrow)) << 4);
+  const uint32_t a_rd = (uint32_t)(wave_m * MT * 16 + lrow) * 128u + (uint32_t)((lgrp ^ swz_a(lrow)) << 4);
   const int brow = (lrow >> 2) * 8 + (lrow & 3);   // (+ 4 in odd column blocks, + 32 per pair: the same swizzle)
   const uint32_t b_rd =
       T::OFF_B + (uint32_t)(wave_n * NT * 16 + brow) * 128u + (uint32_t)((lgrp ^ swz_b(brow)) << 4);
-  const uint32_t sa_rd = T::OFF_SA + (uint32_t)(wave_m * MT * 16 + lrow * MT) * 4u;
-  const uint32_t sb_rd = T::OFF_SB + (uint32_t)(wave_n * NT * 16 + lrow * NT) * 4u;
+  const uint32_t sa_rd = T::OFF_SA + (uint32_t)(wave_m * MT * 16 + lrow) * 4u;
+  const uint32_t sb_rd = T::OFF_SB + (uint32_t)(wave_n * NT * 16 + brow) * 4u;
   const int sh = 8 * lgrp;
 
   v4i af[2][MT], bf[NT];
@@ -211,7 +243,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     constexpr int H = decltype(half_tag)::value;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-      sa[H][mt] = *reinterpret_cast<const uint32_t*>(smem + rd + sa_rd + H * (T::BM * 4) + mt * 4);
+      sa[H][mt] = *reinterpret_cast<const uint32_t*>(smem + rd + sa_rd + H * (T::BM * 4) + mt * 64);
   };
   // what column block nt's registers take over after their last use: its fragment,
   // and after the last of a half of the column blocks that half's scale words
@@ -221,7 +253,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     if constexpr (nt % NH == NH - 1) {
 #pragma unroll
       for (int e = nt - NH + 1; e <= nt; ++e)
-        sb[e] = *reinterpret_cast<const uint32_t*>(smem + rd + sb_rd + H * (T::BN * 4) + e * 4);
+        sb[e] = *reinterpret_cast<const uint32_t*>(smem + rd + sb_rd + H * (T::BN * 4) + (e >> 1) * 128 + (e & 1) * 16);
     }
   };
   using I0 = std::integral_constant<int, 0>;
@@ -229,6 +261,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
 
   // prologue: R stages in flight, the first one's fragments
   cursor_to(decode(cu));
+  if (c_nkb == 1) cursor_odd_end();
   static_for<R>([&](auto r) {
     static_for<T::LPS>([&](auto i) { issue(i); });
     if constexpr (decltype(r)::value + 1 < R) advance();
@@ -245,6 +278,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   // the copies of the stage waited for (the first unit of all waited in the prologue).
   auto stage = [&](auto first_tag) {
     constexpr bool FIRST = decltype(first_tag)::value;
+    if constexpr (!FIRST) keep_late();
     advance();   // (ahead of the matrix instructions: its branch must not split them)
     const uint32_t nx = rd + T::STAGE == T::LDS ? 0u : rd + T::STAGE;
     // first K block: read the second one's fragments
@@ -261,6 +295,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if constexpr (nt < MT) read_a(rd, I1{}, nt_tag);
       if constexpr (nt == NT - 1 && MT > NT)
         static_for<(MT > NT ? MT - NT : 0)>([&](auto e) { read_a(rd, I1{}, std::integral_constant<int, NT + decltype(e)::value>{}); });
+      if constexpr (!FIRST) {
+        if constexpr (nt < T::LATE) issue_late(nt_tag);
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
     // second K block: after BAR column blocks the barrier, then the next stage's
@@ -292,7 +329,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if constexpr (nt >= T::BAR - 1) {
         // the copies, spread over the column blocks from the barrier on
         constexpr int parts = NT - T::BAR + 1, q = nt - (T::BAR - 1);
-        constexpr int lo = T::LPS * q / parts, hi = T::LPS * (q + 1) / parts;
+        constexpr int now = T::LPS - T::LATE, lo = now * q / parts, hi = now * (q + 1) / parts;
         static_for<hi - lo>([&](auto e) { issue(std::integral_constant<int, lo + decltype(e)::value>{}); });
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -311,6 +348,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     stage(std::true_type{});
 #pragma clang loop unroll(disable)
     for (int s = 1; s < S; ++s) stage(std::false_type{});
+    // (the last stage's late copies go out ahead of the stores)
+    keep_late();
+    static_for<T::LATE>([&](auto i) { issue_late(i); });
 
     if (cur.part >= 0) {
       // fp32 partial tile of this slice: ws[part][BM][BN]
