@@ -454,11 +454,10 @@ _X_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
 QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4 = 0, 1, 2
 
 
-def _call(name, dev, *args):
-    """The C entry point on device dev and torch's current stream there.  (A decode step makes many calls of a few
+def _call(name, index, *args):
+    """The C entry point on device `index` and torch's current stream there.  (A decode step makes many calls of a few
     microseconds: these wrappers read the raw stream and device index, and pass addresses as plain integers.)"""
     f = getattr(_lib or load_library(), name)
-    index = dev.index
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             st = f(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -468,11 +467,11 @@ def _call(name, dev, *args):
         raise DgError(name, st)
 
 
-def _arg(t, dtypes, shape, dev, name):
-    """Checks one tensor argument (None passes) and returns its address."""
+def _arg(t, dtypes, shape, index, name):
+    """Checks one tensor argument (None passes; index: the device it has to be on) and returns its address."""
     if t is None:
         return None
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.device == dev and t.is_cuda:
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == index >= 0:
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
@@ -480,9 +479,14 @@ def _arg(t, dtypes, shape, dev, name):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if not t.is_cuda:
+    if t.get_device() < 0 or index < 0:
         raise ValueError(f"{name}: must be a device tensor")
-    raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    raise ValueError(f"{name}: on device {t.get_device()}, expected {index}")
+
+
+def _new(shape, dtype, dev):
+    """A new contiguous 1-D or 2-D tensor (the quickest of torch's constructors)."""
+    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=dev)
 
 
 _U8S, _I32S, _F32S = (_U8,), (torch.int32,), (torch.float32,)
@@ -499,7 +503,7 @@ def dg_quantize_mxfp4(x, q=None, sf=None, qt=None, sft=None, values=None):
     sf [.., k/128, m] int32; blocks along m, transposed: qt [.., k, mp/2] and sft [.., mp/128, k], mp = m rounded up
     to 128; values [.., m, k] bf16: what q and sf stand for.  Outputs that are None are not computed."""
     G, m, k = _matrix_dims(x)
-    lead, mb, dev = x.shape[:-2], (m + 127) // 128, x.device
+    lead, mb, dev = x.shape[:-2], (m + 127) // 128, x.get_device()
     xp = _arg(x, _X_TYPES, x.shape, dev, "x")
     _call("dg_quantize_mxfp4", dev, xp, _X_TYPES[x.dtype], _arg(q, _U8S, (*lead, m, k // 2), dev, "q"),
           _arg(sf, _I32S, (*lead, k // 128, m), dev, "sf"), _arg(qt, _U8S, (*lead, k, mb * 64), dev, "qt"),
@@ -515,13 +519,13 @@ def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
     """d = c + a . b^T, both operands MXFP4: a [M, K/2] uint8, a_sf [K/128, M] int32, b [N, K/2], b_sf [K/128, N].
     workspace: optional uint8 device tensor (allocated here when needed and not given)."""
     m, kh = a.shape
-    n, k, dev = b.shape[0], 2 * kh, a.device
+    n, k, dev = b.shape[0], 2 * kh, a.get_device()
     kb = k // 128
     ap = _arg(a, _U8S, (m, kh), dev, "a")
     if workspace is None:
         nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=_U8, device=dev)
+            workspace = _new((nbytes,), _U8, a.device)
             wp = workspace.data_ptr()
     else:
         nbytes = workspace.numel()
@@ -539,7 +543,7 @@ def dg_add_rms_norm(x, residual, weight, h, q, sf, eps, quant_format, rstd=None)
     m, k = x.shape
     if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
         raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
-    shape, dev = (m, k), x.device
+    shape, dev = (m, k), x.get_device()
     sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
     _call("dg_add_rms_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
           _arg(weight, _BF, (k,), dev, "weight"), _arg(h, _BF, shape, dev, "h"),
@@ -556,7 +560,7 @@ def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace):
     """dx [m, k] bf16 and dweight [k] fp32 from dy, dh (or None), h [m, k] bf16, weight [k] bf16 and the forward
     pass's rstd [m] (see include/dg.h)."""
     m, k = dy.shape
-    shape, dev = (m, k), dy.device
+    shape, dev = (m, k), dy.get_device()
     _call("dg_add_rms_norm_backward", dev, _arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"),
           _arg(h, _BF, shape, dev, "h"), _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"),
           _arg(dx, _BF, shape, dev, "dx"), _arg(dweight, _F32S, (k,), dev, "dweight"), m, k,
@@ -647,65 +651,61 @@ def quantize_mxfp4(x, transposed=False, values=False):
     (q, sf, qt, sft), qt and sft the transposed operand, whose products sum over m; with values, also the bf16 values
     that q and sf stand for, as the last item."""
     G, m, k = _matrix_dims(x)
-    lead, dev = x.shape[:-2], x.device
-    xp = _arg(x, _X_TYPES, x.shape, dev, "x")
-    q = torch.empty((*lead, m, k // 2), dtype=_U8, device=dev)
-    sf = torch.empty((*lead, k // 128, m), dtype=torch.int32, device=dev)
-    out = (q, sf)
-    qtp = sftp = vp = None
+    index, dev = x.get_device(), x.device
+    xp = _arg(x, _X_TYPES, x.shape, index, "x")
+    grouped = x.dim() == 3
+    q, sf = _new((G * m, k // 2), _U8, dev), _new((G * (k // 128), m), torch.int32, dev)
+    qt = sft = v = qtp = sftp = vp = None
     if transposed:
         mb = (m + 127) // 128
-        qt = torch.empty((*lead, k, mb * 64), dtype=_U8, device=dev)
-        sft = torch.empty((*lead, mb, k), dtype=torch.int32, device=dev)
+        qt, sft = _new((G * k, mb * 64), _U8, dev), _new((G * mb, k), torch.int32, dev)
         qtp, sftp = qt.data_ptr(), sft.data_ptr()
-        out += (qt, sft)
     if values:
-        v = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        v = torch.empty_like(x, dtype=torch.bfloat16)
         vp = v.data_ptr()
-        out += (v,)
-    _call("dg_quantize_mxfp4", dev, xp, _X_TYPES[x.dtype], q.data_ptr(), sf.data_ptr(), qtp, sftp, vp, G, m, k)
-    return out
+    _call("dg_quantize_mxfp4", index, xp, _X_TYPES[x.dtype], q.data_ptr(), sf.data_ptr(), qtp, sftp, vp, G, m, k)
+    out = (q, sf, qt, sft) if transposed else (q, sf)
+    if grouped:
+        out = tuple(t.view(G, -1, t.shape[1]) for t in out)
+    return out if v is None else (*out, v)
 
 
 def mxfp4_gemm_nt(a, a_sf, b, b_sf, c=None):
     """Returns a new bf16 tensor d = c + a . b^T, both operands MXFP4."""
-    d = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
-    return dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d)
+    return dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, _new((a.shape[0], b.shape[0]), torch.bfloat16, a.device))
 
 
 def add_rms_norm(x, residual, weight, eps=1e-6, quant_format=QUANT_E4M3_F32):
     """(q, sf, h, rstd): the quantised norm of h = x + residual (residual None: h is x itself), with h and
     rstd = 1 / rms(h) for the residual stream and the backward pass."""
     m, k = x.shape
-    shape, dev = (m, k), x.device
-    xp, rp = _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual")
-    wp = _arg(weight, _BF, (k,), dev, "weight")
-    q = torch.empty((m, k // 2) if quant_format == QUANT_MXFP4 else shape, dtype=_U8, device=dev)
+    shape, index, dev = (m, k), x.get_device(), x.device
+    xp, rp = _arg(x, _BF, shape, index, "x"), _arg(residual, _BF, shape, index, "residual")
+    wp = _arg(weight, _BF, (k,), index, "weight")
+    q = _new((m, k // 2) if quant_format == QUANT_MXFP4 else shape, _U8, dev)
     if quant_format == QUANT_E4M3_UE8M0:
-        sf = torch.empty((m, _kw(k)), dtype=torch.int32, device=dev)
+        sf = _new((m, _kw(k)), torch.int32, dev)
     else:
-        sf = torch.empty((k // 128, m), dtype=torch.float32 if quant_format == QUANT_E4M3_F32 else torch.int32,
-                         device=dev)
-    rstd = torch.empty(m, dtype=torch.float32, device=dev)
+        sf = _new((k // 128, m), torch.float32 if quant_format == QUANT_E4M3_F32 else torch.int32, dev)
+    rstd = _new((m,), torch.float32, dev)
     h, hp = x, None
     if residual is not None:
         h = torch.empty_like(x)
         hp = h.data_ptr()
-    _call("dg_add_rms_norm", dev, xp, rp, wp, hp, q.data_ptr(), sf.data_ptr(), quant_format, rstd.data_ptr(), m, k, eps)
+    _call("dg_add_rms_norm", index, xp, rp, wp, hp, q.data_ptr(), sf.data_ptr(), quant_format, rstd.data_ptr(), m, k, eps)
     return q, sf, h, rstd
 
 
 def add_rms_norm_backward(dy, dh, h, weight, rstd):
     """(dx, dweight) of add_rms_norm: dx bf16 is the gradient of x and of residual alike, dweight fp32."""
     m, k = dy.shape
-    shape, dev = (m, k), dy.device
-    ins = (_arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"), _arg(h, _BF, shape, dev, "h"),
-           _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"))
-    dx = torch.empty_like(dy)
-    dweight = torch.empty(k, dtype=torch.float32, device=dev)
+    shape, index, dev = (m, k), dy.get_device(), dy.device
+    ins = (_arg(dy, _BF, shape, index, "dy"), _arg(dh, _BF, shape, index, "dh"), _arg(h, _BF, shape, index, "h"),
+           _arg(weight, _BF, (k,), index, "weight"), _arg(rstd, _F32S, (m,), index, "rstd"))
+    dx, dweight = torch.empty_like(dy), _new((k,), torch.float32, dev)
     nbytes = (_lib or load_library()).dg_add_rms_norm_backward_workspace_bytes(m, k)
-    ws = torch.empty(nbytes, dtype=_U8, device=dev)
-    _call("dg_add_rms_norm_backward", dev, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, ws.data_ptr(), nbytes)
+    ws = _new((nbytes,), _U8, dev)
+    _call("dg_add_rms_norm_backward", index, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, ws.data_ptr(), nbytes)
     return dx, dweight
 
 

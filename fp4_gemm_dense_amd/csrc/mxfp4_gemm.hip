@@ -56,24 +56,25 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, uint32_t sa, const v4i& 
 #define MXBAR(NT) 1
 #define MXLATE(NT, LPS) (NT == 8 ? 2 : NT == 4 ? 4 : 1)
 #endif
-// WM x WN waves of MT x NT blocks of 16 x 16; R ring slots.
-template <int MT_, int NT_, int WM_, int WN_, int R_>
+// WM x WN waves of MT x NT blocks of 16 x 16; R ring slots; KG groups of such waves,
+// each with a ring of its own, that take the stages of a tile in turn.
+template <int MT_, int NT_, int WM_, int WN_, int R_, int KG_>
 struct MxTile {
-  static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, R = R_;
-  static constexpr int NW = WM * WN, THREADS = NW * 64;
+  static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, R = R_, KG = KG_;
+  static constexpr int NW = WM * WN, THREADS = NW * KG * 64;
   static constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
   // a stage: A rows, B rows, then the scale words of both K blocks ([2][BM], [2][BN]) in
   // whole 1-KB copies
   static constexpr int NSA = (BM * 8 + 1023) / 1024, NSB = (BN * 8 + 1023) / 1024;
   static constexpr int OFF_B = BM * 128, OFF_SA = OFF_B + BN * 128, OFF_SB = OFF_SA + NSA * 1024;
-  static constexpr int STAGE = OFF_SB + NSB * 1024, LDS = R * STAGE;
+  static constexpr int STAGE = OFF_SB + NSB * 1024, RING = R * STAGE, LDS = KG * RING;
   static constexpr int RA = BM / 8 / NW, RB = BN / 8 / NW;   // 1-KB copies (8 rows) per wave and stage
   static constexpr int LPS = RA + RB + 1;                    // copies per wave and stage, with one of scales
   static constexpr int NSTORE = MT * NT / 2;                 // 16-byte stores of D per lane
   static constexpr int BAR = MXBAR(NT);   // column blocks ahead of the barrier
   static constexpr int LATE = MXLATE(NT, LPS);   // copies of a stage issued in the next stage's first K block
-  static_assert(NW == 8 && NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
-  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024, "tile shape");
+  static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
+  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && MT % 2 == 0)), "tile shape");
 };
 
 // Chunk swizzles of an A and a B row.  A 16-byte LDS read serves lanes {0-3, 12-15,
@@ -94,9 +95,11 @@ __device__ __forceinline__ int opaque(int x) {
 template <typename T>
 __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p) {
   constexpr int MT = T::MT, NT = T::NT, R = T::R;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_all % T::NW, grp = wave_all / T::NW;   // K group, and the wave in it
+  uint8_t* const smem = smem_all + grp * T::RING;
   const int wave_m = wave / T::WN, wave_n = wave % T::WN;
   const int lrow = lane & 15, lgrp = lane >> 4;
   const int M = p.m, N = p.n;
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   // 8 (RA wave + j) .. + 7 of the A tile: lane l position l % 8 of row (..) + l / 8,
   // which holds chunk (l % 8) ^ swizzle(row).  Rows past M lie past the buffer and read zeros, and so does the second
   // K block of a stage at an odd end of K: a zero code under a finite scale adds nothing.
-  int cu = vb, cs = 0, c_kb0 = 0, c_nkb = 0;
+  int cu = vb, cs = 0, c_kb = 0, c_nkb = 0;   // unit, stage of this group, its first K block, K blocks of the unit
   uint32_t slot_w = 0;   // the slot copied into next
   uint32_t off[T::LPS];
   // per-lane offset of copy idx within its buffer, from tile row 0's bytes; chunks 4-7
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   auto cursor_to = [&](const Unit& w) {
     c_m0 = w.m0;
     c_n0 = w.n0;
-    c_kb0 = w.kb0;
+    c_kb = w.kb0 + 2 * grp;
     c_nkb = w.nkb;
     cs = 0;
     const int ln = opaque(lane);
@@ -197,30 +200,50 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     }
   };
   // copy idx of the cursor's stage
-  auto issue = [&](auto idx_tag) { issue_at(idx_tag, off[decltype(idx_tag)::value], c_kb0 + 2 * cs, slot_w); };
+  auto issue = [&](auto idx_tag) { issue_at(idx_tag, off[decltype(idx_tag)::value], c_kb, slot_w); };
   // the last LATE copies of a stage are issued in the next one, from these
   uint32_t late_off[T::LATE > 0 ? T::LATE : 1], late_slot = 0;
   int late_kb = 0;
   auto keep_late = [&]() {
 #pragma unroll
     for (int i = 0; i < T::LATE; ++i) late_off[i] = off[T::LPS - T::LATE + i];
-    late_kb = c_kb0 + 2 * cs;
+    late_kb = c_kb;
     late_slot = slot_w;
   };
   auto issue_late = [&](auto i_tag) {
     constexpr int i = decltype(i_tag)::value;
     issue_at(std::integral_constant<int, T::LPS - T::LATE + i>{}, late_off[i], late_kb, late_slot);
   };
-  // to the next stage, of the next unit if this one has no more (past the last unit
-  // the last unit is copied again; nothing reads it)
+  // nothing more to copy: out of range from here on (the instructions still count), with
+  // a scalar offset of 0, so that the range check sees the lane's offset alone
+  auto cursor_none = [&]() {
+    c_kb = 0;
+#pragma unroll
+    for (int j = 0; j < T::LPS; ++j) off[j] = kBufferOutOfRange;
+  };
+  // the cursor's stage st: its second K block may be past the end, or all of it (the
+  // last stage of the last K group)
+  auto cursor_check = [&]() {
+    const int st = cs * T::KG + grp;
+    if (2 * st + 1 == c_nkb) cursor_odd_end();
+    if (T::KG > 1 && 2 * st >= c_nkb) cursor_none();
+  };
+  // to the next stage, of the next unit if this one has no more
   auto advance = [&]() {
-    slot_w = slot_w + T::STAGE == T::LDS ? 0u : slot_w + T::STAGE;
+    slot_w = slot_w + T::STAGE == T::RING ? 0u : slot_w + T::STAGE;
     ++cs;
-    if (2 * cs >= c_nkb) {
-      if (cu + G < p.units) cu += G;
-      cursor_to(decode(cu));
+    c_kb += 2 * T::KG;
+    if (2 * cs * T::KG >= c_nkb) {
+      if (T::KG == 1 && cu + G < p.units) {
+        cu += G;
+        cursor_to(decode(cu));
+        cursor_check();
+      } else {
+        cursor_none();
+      }
+    } else {
+      cursor_check();
     }
-    if (2 * cs + 1 == c_nkb) cursor_odd_end();
   };
 
   // fragment addresses within a slot; K block 1 of a stage is chunks 4-7
@@ -261,12 +284,12 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
 
   // prologue: R stages in flight, the first one's fragments
   cursor_to(decode(cu));
-  if (c_nkb == 1) cursor_odd_end();
+  cursor_check();
   static_for<R>([&](auto r) {
     static_for<T::LPS>([&](auto i) { issue(i); });
     if constexpr (decltype(r)::value + 1 < R) advance();
   });
-  wait_vmcnt<0>();
+  wait_vmcnt<T::KG == 1 ? 0 : (R - 1) * T::LPS>();   // (KG 1: the first stage below counts on all of them)
   block_barrier();
   uint32_t rd = 0;
   read_sa(0u, I0{});
@@ -274,13 +297,13 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   static_for<NT>([&](auto nt) { read_b(0u, I0{}, nt); });
 
   v4f acc[MT][NT];
-  // One stage.  FIRST: the first of a unit, whose predecessor's stores were issued after
-  // the copies of the stage waited for (the first unit of all waited in the prologue).
-  auto stage = [&](auto first_tag) {
-    constexpr bool FIRST = decltype(first_tag)::value;
+  // One stage.  FIRST: the first of a unit (the stage before has no late copies left);
+  // STORES: the unit before stored D after the copies of the stage waited for here.
+  auto stage = [&](auto first_tag, auto stores_tag) {
+    constexpr bool FIRST = decltype(first_tag)::value, STORES = decltype(stores_tag)::value;
     if constexpr (!FIRST) keep_late();
     advance();   // (ahead of the matrix instructions: its branch must not split them)
-    const uint32_t nx = rd + T::STAGE == T::LDS ? 0u : rd + T::STAGE;
+    const uint32_t nx = rd + T::STAGE == T::RING ? 0u : rd + T::STAGE;
     // first K block: read the second one's fragments
     static_for<NT>([&](auto nt_tag) {
       constexpr int nt = decltype(nt_tag)::value;
@@ -313,7 +336,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if constexpr (nt == T::BAR - 1) {
         __builtin_amdgcn_sched_barrier(0);
         wait_lgkmcnt0();
-        wait_vmcnt<(R - 2) * T::LPS + (FIRST ? T::NSTORE : 0)>();
+        wait_vmcnt<(R - 2) * T::LPS + (STORES ? T::NSTORE : 0)>();
         block_barrier();
         read_sa(nx, I0{});
         static_for<T::BAR>([&](auto e) {
@@ -344,14 +367,41 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    const int S = (cur.nkb + 1) >> 1;
-    stage(std::true_type{});
+    const int S = ((cur.nkb + 1) / 2 + T::KG - 1) / T::KG;   // stages of this group
+    stage(std::true_type{}, std::integral_constant<bool, T::KG == 1>{});
 #pragma clang loop unroll(disable)
-    for (int s = 1; s < S; ++s) stage(std::false_type{});
+    for (int s = 1; s < S; ++s) stage(std::false_type{}, std::false_type{});
     // (the last stage's late copies go out ahead of the stores)
     keep_late();
     static_for<T::LATE>([&](auto i) { issue_late(i); });
 
+    int mt0 = 0, mt1 = MT;   // the row blocks this group stores
+    if constexpr (T::KG == 2) {
+      // the groups' sums meet: each hands the other half of its row blocks over in LDS
+      // (one unit per workgroup: the rings are done with)
+      wait_vmcnt<0>();
+      wait_lgkmcnt0();
+      block_barrier();
+      constexpr int MH = MT / 2;
+      v4f* xch = reinterpret_cast<v4f*>(smem_all) + wave * 64 + lane;   // [group][MH][NT][wave][lane]
+#pragma unroll
+      for (int mt = 0; mt < MH; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          xch[((grp * MH + mt) * NT + nt) * (T::NW * 64)] = grp ? acc[mt][nt] : acc[MH + mt][nt];
+      wait_lgkmcnt0();
+      block_barrier();
+#pragma unroll
+      for (int mt = 0; mt < MH; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const v4f o = xch[(((1 - grp) * MH + mt) * NT + nt) * (T::NW * 64)];
+          if (grp) acc[MH + mt][nt] += o;
+          else acc[mt][nt] += o;
+        }
+      mt0 = grp * MH;
+      mt1 = mt0 + MH;
+    }
     if (cur.part >= 0) {
       // fp32 partial tile of this slice: ws[part][BM][BN]
       const v4i rsW = make_buffer_rsrc(p.ws + (size_t)cur.part * (T::BM * T::BN), (uint32_t)(T::BM * T::BN * 4));
@@ -359,6 +409,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          if (mt < mt0 || mt >= mt1) continue;
           const int row = wave_m * MT * 16 + mt * 16 + lrow;
           const int col = wave_n * NT * 16 + (nt >> 1) * 32 + lgrp * 8 + (nt & 1) * 4;
           const v4i w = {__float_as_int(acc[mt][nt][0]), __float_as_int(acc[mt][nt][1]),
@@ -370,6 +421,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       const v4i rsC = make_buffer_rsrc(p.c, p.c ? (uint32_t)M * (uint32_t)N * 2u : 0u);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
+        if (mt < mt0 || mt >= mt1) continue;
         const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + lrow;
 #pragma unroll
         for (int np = 0; np < NT / 2; ++np) {
@@ -397,28 +449,29 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   wait_vmcnt<0>();   // the copies past the last stage: LDS is not given back before they have landed
 }
 
-// id, MT, NT, WM, WN, ring slots
+// id, MT, NT, WM, WN, ring slots, K groups
 #define DG_MXFP4_TILES(X) \
-  X(0, 4, 8, 4, 2, 2)     \
-  X(1, 4, 4, 2, 4, 3)     \
-  X(2, 2, 4, 4, 2, 4)     \
-  X(3, 2, 2, 2, 4, 6)
+  X(0, 4, 8, 4, 2, 2, 1)  \
+  X(1, 4, 4, 2, 4, 3, 1)  \
+  X(2, 2, 4, 4, 2, 4, 1)  \
+  X(3, 2, 2, 2, 4, 6, 1)  \
+  X(4, 4, 4, 2, 2, 2, 2)  \
+  X(5, 2, 4, 2, 2, 3, 2)
 
 struct Mxfp4TileInfo {
-  int bm, bn, lds, threads;
+  int bm, bn, kg;
 };
 static const Mxfp4TileInfo kMxTiles[] = {
-#define X(id, MT, NT, WM, WN, R) \
-  {MxTile<MT, NT, WM, WN, R>::BM, MxTile<MT, NT, WM, WN, R>::BN, MxTile<MT, NT, WM, WN, R>::LDS, MxTile<MT, NT, WM, WN, R>::THREADS},
+#define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG},
     DG_MXFP4_TILES(X)
 #undef X
 };
 
 static hipError_t launch_mxfp4_tile(const Mxfp4Params& p, int id, int grid, hipStream_t stream) {
   switch (id) {
-#define X(i, MT, NT, WM, WN, R)                                                                          \
+#define X(i, MT, NT, WM, WN, R, KG)                                                                      \
   case i: {                                                                                              \
-    using T = MxTile<MT, NT, WM, WN, R>;                                                                 \
+    using T = MxTile<MT, NT, WM, WN, R, KG>;                                                             \
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T>), \
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);  \
     if (attr != hipSuccess) return attr;                                                                 \
@@ -592,7 +645,7 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
   const long long tiles = (long long)pl.tiles_m * pl.tiles_n;
   const int kb = k / 128;
   long long full = tiles;
-  pl.splits = split_rule(tiles, cus, kb, &full);
+  pl.splits = t.kg > 1 ? 1 : split_rule(tiles, cus, kb, &full);
   pl.kb_per_split = kb;
   if (pl.splits > 1) {
     pl.kb_per_split = ((kb + pl.splits - 1) / pl.splits + 1) & ~1;   // whole stages
@@ -615,7 +668,7 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
 // K = 7168 and 16384) and a fixed share per unit (pipeline fill, D), and for a split
 // the partials' round trip and a second launch.
 static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.90, 1.30, 0.78, 0.52}, kUnit[] = {3.5, 1.6, 0.8, 0.6};
+  constexpr double kStage[] = {1.80, 1.12, 0.74, 0.52, 0.90, 0.65}, kUnit[] = {3.5, 1.6, 0.8, 0.6, 2.0, 1.5};
   constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
   int force = -1;
   if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
@@ -624,7 +677,9 @@ static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
   for (int id = 0; id < kTiles; ++id) {
     if (force >= 0 && force < kTiles && id != force) continue;
     const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
-    const int stages = (pl.kb_per_split + 1) / 2, whole = (k / 128 + 1) / 2;
+    const int kg = kMxTiles[id].kg;
+    if (kg > 1 && pl.units > cus) continue;   // one unit per workgroup
+    const int stages = (pl.kb_per_split + 1) / 2, whole = ((k / 128 + 1) / 2 + kg - 1) / kg;
     double t;
     if (pl.splits > 1) {
       t = (double)(pl.full_tiles / cus) * (whole * kStage[id] + kUnit[id]) + stages * kStage[id] + kUnit[id] + 4.0 +
