@@ -14,15 +14,28 @@
 //   * a wave multiplies K block kb while it reads the fragments of kb + 1: A's into a
 //     second register set, B's into the registers of the column block that has just
 //     had its last use;
-//   * one barrier per stage, inside its second K block, after the first two column
-//     blocks: by then the wave's reads of the slot are back without a wait.  It frees
-//     the slot for stage s + R and certifies stage s + 1;
+//   * one barrier per stage, inside its second K block, after the first column blocks:
+//     by then the wave's reads of the slot are back without a wait.  It frees the slot
+//     for stage s + R and certifies stage s + 1;
 //   * the stage copies run on into the next tile, so its first stage is there when
 //     the tile ends; D goes from the registers to memory, 16 bytes a lane: the columns
 //     of B's fragments are permuted so that a lane's two neighbouring column blocks
 //     are eight adjacent columns;
 //   * K may be split (few tiles, or a small last round): slices write fp32 partial
-//     tiles to the workspace, which the split-K reduce adds in slice order.
+//     tiles to the workspace, which the split-K reduce adds in slice order.  The 64x128
+//     tile instead runs two groups of four waves that take its stages in turn, where
+//     one tile per workgroup covers the problem.
+//
+// Measured (one MI355X, operands not in L2): 8192 x 8192 x 8192 247-252 us (4.4
+// PFLOP/s), 4096 x 7168 x 16384 222-232 us, 4096 x 4096 x 7168 58-64 us, all on
+// 256x256.  What bounds it: the clock holds 1.9 GHz there with the matrix cores 56 %
+// busy (pure matrix instructions reach 7.8-8.1 PFLOP/s).  Timing copies without the
+// stage copies ran 20 % faster, without the barrier 6 %, without the scales 6 %,
+// without the fragment reads 11 %, without any of them 6.4 PFLOP/s; waiting for fewer
+// copies, or copying from L2 only, changed 1 and 3-8 %: it is the copies' issue beside
+// the matrix work, not their latency.  Tried without gain: only half of the waves
+// copying, more of a stage's copies put off into the next one, a later barrier, raised
+// wave priority, other raster bands, a 256x224 tile.
 #include <algorithm>
 #include <cstdlib>
 
@@ -52,10 +65,6 @@ __device__ __forceinline__ v4f mfma_mxfp4(const v4i& a, uint32_t sa, const v4i& 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, FMT_E2M1, FMT_E2M1, 0, (int)sa, 0, (int)sb);
 }
 
-#ifndef MXBAR
-#define MXBAR(NT) 1
-#define MXLATE(NT, LPS) (NT == 8 ? 2 : NT == 4 ? 4 : 1)
-#endif
 // WM x WN waves of MT x NT blocks of 16 x 16; R ring slots; KG groups of such waves,
 // each with a ring of its own, that take the stages of a tile in turn.
 template <int MT_, int NT_, int WM_, int WN_, int R_, int KG_>
@@ -71,8 +80,11 @@ struct MxTile {
   static constexpr int RA = BM / 8 / NW, RB = BN / 8 / NW;   // 1-KB copies (8 rows) per wave and stage
   static constexpr int LPS = RA + RB + 1;                    // copies per wave and stage, with one of scales
   static constexpr int NSTORE = MT * NT / 2;                 // 16-byte stores of D per lane
-  static constexpr int BAR = MXBAR(NT);   // column blocks ahead of the barrier
-  static constexpr int LATE = MXLATE(NT, LPS);   // copies of a stage issued in the next stage's first K block
+  static constexpr int BAR = 1;                              // column blocks ahead of the barrier
+  // copies of a stage issued in the next stage's first K block, so that they spread over
+  // both: with four column blocks half of them (4096 x 4096 x 7168 on 128x256 75 -> 69
+  // us), with eight two (none and three measured the same, five 3 % slower: they come late)
+  static constexpr int LATE = NT == 8 ? 2 : NT == 4 ? 4 : 1;
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
   static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && MT % 2 == 0)), "tile shape");
 };
@@ -455,8 +467,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   X(1, 4, 4, 2, 4, 3, 1)  \
   X(2, 2, 4, 4, 2, 4, 1)  \
   X(3, 2, 2, 2, 4, 6, 1)  \
-  X(4, 4, 4, 2, 2, 2, 2)  \
-  X(5, 2, 4, 2, 2, 3, 2)
+  X(4, 2, 4, 2, 2, 3, 2)
 
 struct Mxfp4TileInfo {
   int bm, bn, kg;
@@ -486,45 +497,43 @@ static hipError_t launch_mxfp4_tile(const Mxfp4Params& p, int id, int grid, hipS
 
 // ---------------------------------------------------------------------------
 // Few rows (decode): the product streams B once, bound by how much of it is in
-// flight, and by the launch.  A workgroup takes 16 NT columns and all rows of A (MT
-// blocks of 16); its waves split K between them, pair of K blocks by pair (a 128-byte
+// flight, and by the launch.  A workgroup takes 16 columns and all rows of A (MT blocks
+// of 16); its four waves split K between them, pair of K blocks by pair (a 128-byte
 // line of each row), with fragments and scale words loaded straight into registers, P
 // pairs ahead.  The waves' sums meet in LDS, added in wave order, so no second launch
-// and no workspace is needed.
+// and no workspace is needed.  (1 x 4096 x 7168: 6.1 us, 2.7 of them the launch, at 4.6
+// TB/s of B in between; eight waves and 32 columns measured 4-40 % slower.)
 // ---------------------------------------------------------------------------
 extern "C" __device__ int dg_raw_buffer_load_i32_mx(v4i rsrc, int voffset, int soffset,
                                                     int aux) __asm("llvm.amdgcn.raw.buffer.load.i32");
 
-template <int MT, int NT, int NW, int P>
-__global__ void __launch_bounds__(NW * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
-  __shared__ v4f red[NW][NT][64];
+constexpr int MX_SKINNY_WAVES = 4;
+template <int MT, int P>
+__global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
+  constexpr int NW = MX_SKINNY_WAVES;
+  __shared__ v4f red[NW][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lrow = lane & 15, lgrp = lane >> 4, sh = 8 * lgrp;
   const int M = p.m, N = p.n;
   const uint32_t Kh = (uint32_t)p.k >> 1;
   const int KB = p.k >> 7, PAIRS = (KB + 1) >> 1;
-  const int n0 = blockIdx.x * (16 * NT);
+  const int n0 = blockIdx.x * 16;   // (N % 16 == 0: every column is there)
   const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
   const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
   const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
   const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
   // per-lane offsets; a row past the end reads zeros (and its results are not stored)
-  uint32_t a_off[MT], b_off[NT], sa_off[MT], sb_off[NT];
+  uint32_t a_off[MT], sa_off[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = i * 16 + lrow;
     a_off[i] = r < M ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
     sa_off[i] = r < M ? (uint32_t)r * 4u : kBufferOutOfRange;
   }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int r = n0 + i * 16 + lrow;
-    b_off[i] = r < N ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
-    sb_off[i] = r < N ? (uint32_t)r * 4u : kBufferOutOfRange;
-  }
-  v4i af[P][2][MT], bf[P][2][NT];
-  uint32_t sa[P][2][MT], sb[P][2][NT];
+  const uint32_t b_off = (uint32_t)(n0 + lrow) * Kh + (uint32_t)lgrp * 16u, sb_off = (uint32_t)(n0 + lrow) * 4u;
+  v4i af[P][2][MT], bf[P][2];
+  uint32_t sa[P][2][MT], sb[P][2];
   // pair j of this wave (pair j NW + wave of K); K blocks past the end read zeros
   auto load = [&](int j, auto set_tag) {
     constexpr int S = decltype(set_tag)::value;
@@ -534,11 +543,8 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
       const bool in = kb < KB;
       const int ko = in ? kb * 64 : 0;
       const uint32_t none = in ? 0u : kBufferOutOfRange;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        bf[S][h][i] = dg_raw_buffer_load_v4i32(rsB, (int)(b_off[i] | none), ko, 0);
-        sb[S][h][i] = (uint32_t)dg_raw_buffer_load_i32_mx(rsSB, (int)(sb_off[i] | none), in ? kb * N * 4 : 0, 0);
-      }
+      bf[S][h] = dg_raw_buffer_load_v4i32(rsB, (int)(b_off | none), ko, 0);
+      sb[S][h] = (uint32_t)dg_raw_buffer_load_i32_mx(rsSB, (int)(sb_off | none), in ? kb * N * 4 : 0, 0);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         af[S][h][i] = dg_raw_buffer_load_v4i32(rsA, (int)(a_off[i] | none), ko, 0);
@@ -546,11 +552,9 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
       }
     }
   };
-  v4f acc[MT][NT];
+  v4f acc[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < MT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
   const int mine = (PAIRS - wave + NW - 1) / NW;   // (0 for a wave past the last pair)
   static_for<P>([&](auto s) { load(decltype(s)::value, s); });
   for (int j = 0; j < mine; j += P) {
@@ -559,58 +563,44 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_skinny_kernel(Mxfp4Params p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            acc[mt][nt] = mfma_mxfp4(bf[S][h][nt], sb[S][h][nt] >> sh, af[S][h][mt], sa[S][h][mt] >> sh, acc[mt][nt]);
+        for (int mt = 0; mt < MT; ++mt)
+          acc[mt] = mfma_mxfp4(bf[S][h], sb[S][h] >> sh, af[S][h][mt], sa[S][h][mt] >> sh, acc[mt]);
       load(j + P + S, s);
     });
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (mt > 0) __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) red[wave][nt][lane] = acc[mt][nt];
+    red[wave][lane] = acc[mt];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * 64; e += NW * 64) {
-      v4f v = red[0][e >> 6][e & 63];
+    const int row = mt * 16 + lrow;
+    if (wave == 0 && row < M) {
+      v4f v = red[0][lane];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += red[w][e >> 6][e & 63];
-      const int row = mt * 16 + (e & 15), col = n0 + (e >> 6) * 16 + 4 * ((e & 63) >> 4);
-      if (row < M && col < N) {
-        const size_t at = (size_t)row * N + col;
-        if (p.c) {
-          const uint2 cv = *reinterpret_cast<const uint2*>(p.c + at);
-          v[0] += __uint_as_float(cv.x << 16);
-          v[1] += __uint_as_float(cv.x & 0xffff0000u);
-          v[2] += __uint_as_float(cv.y << 16);
-          v[3] += __uint_as_float(cv.y & 0xffff0000u);
-        }
-        *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
+      for (int w = 1; w < NW; ++w) v += red[w][lane];
+      const size_t at = (size_t)row * N + n0 + 4 * lgrp;
+      if (p.c) {
+        const uint2 cv = *reinterpret_cast<const uint2*>(p.c + at);
+        v[0] += __uint_as_float(cv.x << 16);
+        v[1] += __uint_as_float(cv.x & 0xffff0000u);
+        v[2] += __uint_as_float(cv.y << 16);
+        v[3] += __uint_as_float(cv.y & 0xffff0000u);
       }
+      *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
     }
   }
 }
 
-// id, MT, NT, waves, pairs in flight per wave
+// id, MT, pairs in flight per wave
 #define DG_MXFP4_SKINNY(X) \
-  X(0, 1, 1, 8, 4)         \
-  X(1, 2, 1, 8, 4)         \
-  X(2, 4, 1, 8, 2)         \
-  X(3, 8, 1, 8, 1)         \
-  X(4, 1, 2, 8, 4)         \
-  X(5, 2, 2, 8, 2)         \
-  X(6, 4, 2, 8, 2)         \
-  X(7, 8, 2, 8, 1)         \
-  X(8, 1, 1, 16, 2)        \
-  X(9, 4, 1, 16, 1)        \
-  X(10, 1, 1, 4, 4)        \
-  X(11, 4, 1, 4, 2)        \
-  X(12, 4, 2, 4, 2)
+  X(0, 1, 4)               \
+  X(1, 2, 4)               \
+  X(2, 4, 2)
+constexpr int kMxSkinnyIdBase = 100;   // in DG_FORCE_MXFP4
 
 static int skinny_rows(int id) {
   switch (id) {
-#define X(i, MT, NT, NW, P) case i: return MT * 16;
+#define X(i, MT, P) case i: return MT * 16;
     DG_MXFP4_SKINNY(X)
 #undef X
   }
@@ -619,10 +609,9 @@ static int skinny_rows(int id) {
 
 static hipError_t launch_mxfp4_skinny(const Mxfp4Params& p, int id, hipStream_t stream) {
   switch (id) {
-#define X(i, MT, NT, NW, P)                                                                                  \
-  case i:                                                                                                    \
-    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, NT, NW, P>), dim3((p.n + 16 * NT - 1) / (16 * NT)), dim3(NW * 64), 0, \
-                       stream, p);                                                                           \
+#define X(i, MT, P)                                                                                       \
+  case i:                                                                                                 \
+    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, P>), dim3(p.n / 16), dim3(MX_SKINNY_WAVES * 64), 0, stream, p); \
     return hipGetLastError();
     DG_MXFP4_SKINNY(X)
 #undef X
@@ -663,43 +652,44 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
   return pl;
 }
 
-// The tile with the least estimated time: rounds of units, each its stages at the
-// tile's measured pace (microseconds per 256 values of K, all CUs busy: 4096 rows,
-// K = 7168 and 16384) and a fixed share per unit (pipeline fill, D), and for a split
-// the partials' round trip and a second launch.
+// Few rows: the streaming kernel reads all of A once per 16 columns, so it is taken
+// while row blocks x columns stay small (measured against the best tile: 1 x 4096 x 7168
+// 6.1 against 11.8 us, 16 x 7168 x 2048 6.0 / 6.7, 32 x 4096 x 7168 9.9 / 12.0; past the
+// limit 1 x 24576 x 1536 10.7 / 7.6, 32 x 7168 x 16384 30.9 / 19.6).  Otherwise the tile
+// with the least estimated time in microseconds: rounds of units, each its stages at the
+// tile's pace and a fixed share (pipeline fill, D); a split plan's partials' round trip
+// and second launch; and the rate at which the units' CUs stream B.  The constants fit
+// 120 shapes from 1 x 512 x 2048 to 4096 x 24576 x 1536 (geometric mean 1.5 % over the
+// best tile of each).
 static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.80, 1.12, 0.74, 0.52, 0.90, 0.65}, kUnit[] = {3.5, 1.6, 0.8, 0.6, 2.0, 1.5};
+  constexpr double kStage[] = {1.80, 1.12, 0.66, 0.50, 0.60}, kUnit[] = {5.0, 1.6, 0.8, 0.6, 1.4};
+  constexpr double kSplit = 5.5, kPartialRate = 4.0e6, kStreamRate = 40.0e3;   // us, bytes per us
   constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
   int force = -1;
   if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
+  int skinny = -1;
+  const int mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 0;
+  if (mt && (long long)mt * n <= 8192) skinny = mt >> 1;
+  if (force >= 0) skinny = force >= kMxSkinnyIdBase && skinny_rows(force - kMxSkinnyIdBase) >= m ? force - kMxSkinnyIdBase : -1;
   Mxfp4Plan best{};
+  if (skinny >= 0) {
+    best.skinny = skinny;
+    return best;
+  }
   double best_t = 1e30;
   for (int id = 0; id < kTiles; ++id) {
-    if (force >= 0 && force < kTiles && id != force) continue;
-    const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
     const int kg = kMxTiles[id].kg;
+    const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
     if (kg > 1 && pl.units > cus) continue;   // one unit per workgroup
-    const int stages = (pl.kb_per_split + 1) / 2, whole = ((k / 128 + 1) / 2 + kg - 1) / kg;
-    double t;
-    if (pl.splits > 1) {
-      t = (double)(pl.full_tiles / cus) * (whole * kStage[id] + kUnit[id]) + stages * kStage[id] + kUnit[id] + 4.0 +
-          2.0 * (double)pl.ws_bytes / 4.0e6;
-    } else {
-      t = (double)((pl.units + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
-    }
-    if (t < best_t - 1e-9) {
-      best_t = t;
+    const int whole = ((k / 128 + 1) / 2 + kg - 1) / kg;
+    double t = (double)((pl.full_tiles + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
+    if (pl.splits > 1)
+      t += (pl.kb_per_split + 1) / 2 * kStage[id] + kUnit[id] + kSplit + 2.0 * (double)pl.ws_bytes / kPartialRate;
+    t = std::max(t, 0.5 * n * k / (kStreamRate * std::min(pl.units, cus)));
+    if (t < best_t - 1e-9 || id == force) {
+      best_t = id == force ? 0.0 : t;
       best = pl;
     }
-  }
-  // Few rows: where the tiles would be split along K, the streaming kernel needs no
-  // second launch.
-  int sk = -1;
-  if (best.splits > 1 && best.full_tiles == 0) sk = m <= 16 ? 10 : m <= 32 ? 1 : m <= 64 && k <= 8192 ? 11 : -1;
-  if (force >= 0) sk = force >= 100 && skinny_rows(force - 100) >= m ? force - 100 : -1;
-  if (sk >= 0) {
-    best.skinny = sk;
-    best.ws_bytes = 0;
   }
   return best;
 }

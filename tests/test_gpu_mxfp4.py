@@ -168,6 +168,28 @@ def test_gemm_exact_integers(dg, m, n, k):
     check_bit_exact(run_gemm(dg, a, one(m), b, one(n), c), X.mxfp4_gemm_nt(a, one(m), b, one(n), c), "exact")
 
 
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 100, 101, 102])
+def test_gemm_every_kernel(dg, kernel, monkeypatch):
+    """Each tile and each form for few rows pinned, over partial tiles, odd counts of K blocks, a split along K and
+    (where units exceed the workgroups, with the CU cap) several tiles per workgroup; exact integers with C."""
+    monkeypatch.setenv("DG_FORCE_MXFP4", str(kernel))
+    ints = np.array([0, 2, 4, 6, 10, 12], dtype=np.uint8)
+    rows = {100: (1, 16), 101: (17, 32), 102: (33, 64)}.get(kernel, (1, 70, 200, 300))
+    for m in rows:
+        for n, k, cap in ((272, 128, 0), (528, 2176, 0), (400, 1152, 8)):
+            dg.dg_set_num_cus(cap)
+            try:
+                rng = np.random.default_rng(m + n)
+                ca, cb = (ints[rng.integers(0, 6, (r, k))] for r in (m, n))
+                byte = [(127 + rng.integers(0, 2, (r, k // 32))).astype(np.uint8) for r in (m, n)]
+                a, b = X.pack_pairs(ca), X.pack_pairs(cb)
+                sa, sb = (np.ascontiguousarray(X.pack_words(v).T) for v in byte)
+                c = f64_to_bf16_bits(rng.integers(-100, 101, (m, n)).astype(np.float64))
+                check_bit_exact(run_gemm(dg, a, sa, b, sb, c), X.mxfp4_gemm_nt(a, sa, b, sb, c), f"{m} {n} {k}")
+            finally:
+                dg.dg_set_num_cus(0)
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 128, 512), (100, 272, 640), (600, 1040, 768)])
 def test_gemm_every_scale_byte_counts(dg, m, n, k):
     """Codes 1.0 everywhere: D is the sum over 32-blocks of 32 * 2^(ea + eb); a power of two apart from block to
