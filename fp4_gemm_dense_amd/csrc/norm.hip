@@ -28,6 +28,7 @@ struct NormParams {
   float* rstd;
   int m, k;
   float eps;
+  double inv_k;
 };
 
 // A row is spread over a workgroup of 64 .. 1024 threads (whole waves), V vectors of 8
@@ -45,14 +46,15 @@ constexpr int NORM_MAX_K = 32768, NORM_MAX_WAVES = 16;
 
 // Sum of v over the workgroup, in a fixed order; every thread gets it.  One barrier: a
 // caller that sums again passes another buffer.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+template <typename F>
+__device__ __forceinline__ F block_sum(F v, F* red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   const int waves = blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
+  F s = 0;
   for (int w = 0; w < waves; ++w) s += red[w];
   return s;
 }
@@ -63,7 +65,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // in every format, 70-75 us against 73-84.)
 template <int FMT, int V>
 __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormParams p) {
-  __shared__ float red[NORM_MAX_WAVES];
+  __shared__ double red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3, kb_n = p.k >> 7;
   const int row = blockIdx.x;
@@ -97,7 +99,9 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
   }
-  const float r = 1.0f / sqrtf(block_sum(ss, red) / (float)p.k + p.eps);
+  // the sum between threads and r in 64 bits, rounded once: a code near a border follows
+  // y = (h * weight) * r, whose first product is exact (two bf16 values)
+  const float r = (float)(1.0 / sqrt(block_sum((double)ss, red) * p.inv_k + (double)p.eps));
   if (p.rstd && tid == 0) p.rstd[row] = r;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
     uint32_t amax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = y[e] * r * w[e];
+      y[e] = y[e] * w[e] * r;
       amax = umax(amax, abs_bits(y[e]));
     }
     const int kb = j >> 4;
@@ -126,7 +130,8 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
       if constexpr (FMT == DG_QUANT_E4M3_F32) {
         float s = __uint_as_float(amax) / 448.0f;
         s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(s, 0x1p-126f));
-        inv = 1.0f / s;
+        inv = fminf(448.0f / __uint_as_float(amax), 0x1p126f);   // (a NaN scale: the codes are NaN by y)
+        if (amax == 0 || amax >= 0x7f800000u) inv = s;
         if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
       } else {
         // the wave's four blocks make one word (past the end: 2^0)
@@ -314,7 +319,7 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
     if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps};
+    NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const hipError_t e = format == DG_QUANT_E4M3_F32     ? launch_norm<DG_QUANT_E4M3_F32>(p, hs)
                          : format == DG_QUANT_E4M3_UE8M0 ? launch_norm<DG_QUANT_E4M3_UE8M0>(p, hs)
