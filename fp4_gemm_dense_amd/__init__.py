@@ -454,15 +454,18 @@ _X_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
 QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4 = 0, 1, 2
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _call(name, index, *args):
     """The C entry point on device `index` and torch's current stream there.  (A decode step makes many calls of a few
     microseconds: these wrappers read the raw stream and device index, and pass addresses as plain integers.)"""
     f = getattr(_lib or load_library(), name)
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        st = f(*args, _raw_stream(index))
     else:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            st = f(*args, _raw_stream(index))
     if st:
         raise DgError(name, st)
 
@@ -484,9 +487,12 @@ def _arg(t, dtypes, shape, index, name):
     raise ValueError(f"{name}: on device {t.get_device()}, expected {index}")
 
 
+_empty = torch.empty_strided
+
+
 def _new(shape, dtype, dev):
     """A new contiguous 1-D or 2-D tensor (the quickest of torch's constructors)."""
-    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=dev)
+    return _empty(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=dev)
 
 
 _U8S, _I32S, _F32S = (_U8,), (torch.int32,), (torch.float32,)
@@ -515,13 +521,26 @@ def dg_mxfp4_gemm_workspace_bytes(m, n, k, num_cus=0):
     return int(lib().dg_mxfp4_gemm_workspace_bytes(m, n, k, int(num_cus)))
 
 
+def _mxfp4_operands(a, a_sf, b, b_sf):
+    """Checks the operands of an MXFP4 GEMM; returns (m, n, k, device index)."""
+    m, kh = a.shape
+    n, k, index = b.shape[0], 2 * kh, a.get_device()
+    kb = k // 128
+    if not (a.dtype is b.dtype is _U8 and a_sf.dtype is b_sf.dtype is torch.int32 and b.shape == (n, kh)
+            and a_sf.shape == (kb, m) and b_sf.shape == (kb, n) and a.is_contiguous() and a_sf.is_contiguous()
+            and b.is_contiguous() and b_sf.is_contiguous()
+            and 0 <= index == a_sf.get_device() == b.get_device() == b_sf.get_device()):
+        for t, dtypes, shape, name in ((a, _U8S, (m, kh), "a"), (a_sf, _I32S, (kb, m), "a_sf"), (b, _U8S, (n, kh), "b"),
+                                       (b_sf, _I32S, (kb, n), "b_sf")):
+            _arg(t, dtypes, shape, index, name)
+    return m, n, k, index
+
+
 def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
     """d = c + a . b^T, both operands MXFP4: a [M, K/2] uint8, a_sf [K/128, M] int32, b [N, K/2], b_sf [K/128, N].
     workspace: optional uint8 device tensor (allocated here when needed and not given)."""
-    m, kh = a.shape
-    n, k, dev = b.shape[0], 2 * kh, a.get_device()
-    kb = k // 128
-    ap = _arg(a, _U8S, (m, kh), dev, "a")
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    cp, dp = _arg(c, _BF, (m, n), index, "c"), _arg(d, _BF, (m, n), index, "d")
     if workspace is None:
         nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
         if nbytes:
@@ -529,10 +548,9 @@ def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
             wp = workspace.data_ptr()
     else:
         nbytes = workspace.numel()
-        wp = _arg(workspace, _U8S, (nbytes,), dev, "workspace")
-    _call("dg_mxfp4_gemm_nt", dev, ap, _arg(a_sf, _I32S, (kb, m), dev, "a_sf"), _arg(b, _U8S, (n, kh), dev, "b"),
-          _arg(b_sf, _I32S, (kb, n), dev, "b_sf"), _arg(c, _BF, (m, n), dev, "c"), _arg(d, _BF, (m, n), dev, "d"),
-          m, n, k, wp, nbytes)
+        wp = _arg(workspace, _U8S, (nbytes,), index, "workspace")
+    _call("dg_mxfp4_gemm_nt", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), cp, dp, m, n, k, wp,
+          nbytes)
     return d
 
 
@@ -650,10 +668,11 @@ def quantize_mxfp4(x, transposed=False, values=False):
     """MXFP4 of x [m, k] or [G, m, k] (bf16 or fp32): (q, sf), the operand whose products sum over k; with transposed,
     (q, sf, qt, sft), qt and sft the transposed operand, whose products sum over m; with values, also the bf16 values
     that q and sf stand for, as the last item."""
-    G, m, k = _matrix_dims(x)
+    shape = x.shape
+    grouped = len(shape) != 2
+    G, m, k = _matrix_dims(x) if grouped else (1, *shape)
     index, dev = x.get_device(), x.device
-    xp = _arg(x, _X_TYPES, x.shape, index, "x")
-    grouped = x.dim() == 3
+    xp = _arg(x, _X_TYPES, shape, index, "x")
     q, sf = _new((G * m, k // 2), _U8, dev), _new((G * (k // 128), m), torch.int32, dev)
     qt = sft = v = qtp = sftp = vp = None
     if transposed:
@@ -672,7 +691,16 @@ def quantize_mxfp4(x, transposed=False, values=False):
 
 def mxfp4_gemm_nt(a, a_sf, b, b_sf, c=None):
     """Returns a new bf16 tensor d = c + a . b^T, both operands MXFP4."""
-    return dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, _new((a.shape[0], b.shape[0]), torch.bfloat16, a.device))
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    cp, dev = _arg(c, _BF, (m, n), index, "c"), a.device
+    d = _new((m, n), torch.bfloat16, dev)
+    nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
+    if nbytes:
+        ws = _new((nbytes,), _U8, dev)
+        wp = ws.data_ptr()
+    _call("dg_mxfp4_gemm_nt", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), cp, d.data_ptr(), m, n,
+          k, wp, nbytes)
+    return d
 
 
 def add_rms_norm(x, residual, weight, eps=1e-6, quant_format=QUANT_E4M3_F32):

@@ -51,7 +51,7 @@ DeviceInfo current_device_info() {
   return info;
 }
 
-static int effective_cus(const DeviceInfo& di) {
+int effective_cus(const DeviceInfo& di) {
   int cap = g_cu_cap.load();
   if (cap <= 0) {
     const char* env = std::getenv("DG_NUM_CUS");

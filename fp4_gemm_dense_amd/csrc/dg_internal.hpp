@@ -103,6 +103,8 @@ struct DeviceInfo {
   bool ok;
 };
 DeviceInfo current_device_info();
+// CUs a call may use on that device (the cap of dg_set_num_cus / DG_NUM_CUS applied)
+int effective_cus(const DeviceInfo& di);
 
 // Plan for one GEMM call.
 struct GemmPlan {

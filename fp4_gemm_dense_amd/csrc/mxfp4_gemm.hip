@@ -731,8 +731,7 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
     if (!mxfp4_sizes_fit(m, n, k)) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    int cus = dg_get_num_cus();
-    if (cus <= 0) cus = di.num_cus;
+    const int cus = effective_cus(di);
     const Mxfp4Plan pl = plan_mxfp4(m, n, k, cus);
     if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes || misaligned(workspace, 16)))
       return DG_ERR_INVALID_ARG;

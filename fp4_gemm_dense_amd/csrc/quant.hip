@@ -258,8 +258,7 @@ extern "C" int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t*
     if (k % 128 != 0 || (long long)num_groups * m > 0x7fffffffLL || m > 0x7fffffff - 127) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    int cus = dg_get_num_cus();
-    if (cus <= 0) cus = di.num_cus;
+    const int cus = effective_cus(di);
     QuantParams p{x, q, sf, qt, sft, values, num_groups, m, k};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     if (qt) {
