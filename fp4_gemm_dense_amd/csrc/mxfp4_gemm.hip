@@ -86,7 +86,7 @@ struct MxTile {
   // us), with eight two (none and three measured the same, five 3 % slower: they come late)
   static constexpr int LATE = NT == 8 ? 2 : NT == 4 ? 4 : 1;
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
-  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && MT % 2 == 0)), "tile shape");
+  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && NT % 4 == 0)), "tile shape");
 };
 
 // Chunk swizzles of an A and a B row.  A 16-byte LDS read serves lanes {0-3, 12-15,
@@ -387,32 +387,32 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     keep_late();
     static_for<T::LATE>([&](auto i) { issue_late(i); });
 
-    int mt0 = 0, mt1 = MT;   // the row blocks this group stores
+    int np0 = 0, np1 = NT / 2;   // the pairs of column blocks this group stores
     if constexpr (T::KG == 2) {
-      // the groups' sums meet: each hands the other half of its row blocks over in LDS
-      // (one unit per workgroup: the rings are done with)
+      // the groups' sums meet: each hands the other's half of its column blocks over in
+      // LDS (one unit per workgroup: the rings are done with)
       wait_vmcnt<0>();
       wait_lgkmcnt0();
       block_barrier();
-      constexpr int MH = MT / 2;
-      v4f* xch = reinterpret_cast<v4f*>(smem_all) + wave * 64 + lane;   // [group][MH][NT][wave][lane]
+      constexpr int NH = NT / 2;
+      v4f* xch = reinterpret_cast<v4f*>(smem_all) + wave * 64 + lane;   // [group][MT][NH][wave][lane]
 #pragma unroll
-      for (int mt = 0; mt < MH; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          xch[((grp * MH + mt) * NT + nt) * (T::NW * 64)] = grp ? acc[mt][nt] : acc[MH + mt][nt];
+        for (int nt = 0; nt < NH; ++nt)
+          xch[((grp * MT + mt) * NH + nt) * (T::NW * 64)] = grp ? acc[mt][nt] : acc[mt][NH + nt];
       wait_lgkmcnt0();
       block_barrier();
 #pragma unroll
-      for (int mt = 0; mt < MH; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const v4f o = xch[(((1 - grp) * MH + mt) * NT + nt) * (T::NW * 64)];
-          if (grp) acc[MH + mt][nt] += o;
+        for (int nt = 0; nt < NH; ++nt) {
+          const v4f o = xch[(((1 - grp) * MT + mt) * NH + nt) * (T::NW * 64)];
+          if (grp) acc[mt][NH + nt] += o;
           else acc[mt][nt] += o;
         }
-      mt0 = grp * MH;
-      mt1 = mt0 + MH;
+      np0 = grp * (NT / 4);
+      np1 = np0 + NT / 4;
     }
     if (cur.part >= 0) {
       // fp32 partial tile of this slice: ws[part][BM][BN]
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (mt < mt0 || mt >= mt1) continue;
+          if (nt < 2 * np0 || nt >= 2 * np1) continue;
           const int row = wave_m * MT * 16 + mt * 16 + lrow;
           const int col = wave_n * NT * 16 + (nt >> 1) * 32 + lgrp * 8 + (nt & 1) * 4;
           const v4i w = {__float_as_int(acc[mt][nt][0]), __float_as_int(acc[mt][nt][1]),
@@ -433,10 +433,10 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       const v4i rsC = make_buffer_rsrc(p.c, p.c ? (uint32_t)M * (uint32_t)N * 2u : 0u);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        if (mt < mt0 || mt >= mt1) continue;
         const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + lrow;
 #pragma unroll
         for (int np = 0; np < NT / 2; ++np) {
+          if (np < np0 || np >= np1) continue;
           const int col = cur.n0 + wave_n * NT * 16 + np * 32 + lgrp * 8;
           const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u : kBufferOutOfRange;
           v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   X(1, 4, 4, 2, 4, 3, 1)  \
   X(2, 2, 4, 4, 2, 4, 1)  \
   X(3, 2, 2, 2, 4, 6, 1)  \
-  X(4, 2, 4, 2, 2, 3, 2)
+  X(4, 2, 4, 2, 2, 3, 2)  \
+  X(5, 3, 4, 2, 2, 2, 2)
 
 struct Mxfp4TileInfo {
   int bm, bn, kg;
@@ -662,7 +663,7 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
 // 120 shapes from 1 x 512 x 2048 to 4096 x 24576 x 1536 (geometric mean 1.5 % over the
 // best tile of each).
 static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.80, 1.12, 0.66, 0.50, 0.60}, kUnit[] = {5.0, 1.6, 0.8, 0.6, 1.4};
+  constexpr double kStage[] = {1.80, 1.12, 0.66, 0.50, 0.60, 0.85}, kUnit[] = {5.0, 1.6, 0.8, 0.6, 1.4, 1.7};
   constexpr double kSplit = 5.5, kPartialRate = 4.0e6, kStreamRate = 40.0e3;   // us, bytes per us
   constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
   int force = -1;

@@ -168,7 +168,7 @@ def test_gemm_exact_integers(dg, m, n, k):
     check_bit_exact(run_gemm(dg, a, one(m), b, one(n), c), X.mxfp4_gemm_nt(a, one(m), b, one(n), c), "exact")
 
 
-@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 100, 101, 102])
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 100, 101, 102])
 def test_gemm_every_kernel(dg, kernel, monkeypatch):
     """Each tile and each form for few rows pinned, over partial tiles, odd counts of K blocks, a split along K and
     (where units exceed the workgroups, with the CU cap) several tiles per workgroup; exact integers with C."""
