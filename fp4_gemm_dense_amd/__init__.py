@@ -450,7 +450,7 @@ def dg_fp8_fp4_expert_ffn(x, x_sf, topk_idx, topk_w, w1, w1_sf, w2, w2_sf, y, ex
 
 
 # dg_dtype and dg_quant_format (include/dg.h)
-_X_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
+_X_TYPES = {**{t: 0 for t in _BF}, torch.float32: 1}
 QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4 = 0, 1, 2
 
 

@@ -61,7 +61,7 @@ int effective_cus(const DeviceInfo& di) {
   return di.num_cus;
 }
 
-static bool log_enabled() {
+bool log_enabled() {
   const char* env = std::getenv("DG_LOG");
   return env && env[0] == '1';
 }

@@ -37,6 +37,7 @@
 // copying, more of a stage's copies put off into the next one, a later barrier, raised
 // wave priority, other raster bands, a 256x224 tile.
 #include <algorithm>
+#include <cstdio>
 #include <cstdlib>
 
 #include "../../include/dg.h"
@@ -83,8 +84,8 @@ struct MxTile {
   static constexpr int BAR = 1;                              // column blocks ahead of the barrier
   // copies of a stage issued in the next stage's first K block, so that they spread over
   // both: with four column blocks half of them (4096 x 4096 x 7168 on 128x256 75 -> 69
-  // us), with eight two (none and three measured the same, five 3 % slower: they come late)
-  static constexpr int LATE = NT == 8 ? 2 : NT == 4 ? 4 : 1;
+  // us), with eight, or a ring of two slots, two (more come late: 3 % slower)
+  static constexpr int LATE = NT == 8 || (KG == 2 && R == 2) ? 2 : NT == 4 ? 4 : 1;
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
   static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && NT % 4 == 0)), "tile shape");
 };
@@ -738,6 +739,14 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
       return DG_ERR_INVALID_ARG;
     Mxfp4Params p{a, a_sf, b, b_sf, c, d, static_cast<float*>(workspace), m, n, k,
                   pl.tiles_m, pl.tiles_n, 8, pl.splits, pl.kb_per_split, pl.full_tiles, pl.units};
+    if (log_enabled()) {
+      if (pl.skinny >= 0)
+        std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> streaming kernel, %d rows\n", m, n, k, skinny_rows(pl.skinny));
+      else
+        std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> tile %dx%d, %d tiles (%d whole, the rest x %d K slices), "
+                     "%d workgroups, workspace %zu bytes\n", m, n, k, kMxTiles[pl.tile].bm, kMxTiles[pl.tile].bn,
+                     pl.tiles_m * pl.tiles_n, pl.full_tiles, pl.splits, pl.grid, pl.ws_bytes);
+    }
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = pl.skinny >= 0 ? launch_mxfp4_skinny(p, pl.skinny, hs) : launch_mxfp4_tile(p, pl.tile, pl.grid, hs);
     if (e == hipSuccess && pl.ws_bytes) {

@@ -230,6 +230,15 @@ def test_gemm_extreme_exponents(dg):
     assert np.isposinf(got).all()
 
 
+def test_gemm_results_below_fp32_normals_are_zero(dg):
+    """The matrix cores flush sums below 2^-126; just above it they are exact."""
+    one = np.full((20, 128), 0x22, np.uint8)
+    sf = lambda r, e: np.ascontiguousarray(X.pack_words(np.full((r, 8), 127 + e, np.uint8)).T)      # noqa: E731
+    for ea, eb, want in ((-60, -74, 2.0 ** -126), (-60, -90, 0.0), (-127, -127, 0.0)):               # 256 * 2^(ea + eb)
+        got = bf16_bits_to_f64(run_gemm(dg, one, sf(20, ea), one[:16], sf(16, eb)))
+        assert (got == want).all(), (ea, eb, got[0, 0])
+
+
 def test_gemm_in_place_c(dg):
     rng = np.random.default_rng(4)
     for m, n, k in ((5, 256, 1024), (300, 528, 512)):
@@ -242,8 +251,12 @@ def test_gemm_in_place_c(dg):
         assert torch.equal(c, want)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 7168), (64, 2112, 7168), (200, 4096, 2048), (512, 512, 8192)])
-def test_gemm_repeats_bit_for_bit_and_graph_replays(dg, m, n, k):
+@pytest.mark.parametrize("m,n,k,kernel", [(1, 4096, 7168, None), (64, 2112, 7168, None), (200, 4096, 2048, None),
+                                          (512, 512, 8192, "2"), (300, 7168, 16384, "3")])
+def test_gemm_repeats_bit_for_bit_and_graph_replays(dg, m, n, k, kernel, monkeypatch):
+    if kernel:                                            # a tile that splits along K at this size
+        monkeypatch.setenv("DG_FORCE_MXFP4", kernel)
+        assert kernel == "3" or dg.dg_mxfp4_gemm_workspace_bytes(m, n, k) > 0
     rng = np.random.default_rng(9)
     t = [torch.from_numpy(v).cuda() for v in rand_mx(rng, m, k) + rand_mx(rng, n, k)]
     want = dg.mxfp4_gemm_nt(*t)
@@ -268,11 +281,11 @@ def test_gemm_repeats_bit_for_bit_and_graph_replays(dg, m, n, k):
         assert torch.equal(d, want), f"replay {i}"
 
 
-def test_gemm_refuses_a_small_workspace(dg):
+def test_gemm_refuses_a_small_workspace(dg, monkeypatch):
+    monkeypatch.setenv("DG_FORCE_MXFP4", "2")             # 16 tiles of 128x128, split along K
     m, n, k = 512, 512, 8192
     need = dg.dg_mxfp4_gemm_workspace_bytes(m, n, k)
-    if need == 0:
-        pytest.skip("no split at this size")
+    assert need > 0
     t = [torch.from_numpy(v).cuda() for v in rand_mx(np.random.default_rng(0), m, k) + rand_mx(np.random.default_rng(1), n, k)]
     d = sentinel_like((m, n)).view(torch.bfloat16)
     with pytest.raises(dg.DgError):

@@ -315,3 +315,41 @@ def test_a_block_of_calls_and_its_graph(dg):
         torch.cuda.synchronize()
         for a, b in zip(out, block()):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), f"replay {i}"
+
+
+def test_training_step_of_norm_and_layer(dg):
+    """h = x + residual, y = q(norm(h)) . q(w)^T and back: the layer's input gradient dn = q(dy) . qt(w)^T feeds the
+    norm's backward pass with the residual branch's gradient; each step against the oracle on the step's own inputs."""
+    T, K, N = 90, 384, 256
+    x, res, wn = bf(80, T, K), bf(81, T, K), f64_to_bf16_bits(1 + 0.3 * np.random.default_rng(82).standard_normal(K))
+    w, dy, dh = bf(83, N, K), bf(84, T, N), bf(85, T, K)
+    q, sf, h, rstd = dg.add_rms_norm(dev(x), dev(res), dev(wn), 1e-6, dg.QUANT_MXFP4)
+    wq, wsf, wqt, wsft = dg.quantize_mxfp4(dev(w), transposed=True)
+    y = dg.mxfp4_gemm_nt(q, sf, wq, wsf)
+    dyq, dysf = dg.quantize_mxfp4(dev(dy))
+    dn = dg.mxfp4_gemm_nt(dyq, dysf, wqt, wsft)
+    dx, dw = dg.add_rms_norm_backward(dn, dev(dh), h, dev(wn), rstd)
+    n_ = lambda t: t.cpu().numpy()                                                      # noqa: E731
+    for got, a, asf, b, bsf, k in ((y, q, sf, wq, wsf, K), (dn, dyq, dysf, wqt, wsft, N)):
+        a_, b_ = X.dequant_mxfp4(n_(a), n_(asf)), X.dequant_mxfp4(n_(b), n_(bsf))
+        ref, s = a_ @ b_.T, np.abs(a_) @ np.abs(b_).T
+        assert (np.abs(bf16_bits_to_f64(bits(got)) - ref) <= 2.0 ** -8 * np.abs(ref) + (k / 8 + 1) * 2.0 ** -22 * s).all()
+    check_back((bits(dx), n_(dw).astype(np.float64)), bits(dn), dh, bits(h), wn, n_(rstd))
+
+
+def test_two_calls_at_once_on_two_streams(dg):
+    """Backward passes in flight together, each with a workspace of its own, and forward passes between them."""
+    a = [back_inputs(500, 1024, True, seed=s) for s in (1, 2)]
+    t = [[dev(v) for v in i[:4]] + [torch.from_numpy(i[4]).cuda()] for i in a]
+    want = [dg.add_rms_norm_backward(*i) for i in t]
+    fwd = [dg.add_rms_norm(i[2], i[0], i[3]) for i in t]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, dg.add_rms_norm_backward(*t[i]), dg.add_rms_norm(t[i][2], t[i][0], t[i][3])))
+    torch.cuda.synchronize()
+    for i, b, f in got:
+        assert torch.equal(b[0], want[i][0]) and torch.equal(b[1], want[i][1])
+        assert all(torch.equal(u, v) for u, v in zip(f, fwd[i]))
