@@ -51,7 +51,7 @@ DeviceInfo current_device_info() {
   return info;
 }
 
-int effective_cus(const DeviceInfo& di) {
+static int effective_cus(const DeviceInfo& di) {
   int cap = g_cu_cap.load();
   if (cap <= 0) {
     const char* env = std::getenv("DG_NUM_CUS");
@@ -61,7 +61,7 @@ int effective_cus(const DeviceInfo& di) {
   return di.num_cus;
 }
 
-bool log_enabled() {
+static bool log_enabled() {
   const char* env = std::getenv("DG_LOG");
   return env && env[0] == '1';
 }

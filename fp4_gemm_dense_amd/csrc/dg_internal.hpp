@@ -103,10 +103,6 @@ struct DeviceInfo {
   bool ok;
 };
 DeviceInfo current_device_info();
-// CUs a call may use on that device (the cap of dg_set_num_cus / DG_NUM_CUS applied)
-int effective_cus(const DeviceInfo& di);
-// DG_LOG=1: print each GEMM call's plan
-bool log_enabled();
 
 // Plan for one GEMM call.
 struct GemmPlan {

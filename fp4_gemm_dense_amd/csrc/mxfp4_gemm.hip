@@ -27,15 +27,20 @@
 //     one tile per workgroup covers the problem.
 //
 // Measured (one MI355X, operands not in L2): 8192 x 8192 x 8192 247-252 us (4.4
-// PFLOP/s), 4096 x 7168 x 16384 222-232 us, 4096 x 4096 x 7168 58-64 us, all on
-// 256x256.  What bounds it: the clock holds 1.9 GHz there with the matrix cores 56 %
-// busy (pure matrix instructions reach 7.8-8.1 PFLOP/s).  Timing copies without the
-// stage copies ran 20 % faster, without the barrier 6 %, without the scales 6 %,
-// without the fragment reads 11 %, without any of them 6.4 PFLOP/s; waiting for fewer
-// copies, or copying from L2 only, changed 1 and 3-8 %: it is the copies' issue beside
-// the matrix work, not their latency.  Tried without gain: only half of the waves
-// copying, more of a stage's copies put off into the next one, a later barrier, raised
-// wave priority, other raster bands, a 256x224 tile.
+// PFLOP/s), 4096 x 7168 x 16384 222-238 us, 4096 x 4096 x 7168 58-65 us, all on
+// 256x256; 1111 x 2112 x 7168 20 us on 96x128; 200 x 4096 x 7168 12.6 us.  What bounds
+// the large ones is power: on random codes the clock holds 1.8-1.9 GHz with the matrix
+// cores 56-61 % busy, and the same call on zeros runs at 2.4 GHz (4096 x 7168 x 16384
+// 178 us; matrix instructions alone reach 6.8 PFLOP/s on random codes and 9.6 on
+// zeros).  Timing copies without the stage copies ran 20 % faster, without the barrier
+// 6 %, without the scales 6 %, without the fragment reads 11 %, without any of them 6.4
+// PFLOP/s; waiting for fewer copies, or copying from L2 only, changed 1 and 3-8 %.  The
+// middle sizes (one 96x128 tile per workgroup) wait for copies: from L2 only they ran 12
+// % faster.  Tried without gain: four waves of 128x128 each (fewer LDS reads per matrix
+// instruction, but the accumulators take half of the registers and the rest spills:
+// 3-8 % slower), only half of the waves copying, more of a stage's copies put off into
+// the next one, loads that pull the next stage into L2, a later barrier, raised wave
+// priority, other raster bands, a 256x224 tile.
 #include <algorithm>
 #include <cstdio>
 #include <cstdlib>
@@ -503,8 +508,8 @@ static hipError_t launch_mxfp4_tile(const Mxfp4Params& p, int id, int grid, hipS
 // of 16); its four waves split K between them, pair of K blocks by pair (a 128-byte
 // line of each row), with fragments and scale words loaded straight into registers, P
 // pairs ahead.  The waves' sums meet in LDS, added in wave order, so no second launch
-// and no workspace is needed.  (1 x 4096 x 7168: 6.1 us, 2.7 of them the launch, at 4.6
-// TB/s of B in between; eight waves and 32 columns measured 4-40 % slower.)
+// and no workspace is needed.  (1 x 4096 x 7168: 5.9 us, 2.7 of them the launch, at 4.9
+// TB/s of B in between; 32 x 4096 x 7168 8.3 us; eight waves and 32 columns measured 4-40 % slower.)
 // ---------------------------------------------------------------------------
 extern "C" __device__ int dg_raw_buffer_load_i32_mx(v4i rsrc, int voffset, int soffset,
                                                     int aux) __asm("llvm.amdgcn.raw.buffer.load.i32");
@@ -733,13 +738,13 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
     if (!mxfp4_sizes_fit(m, n, k)) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    const int cus = effective_cus(di);
+    const int cus = dg_get_num_cus();
     const Mxfp4Plan pl = plan_mxfp4(m, n, k, cus);
     if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes || misaligned(workspace, 16)))
       return DG_ERR_INVALID_ARG;
     Mxfp4Params p{a, a_sf, b, b_sf, c, d, static_cast<float*>(workspace), m, n, k,
                   pl.tiles_m, pl.tiles_n, 8, pl.splits, pl.kb_per_split, pl.full_tiles, pl.units};
-    if (log_enabled()) {
+    if (const char* log = std::getenv("DG_LOG"); log && log[0] == '1') {
       if (pl.skinny >= 0)
         std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> streaming kernel, %d rows\n", m, n, k, skinny_rows(pl.skinny));
       else

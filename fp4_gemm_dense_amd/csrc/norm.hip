@@ -8,7 +8,10 @@
 // Backward, with n = h * r and g = dy * weight: dx = dh + r (g - n mean(g n)),
 // dweight = sum over rows of dy * n.
 //
-// Bound: HBM (forward 7 bytes per element with a residual, backward 8).
+// Bound: HBM (forward 7 bytes per element with a residual, backward 8).  Measured (one
+// MI355X, inputs not in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168
+// 71 us MXFP4, 74 UE8M0, 77 fp32 scales (5.4-5.6 TB/s), 3 x 7168 3.9 us, of which the
+// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 5.8 us (two launches).
 #include <algorithm>
 #include <cmath>
 
