@@ -82,7 +82,7 @@ struct MxTile {
   // whole 1-KB copies
   static constexpr int NSA = (BM * 8 + 1023) / 1024, NSB = (BN * 8 + 1023) / 1024;
   static constexpr int OFF_B = BM * 128, OFF_SA = OFF_B + BN * 128, OFF_SB = OFF_SA + NSA * 1024;
-  static constexpr int STAGE = OFF_SB + NSB * 1024, RING = R * STAGE, LDS = KG * RING;
+  static constexpr int STAGE = OFF_SB + NSB * 1024, RING = R * STAGE;
   static constexpr int RA = BM / 8 / NW, RB = BN / 8 / NW;   // 1-KB copies (8 rows) per wave and stage
   static constexpr int LPS = RA + RB + 1;                    // copies per wave and stage, with one of scales
   static constexpr int NSTORE = MT * NT / 2;                 // 16-byte stores of D per lane
@@ -91,6 +91,13 @@ struct MxTile {
   // both: with four column blocks half of them (4096 x 4096 x 7168 on 128x256 75 -> 69
   // us), with eight, or a ring of two slots, two (more come late: 3 % slower)
   static constexpr int LATE = NT == 8 || (KG == 2 && R == 2) ? 2 : NT == 4 ? 4 : 1;
+  // One instance of the stage's code for a unit's first stage and the others, or two (the
+  // first one's sums start from a constant).  With two the 256x256 tile runs out of
+  // registers: 24 a lane go to memory as it starts (4001 x 4096 x 7168 63.3 us, 60.7 with
+  // one).  The smaller tiles have room for both (200 x 4096 x 7168 13.4 us with one, 12.3
+  // with two).
+  static constexpr bool ONE = MT * NT == 32;
+  static constexpr int LDS = KG * RING + (ONE ? 1024 : 0);   // and 1 KB that is written and not read
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
   static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && NT % 4 == 0)), "tile shape");
 };
@@ -108,6 +115,20 @@ __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) & 1) | ((r >> 2) 
 __device__ __forceinline__ int opaque(int x) {
   asm volatile("" : "+v"(x));
   return x;
+}
+
+// Waits until at most MORE (where first is set) or LESS vector-memory operations are in
+// flight.  One asm block: a branch of the compiler's own would split the matrix
+// instructions around it.
+template <int LESS, int MORE>
+__device__ __forceinline__ void wait_vmcnt_first(int first) {
+  static_assert(LESS <= MORE && MORE < 64, "vmcnt");
+  asm volatile(
+      "s_cmp_lg_u32 %0, 0\n\t"
+      "s_cbranch_scc1 .Lmore%=\n\t"
+      "s_waitcnt vmcnt(%1)\n"
+      ".Lmore%=:\n\t"
+      "s_waitcnt vmcnt(%2)" ::"s"(first), "n"(LESS), "n"(MORE) : "memory", "scc");
 }
 
 template <typename T>
@@ -128,6 +149,11 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   int vb = blockIdx.x;
   if ((G & 7) == 0) vb = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
   if (vb >= p.units) return;
+
+  // the lane, for terms formed where they are used
+  auto lane_here = [&]() -> int {
+    return opaque(T::ONE ? (int)__builtin_amdgcn_mbcnt_hi(-1, __builtin_amdgcn_mbcnt_lo(-1, 0)) : lane);
+  };
 
   struct Unit {
     int m0, n0, kb0, nkb, part;
@@ -184,7 +210,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     c_kb = w.kb0 + 2 * grp;
     c_nkb = w.nkb;
     cs = 0;
-    const int ln = opaque(lane);
+    const int ln = lane_here();
 #pragma unroll
     for (int j = 0; j < T::RA; ++j)
       off[j] = (uint32_t)(w.m0 + (wave * T::RA + j) * 8 + (ln >> 3)) * Kh + chunk_a(ln, j);
@@ -197,40 +223,51 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   // the cursor's stage is a unit's last and has one K block only: its second one is
   // out of range (the offsets are formed anew for the next unit)
   auto cursor_odd_end = [&]() {
-    const int ln = opaque(lane);
+    const int ln = lane_here();
 #pragma unroll
     for (int j = 0; j < T::RA; ++j) off[j] |= (chunk_a(ln, j) & 64u) << 25;
 #pragma unroll
     for (int j = 0; j < T::RB; ++j) off[T::RA + j] |= (chunk_b(ln, j) & 64u) << 25;
     off[T::RA + T::RB] = scale_offset(ln, c_m0, c_n0, true);
   };
-  // copy idx of a stage: per-lane offset o, first K block kb, slot
-  auto issue_at = [&](auto idx_tag, uint32_t o, int kb, uint32_t slot) {
+  // copy idx of a stage: where to in the slot's LDS; per-lane offset o, first K block kb
+  auto dst_of = [&](auto idx_tag, uint32_t slot) -> uint32_t {
+    constexpr int idx = decltype(idx_tag)::value;
+    if constexpr (idx < T::RA) return slot + (wave * T::RA + idx) * 1024;
+    else if constexpr (idx < T::RA + T::RB) return slot + T::OFF_B + (wave * T::RB + idx - T::RA) * 1024;
+    else return slot + s_dst;
+  };
+  auto issue_at = [&](auto idx_tag, uint32_t o, int kb, uint32_t dst) {
     constexpr int idx = decltype(idx_tag)::value;
     if constexpr (idx < T::RA) {
-      buf16_to_lds(rsA, o, (uint32_t)kb * 64u, smem + slot + (wave * T::RA + idx) * 1024);
+      buf16_to_lds(rsA, o, (uint32_t)kb * 64u, smem + dst);
     } else if constexpr (idx < T::RA + T::RB) {
-      buf16_to_lds(rsB, o, (uint32_t)kb * 64u, smem + slot + T::OFF_B + (wave * T::RB + idx - T::RA) * 1024);
+      buf16_to_lds(rsB, o, (uint32_t)kb * 64u, smem + dst);
     } else {
       // (the K block in the lane's offset: a lane's last words may lie past the end, and
       // the range check of each then needs no scalar offset)
-      buf16_to_lds(rsS, o == kBufferOutOfRange ? o : o + (uint32_t)kb * s_stride, 0u, smem + slot + s_dst);
+      buf16_to_lds(rsS, o == kBufferOutOfRange ? o : o + (uint32_t)kb * s_stride, 0u, smem + dst);
     }
   };
   // copy idx of the cursor's stage
-  auto issue = [&](auto idx_tag) { issue_at(idx_tag, off[decltype(idx_tag)::value], c_kb, slot_w); };
-  // the last LATE copies of a stage are issued in the next one, from these
-  uint32_t late_off[T::LATE > 0 ? T::LATE : 1], late_slot = 0;
+  auto issue = [&](auto idx_tag) { issue_at(idx_tag, off[decltype(idx_tag)::value], c_kb, dst_of(idx_tag, slot_w)); };
+  // The last LATE copies of a stage are issued in the next one, from these.  A unit's
+  // last stage issues them itself, ahead of the stores, so the next unit's first stage
+  // has none: where it is no instance of its own, it copies zeros to where nothing is
+  // read.
+  uint32_t late_off[T::LATE], late_dst[T::LATE];
   int late_kb = 0;
-  auto keep_late = [&]() {
-#pragma unroll
-    for (int i = 0; i < T::LATE; ++i) late_off[i] = off[T::LPS - T::LATE + i];
-    late_kb = c_kb;
-    late_slot = slot_w;
+  auto keep_late = [&](int first) {
+    static_for<T::LATE>([&](auto i) {
+      using Idx = std::integral_constant<int, T::LPS - T::LATE + decltype(i)::value>;
+      late_off[decltype(i)::value] = first ? kBufferOutOfRange : off[Idx::value];
+      late_dst[decltype(i)::value] = first ? (uint32_t)(T::KG * T::RING - grp * T::RING) : dst_of(Idx{}, slot_w);
+    });
+    late_kb = first ? 0 : c_kb;
   };
   auto issue_late = [&](auto i_tag) {
     constexpr int i = decltype(i_tag)::value;
-    issue_at(std::integral_constant<int, T::LPS - T::LATE + i>{}, late_off[i], late_kb, late_slot);
+    issue_at(std::integral_constant<int, T::LPS - T::LATE + i>{}, late_off[i], late_kb, late_dst[i]);
   };
   // nothing more to copy: out of range from here on (the instructions still count), with
   // a scalar offset of 0, so that the range check sees the lane's offset alone
@@ -315,11 +352,11 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   static_for<NT>([&](auto nt) { read_b(0u, I0{}, nt); });
 
   v4f acc[MT][NT];
-  // One stage.  FIRST: the first of a unit (the stage before has no late copies left);
-  // STORES: the unit before stored D after the copies of the stage waited for here.
-  auto stage = [&](auto first_tag, auto stores_tag) {
-    constexpr bool FIRST = decltype(first_tag)::value, STORES = decltype(stores_tag)::value;
-    if constexpr (!FIRST) keep_late();
+  // One stage.  The first of a unit (FIRST in an instance of its own, first otherwise):
+  // the unit before stored D after the copies of the stage waited for here.
+  auto stage = [&](auto first_tag, int first) {
+    constexpr bool FIRST = decltype(first_tag)::value;
+    if constexpr (!FIRST) keep_late(first);
     advance();   // (ahead of the matrix instructions: its branch must not split them)
     const uint32_t nx = rd + T::STAGE == T::RING ? 0u : rd + T::STAGE;
     // first K block: read the second one's fragments
@@ -336,9 +373,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if constexpr (nt < MT) read_a(rd, I1{}, nt_tag);
       if constexpr (nt == NT - 1 && MT > NT)
         static_for<(MT > NT ? MT - NT : 0)>([&](auto e) { read_a(rd, I1{}, std::integral_constant<int, NT + decltype(e)::value>{}); });
-      if constexpr (!FIRST) {
-        if constexpr (nt < T::LATE) issue_late(nt_tag);
-      }
+      if constexpr (!FIRST && nt < T::LATE) issue_late(nt_tag);
       __builtin_amdgcn_sched_barrier(0);
     });
     // second K block: after BAR column blocks the barrier, then the next stage's
@@ -354,7 +389,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       if constexpr (nt == T::BAR - 1) {
         __builtin_amdgcn_sched_barrier(0);
         wait_lgkmcnt0();
-        wait_vmcnt<(R - 2) * T::LPS + (STORES ? T::NSTORE : 0)>();
+        constexpr int more = (R - 2) * T::LPS, stores = T::KG == 1 ? T::NSTORE : 0;
+        if constexpr (T::ONE) wait_vmcnt_first<more, more + T::LATE + stores>(first);
+        else wait_vmcnt<more + (FIRST ? stores : 0)>();
         block_barrier();
         read_sa(nx, I0{});
         static_for<T::BAR>([&](auto e) {
@@ -386,11 +423,21 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
 
     const int S = ((cur.nkb + 1) / 2 + T::KG - 1) / T::KG;   // stages of this group
-    stage(std::true_type{}, std::integral_constant<bool, T::KG == 1>{});
+    int s = 0, first = 1;
+    if constexpr (T::ONE) {
+      asm volatile("" : "+s"(first));   // (the first stage is not peeled off the loop)
+    } else {
+      stage(std::true_type{}, 0);
+      s = 1;
+      first = 0;
+    }
 #pragma clang loop unroll(disable)
-    for (int s = 1; s < S; ++s) stage(std::false_type{}, std::false_type{});
+    for (; s < S; ++s) {
+      stage(std::false_type{}, first);
+      first = 0;
+    }
     // (the last stage's late copies go out ahead of the stores)
-    keep_late();
+    keep_late(0);
     static_for<T::LATE>([&](auto i) { issue_late(i); });
 
     int np0 = 0, np1 = NT / 2;   // the pairs of column blocks this group stores
@@ -420,30 +467,30 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       np0 = grp * (NT / 4);
       np1 = np0 + NT / 4;
     }
+    const int ln = T::ONE ? lane_here() : lane;
     if (cur.part >= 0) {
       // fp32 partial tile of this slice: ws[part][BM][BN]
       const v4i rsW = make_buffer_rsrc(p.ws + (size_t)cur.part * (T::BM * T::BN), (uint32_t)(T::BM * T::BN * 4));
+      const int at = ((wave_m * MT * 16 + (ln & 15)) * T::BN + wave_n * NT * 16 + (ln >> 4) * 8) * 4;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (nt < 2 * np0 || nt >= 2 * np1) continue;
-          const int row = wave_m * MT * 16 + mt * 16 + lrow;
-          const int col = wave_n * NT * 16 + (nt >> 1) * 32 + lgrp * 8 + (nt & 1) * 4;
           const v4i w = {__float_as_int(acc[mt][nt][0]), __float_as_int(acc[mt][nt][1]),
                          __float_as_int(acc[mt][nt][2]), __float_as_int(acc[mt][nt][3])};
-          dg_raw_buffer_store_v4i32(w, rsW, (int)((uint32_t)(row * T::BN + col) * 4u), 0, 0);
+          dg_raw_buffer_store_v4i32(w, rsW, at, (mt * 16 * T::BN + (nt >> 1) * 32 + (nt & 1) * 4) * 4, 0);
         }
     } else {
       const v4i rsD = make_buffer_rsrc(p.d, (uint32_t)M * (uint32_t)N * 2u);
       const v4i rsC = make_buffer_rsrc(p.c, p.c ? (uint32_t)M * (uint32_t)N * 2u : 0u);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + lrow;
+        const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + (ln & 15);
 #pragma unroll
         for (int np = 0; np < NT / 2; ++np) {
           if (np < np0 || np >= np1) continue;
-          const int col = cur.n0 + wave_n * NT * 16 + np * 32 + lgrp * 8;
+          const int col = cur.n0 + wave_n * NT * 16 + np * 32 + (ln >> 4) * 8;
           const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u : kBufferOutOfRange;
           v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
           if (p.c) {
