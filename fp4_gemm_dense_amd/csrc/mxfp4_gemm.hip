@@ -131,6 +131,14 @@ __device__ __forceinline__ void wait_vmcnt_first(int first) {
       "s_waitcnt vmcnt(%2)" ::"s"(first), "n"(LESS), "n"(MORE) : "memory", "scc");
 }
 
+// The arguments, all read here: left to where each is first used, the reads wait for one
+// another (96 x 24576 x 1536 9.2 us, 9.0 with them together).
+__device__ __forceinline__ void read_arguments(const Mxfp4Params& p) {
+  asm volatile("" ::"s"(p.a), "s"(p.a_sf), "s"(p.b), "s"(p.b_sf), "s"(p.c), "s"(p.d), "s"(p.ws), "s"(p.m), "s"(p.n), "s"(p.k),
+               "s"(p.tiles_m), "s"(p.tiles_n), "s"(p.group_m), "s"(p.splits), "s"(p.kb_per_split), "s"(p.full_tiles),
+               "s"(p.units));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p) {
   constexpr int MT = T::MT, NT = T::NT, R = T::R;
@@ -146,8 +154,11 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   const int KB = p.k >> 7;
 
   const int G = gridDim.x;
-  int vb = blockIdx.x;
-  if ((G & 7) == 0) vb = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
+  read_arguments(p);
+  // Workgroups go round the eight XCDs: one XCD's take units side by side, whose A and B
+  // rows its L2 then holds once.
+  const int xcd = blockIdx.x & 7;
+  const int vb = xcd * (G >> 3) + min(xcd, G & 7) + (int)(blockIdx.x >> 3);
   if (vb >= p.units) return;
 
   // the lane, for terms formed where they are used
@@ -713,11 +724,11 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
 // with the least estimated time in microseconds: rounds of units, each its stages at the
 // tile's pace and a fixed share (pipeline fill, D); a split plan's partials' round trip
 // and second launch; and the rate at which the units' CUs stream B.  The constants fit
-// 120 shapes from 1 x 512 x 2048 to 4096 x 24576 x 1536 (geometric mean 1.5 % over the
-// best tile of each).
+// 247 shapes, M 1 to 8192, 512 x 2048 to 32768 x 512 and 7168 x 16384 (geometric mean
+// 0.4 % over the best tile of each; worst 128 x 7168 x 16384, 33 %).
 static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.80, 1.12, 0.66, 0.50, 0.60, 0.85}, kUnit[] = {5.0, 1.6, 0.8, 0.6, 1.4, 1.7};
-  constexpr double kSplit = 5.5, kPartialRate = 4.0e6, kStreamRate = 40.0e3;   // us, bytes per us
+  constexpr double kStage[] = {1.75, 1.17, 0.76, 0.64, 0.60, 0.81}, kUnit[] = {4.6, 2.0, 1.0, 1.0, 1.9, 1.9};
+  constexpr double kSplit = 5.5, kPartialRate = 3.4e6, kStreamRate = 40.0e3;   // us, bytes per us
   constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
   int force = -1;
   if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
