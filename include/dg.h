@@ -446,8 +446,8 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *                        unused bytes of the last word): A of the _ue8m0 forms, x of the FFN
  *   DG_QUANT_MXFP4       q [m, k/2], sf [k/128, m] int32 as dg_quantize_mxfp4: A of dg_mxfp4_gemm_nt
  * A block of y with a NaN or an infinity gets a NaN scale; its codes are NaN (e4m3)
- * or 0 (E2M1).  Squares are summed in fp32: a row whose sum of squares passes
- * fp32's range gives r = 0.
+ * or 0 (E2M1).  Squares are formed and first added in fp32: a row whose squares pass
+ * its range gives r = 0.
  *   x, residual [m, k]  bf16; weight [k] bf16
  *   h           [m, k]  bf16 output, or NULL; may be x or residual itself (in place)
  *   rstd        [m]     fp32 output r, or NULL (the backward pass needs it)
