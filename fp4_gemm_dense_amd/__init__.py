@@ -574,15 +574,17 @@ def dg_add_rms_norm_backward_workspace_bytes(m, k):
     return int(lib().dg_add_rms_norm_backward_workspace_bytes(m, k))
 
 
-def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace):
+def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace=None):
     """dx [m, k] bf16 and dweight [k] fp32 from dy, dh (or None), h [m, k] bf16, weight [k] bf16 and the forward
-    pass's rstd [m] (see include/dg.h)."""
+    pass's rstd [m] (see include/dg.h).  workspace: uint8 device tensor of at least
+    dg_add_rms_norm_backward_workspace_bytes(m, k) bytes (None where that is 0)."""
     m, k = dy.shape
     shape, dev = (m, k), dy.get_device()
+    nbytes = 0 if workspace is None else workspace.numel()
     _call("dg_add_rms_norm_backward", dev, _arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"),
           _arg(h, _BF, shape, dev, "h"), _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"),
           _arg(dx, _BF, shape, dev, "dx"), _arg(dweight, _F32S, (k,), dev, "dweight"), m, k,
-          _arg(workspace, _U8S, (workspace.numel(),), dev, "workspace"), workspace.numel())
+          _arg(workspace, _U8S, (nbytes,), dev, "workspace"), nbytes)
 
 
 def dg_get_mk_alignment_for_contiguous_layout():
@@ -732,8 +734,11 @@ def add_rms_norm_backward(dy, dh, h, weight, rstd):
            _arg(weight, _BF, (k,), index, "weight"), _arg(rstd, _F32S, (m,), index, "rstd"))
     dx, dweight = torch.empty_like(dy), _new((k,), torch.float32, dev)
     nbytes = (_lib or load_library()).dg_add_rms_norm_backward_workspace_bytes(m, k)
-    ws = _new((nbytes,), _U8, dev)
-    _call("dg_add_rms_norm_backward", index, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, ws.data_ptr(), nbytes)
+    wp = None
+    if nbytes:
+        ws = _new((nbytes,), _U8, dev)
+        wp = ws.data_ptr()
+    _call("dg_add_rms_norm_backward", index, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, wp, nbytes)
     return dx, dweight
 
 

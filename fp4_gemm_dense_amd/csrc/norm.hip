@@ -11,7 +11,7 @@
 // Bound: HBM (forward 7 bytes per element with a residual, backward 8).  Measured (one
 // MI355X, inputs not in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168
 // 71 us MXFP4, 74 UE8M0, 77 fp32 scales (5.4-5.6 TB/s), 3 x 7168 3.9 us, of which the
-// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 5.8 us (two launches).
+// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 3.6 us.
 #include <algorithm>
 #include <cmath>
 
@@ -273,6 +273,100 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, fl
   }
 }
 
+// Few rows: one launch and no workspace.  dweight needs no row's sum (n = h * rstd), so
+// the first k / 64 workgroups read 64 columns of dy and h once more and add them up, 8
+// threads (8 columns each) across and the others down the rows; one workgroup more for
+// each row forms dx.  first: the workgroup to start at (dx written over dy: two launches,
+// dweight's and then the rows').
+template <int V, int THREADS>
+__global__ void __launch_bounds__(THREADS) rms_norm_backward_few_kernel(NormBackParams p, float* dweight, int first) {
+  __shared__ float sums[NORM_MAX_WAVES][64];
+  __shared__ float red[NORM_MAX_WAVES];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int block = first + (int)blockIdx.x, dw_blocks = p.k >> 6;
+  const int nv = p.k >> 3;
+  if (block < dw_blocks) {
+    const int cx = tid & 7, wave = tid >> 6, step = nt >> 3;
+    const size_t col = (size_t)block * 8 + cx;
+    float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int r0 = tid >> 3; r0 < p.m; r0 += 4 * step) {
+      v4i dy[4], h[4];
+      float r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = min(r0 + u * step, p.m - 1);
+        dy[u] = reinterpret_cast<const v4i*>(p.dy)[(size_t)row * nv + col];
+        h[u] = reinterpret_cast<const v4i*>(p.h)[(size_t)row * nv + col];
+        r[u] = p.rstd[row];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (r0 + u * step >= p.m) break;
+        float a[8], n[8];
+        unpack_bf16x8(dy[u], a);
+        unpack_bf16x8(h[u], n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[e] = fmaf(a[e], n[e] * r[u], dw[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = 8; o < 64; o <<= 1) dw[e] += __shfl_xor(dw[e], o, 64);
+      if ((tid & 63) < 8) sums[wave][cx * 8 + e] = dw[e];
+    }
+    __syncthreads();
+    if (tid < 64) {
+      float t = sums[0][tid];
+      for (int w = 1; w < nt >> 6; ++w) t += sums[w][tid];
+      dweight[block * 64 + tid] = t;
+    }
+    return;
+  }
+  const int row = block - dw_blocks;
+  const v4i none = {0, 0, 0, 0};
+  v4i dy[V], h[V], w[V], dh[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = i * nt + tid;
+    const size_t at = (size_t)row * nv + j;
+    const bool in = j < nv;
+    dy[i] = in ? reinterpret_cast<const v4i*>(p.dy)[at] : none;
+    h[i] = in ? reinterpret_cast<const v4i*>(p.h)[at] : none;
+    w[i] = in ? reinterpret_cast<const v4i*>(p.weight)[j] : none;
+    dh[i] = in && p.dh ? reinterpret_cast<const v4i*>(p.dh)[at] : none;
+  }
+  const float r = p.rstd[row];
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float a[8], n[8], wf[8];
+    unpack_bf16x8(dy[i], a);
+    unpack_bf16x8(h[i], n);
+    unpack_bf16x8(w[i], wf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dot = fmaf(a[e] * wf[e], n[e] * r, dot);
+  }
+  const float mean = block_sum(dot, red) * (1.0f / (float)p.k);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = i * nt + tid;
+    float a[8], n[8], wf[8], d[8];
+    unpack_bf16x8(dy[i], a);
+    unpack_bf16x8(h[i], n);
+    unpack_bf16x8(w[i], wf);
+    unpack_bf16x8(dh[i], d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] += r * (a[e] * wf[e] - n[e] * r * mean);
+    if (j < nv) reinterpret_cast<v4i*>(p.dx)[(size_t)row * nv + j] = pack_bf16x8(d);
+  }
+}
+
+// One launch pays up to some 1200 rows (130 x 2048 3.6 us, 5.9 with partial rows and a
+// second launch; 600 x 7168 9.9 / 13.5; 1200 x 7168 18.2 / 21.5; 1200 x 2048 9.9 / 10.2;
+// 2400 x 7168 41 / 34): each column is read by one workgroup.
+static bool norm_few(int m) { return m <= 1024; }
+
 // Workgroups of the backward kernel, each with one partial row of dweight: one of up to
 // eight waves per CU of the whole chip, or up to four smaller ones (more would write and
 // read more partial rows than they overlap: 4096 x 7168 takes 49 us with 256, 54 with
@@ -298,6 +392,20 @@ static hipError_t launch_norm_backward(const NormBackParams& p, int grid, hipStr
   else if (s.v == 2) hipLaunchKernelGGL((rms_norm_backward_kernel<2, 512>), dim3(grid), dim3(s.threads), 0, hs, p);
   else if (s.threads <= 512) hipLaunchKernelGGL((rms_norm_backward_kernel<4, 512>), dim3(grid), dim3(s.threads), 0, hs, p);
   else hipLaunchKernelGGL((rms_norm_backward_kernel<4, 1024>), dim3(grid), dim3(s.threads), 0, hs, p);
+  return hipGetLastError();
+}
+
+// 512 threads up to 256 rows, 1024 for more (300 x 2048 5.3 us with 512, 4.9 with 1024;
+// 130 x 2048 3.6 / 3.8), whatever the row's length: the columns' workgroups need them.
+static hipError_t launch_norm_backward_few(const NormBackParams& p, float* dweight, int first, int grid, hipStream_t hs) {
+  const int nv = p.k >> 3;
+#define DG_FEW(V, T) hipLaunchKernelGGL((rms_norm_backward_few_kernel<V, T>), dim3(grid), dim3(T), 0, hs, p, dweight, first)
+  if (p.m <= 256 && nv <= 512) DG_FEW(1, 512);
+  else if (p.m <= 256 && nv <= 1024) DG_FEW(2, 512);
+  else if (nv <= 1024) DG_FEW(1, 1024);
+  else if (nv <= 2048) DG_FEW(2, 1024);
+  else DG_FEW(4, 1024);
+#undef DG_FEW
   return hipGetLastError();
 }
 
@@ -335,26 +443,38 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 
 size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k) {
   if (m <= 0 || k <= 0 || k % 128 != 0 || k > NORM_MAX_K) return 0;
-  return (size_t)norm_parts(m, k) * k * sizeof(float);
+  return norm_few(m) ? 0 : (size_t)norm_parts(m, k) * k * sizeof(float);
 }
 
 int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                              const float* rstd, uint16_t* dx, float* dweight, int m, int k, void* workspace,
                              size_t workspace_bytes, void* stream) {
   try {
-    if (!dy || !h || !weight || !rstd || !dx || !dweight || !workspace) return DG_ERR_INVALID_ARG;
+    if (!dy || !h || !weight || !rstd || !dx || !dweight) return DG_ERR_INVALID_ARG;
     if (m <= 0 || k <= 0) return DG_ERR_INVALID_ARG;
     if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(h, 16) || misaligned(weight, 16) ||
-        misaligned(dx, 16) || misaligned(dweight, 16) || misaligned(rstd, 4) || misaligned(workspace, 16))
+        misaligned(dx, 16) || misaligned(dweight, 16) || misaligned(rstd, 4))
       return DG_ERR_INVALID_ARG;
     if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
-    if (workspace_bytes < dg_add_rms_norm_backward_workspace_bytes(m, k)) return DG_ERR_INVALID_ARG;
+    const size_t need = dg_add_rms_norm_backward_workspace_bytes(m, k);
+    if (need && (!workspace || workspace_bytes < need || misaligned(workspace, 16))) return DG_ERR_INVALID_ARG;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
-    const int parts = norm_parts(m, k);
     NormBackParams p{dy, dh, h, weight, rstd, dx, static_cast<float*>(workspace), m, k};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    hipError_t e = launch_norm_backward(p, parts, hs);
+    hipError_t e;
+    if (norm_few(m)) {
+      const int dw = k / 64;
+      if (dx == dy) {
+        e = launch_norm_backward_few(p, dweight, 0, dw, hs);
+        if (e == hipSuccess) e = launch_norm_backward_few(p, dweight, dw, m, hs);
+      } else {
+        e = launch_norm_backward_few(p, dweight, 0, dw + m, hs);
+      }
+      return e == hipSuccess ? DG_OK : DG_ERR_HIP;
+    }
+    const int parts = norm_parts(m, k);
+    e = launch_norm_backward(p, parts, hs);
     if (e != hipSuccess) return DG_ERR_HIP;
     hipLaunchKernelGGL(norm_dweight_kernel, dim3(k / 32), dim3(256), 0, hs, p.part, dweight, parts, k);
     return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;

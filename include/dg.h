@@ -467,13 +467,14 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
  *           the residual stream, or NULL
  *   h       [m, k] bf16, weight [k] bf16, rstd [m] fp32 from the forward pass
  *   dx      [m, k] bf16 (may be dy or dh itself); dweight [k] fp32
- *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned
+ *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned;
+ *           may be NULL when that is 0 (up to 1024 rows)
  * Requirements: as dg_add_rms_norm's.
  */
 int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                              const float* rstd, uint16_t* dx, float* dweight, int m, int k, void* workspace,
                              size_t workspace_bytes, void* stream);
-/* Bytes of that workspace (0 for invalid sizes).  Host-only. */
+/* Bytes of that workspace (0: none; 0 also for invalid sizes).  Host-only. */
 size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k);
 
 /* Row alignment of each group in the contiguous layout (usage guide, 工具函数). Returns 128. */

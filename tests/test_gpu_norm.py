@@ -214,6 +214,21 @@ def test_backward_shapes(dg, m, k, with_dh):
     check_back(run_back(dg, *a), *a)
 
 
+@pytest.mark.parametrize("m,k", [(256, 4096), (257, 4096), (256, 4224), (256, 8192), (257, 8320), (200, 16512), (1024, 640),
+                                 (1025, 128), (1025, 640), (1100, 7168), (1030, 16384), (1027, 32768)])
+def test_backward_at_the_kernels_borders(dg, m, k):
+    a = back_inputs(m, k, True, seed=m + k)
+    check_back(run_back(dg, *a), *a)
+
+
+@pytest.mark.parametrize("into", ["dy", "dh"])
+def test_backward_of_many_rows_in_place(dg, into):
+    a = back_inputs(1300, 1024, True)
+    want = run_back(dg, *a)
+    got = run_back(dg, *a, into=into)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("into", ["dy", "dh"])
 def test_backward_in_place(dg, into):
     a = back_inputs(70, 1024, True)
@@ -250,8 +265,9 @@ def test_backward_against_differences_of_the_forward(dg):
     assert (np.abs(got - diff) <= (2.0 ** -8 + 1e-6) * np.sum(np.abs(dx * u), axis=1)).all()
 
 
-def test_backward_repeats_and_graph_replays(dg):
-    m, k = 333, 7168
+@pytest.mark.parametrize("m", [333, 1333])
+def test_backward_repeats_and_graph_replays(dg, m):
+    k = 7168
     a = back_inputs(m, k, True, seed=50)
     t = [dev(v) for v in a[:4]] + [torch.from_numpy(a[4]).cuda()]
     want = dg.add_rms_norm_backward(*t)
@@ -337,9 +353,10 @@ def test_training_step_of_norm_and_layer(dg):
     check_back((bits(dx), n_(dw).astype(np.float64)), bits(dn), dh, bits(h), wn, n_(rstd))
 
 
-def test_two_calls_at_once_on_two_streams(dg):
+@pytest.mark.parametrize("m", [500, 1500])
+def test_two_calls_at_once_on_two_streams(dg, m):
     """Backward passes in flight together, each with a workspace of its own, and forward passes between them."""
-    a = [back_inputs(500, 1024, True, seed=s) for s in (1, 2)]
+    a = [back_inputs(m, 1024, True, seed=s) for s in (1, 2)]
     t = [[dev(v) for v in i[:4]] + [torch.from_numpy(i[4]).cuda()] for i in a]
     want = [dg.add_rms_norm_backward(*i) for i in t]
     fwd = [dg.add_rms_norm(i[2], i[0], i[3]) for i in t]

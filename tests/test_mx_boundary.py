@@ -81,7 +81,8 @@ def test_norm_refusals(change, status):
 @pytest.mark.parametrize("change,status", [
     ({}, OK), (dict(dh=0), OK), (dict(m=5000, ws_bytes=BIG), OK),
     (dict(dy=0), 1), (dict(h=0), 1), (dict(weight=0), 1), (dict(rstd=0), 1), (dict(dx=0), 1), (dict(dweight=0), 1),
-    (dict(ws=0), 1), (dict(ws=A + 8), 1), (dict(ws_bytes=15), 1), (dict(m=0), 1), (dict(k=0), 1), (dict(dy=A + 8), 1),
+    (dict(m=5000, ws=0), 1), (dict(m=5000, ws=A + 8), 1), (dict(m=5000, ws_bytes=15), 1), (dict(ws=0), OK),
+    (dict(m=0), 1), (dict(k=0), 1), (dict(dy=A + 8), 1),
     (dict(dh=A + 8), 1), (dict(dx=A + 2), 1), (dict(dweight=A + 4), 1), (dict(k=200), 2), (dict(k=32768 + 128), 2),
 ])
 def test_norm_backward_refusals(change, status):
@@ -96,7 +97,7 @@ def test_norm_backward_refusals(change, status):
 def test_norm_backward_workspace_query():
     f = dgm.dg_add_rms_norm_backward_workspace_bytes
     assert f(0, 128) == f(8, 0) == f(8, 100) == f(8, 32768 + 128) == 0
-    assert f(1, 128) >= 128 * 4 and f(1 << 30, 7168) <= 64 << 20
+    assert f(1, 128) == f(1024, 7168) == 0 and f(1025, 128) >= 128 * 4 and f(1 << 30, 7168) <= 64 << 20
 
 
 def test_binding_checks_tensors():
