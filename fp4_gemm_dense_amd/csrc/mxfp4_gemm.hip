@@ -22,24 +22,26 @@
 //     of B's fragments are permuted so that a lane's two neighbouring column blocks
 //     are eight adjacent columns;
 //   * K may be split (few tiles, or a small last round): slices write fp32 partial
-//     tiles to the workspace, which the split-K reduce adds in slice order.  The 64x128
-//     tile instead runs two groups of four waves that take its stages in turn, where
-//     one tile per workgroup covers the problem.
+//     tiles to the workspace, which the split-K reduce adds in slice order.  Where one
+//     tile per workgroup covers the problem, tiles of 64x64 to 128x128 instead run two
+//     groups of four waves that take a tile's stages in turn, each with a ring of its own
+//     (a stage's chain of barrier, reads and products is 0.5-0.6 us however small; 200 x
+//     4096 x 7168 18.4 us on 64x128 with one group, 12.6 with two, 10.7 on 64x64).
 //
 // Measured (one MI355X, operands not in L2): 8192 x 8192 x 8192 247-252 us (4.4
-// PFLOP/s), 4096 x 7168 x 16384 222-238 us, 4096 x 4096 x 7168 58-65 us, all on
-// 256x256; 1111 x 2112 x 7168 20 us on 96x128; 200 x 4096 x 7168 12.6 us.  What bounds
-// the large ones is power: on random codes the clock holds 1.8-1.9 GHz with the matrix
-// cores 56-61 % busy, and the same call on zeros runs at 2.4 GHz (4096 x 7168 x 16384
-// 178 us; matrix instructions alone reach 6.8 PFLOP/s on random codes and 9.6 on
-// zeros).  Timing copies without the stage copies ran 20 % faster, without the barrier
-// 6 %, without the scales 6 %, without the fragment reads 11 %, without any of them 6.4
+// PFLOP/s), 4096 x 7168 x 16384 222-238 us, 4096 x 4096 x 7168 58-65 us, all on 256x256;
+// 1111 x 2112 x 7168 19 us on 96x128; 200 x 4096 x 7168 10.8 us on 64x64.  What bounds
+// the large ones is power: on random codes the clock holds 1.8-2.0 GHz with the matrix
+// cores 49-61 % busy, and the same call on zeros runs at 2.4 GHz (4096 x 7168 x 16384
+// 178 us; matrix instructions alone reach 6.8 PFLOP/s on random codes and 9.6 on zeros).
+// Timing copies without the stage copies ran 20 % faster, without the barrier 6 %,
+// without the scales 6 %, without the fragment reads 11 %, without any of them 6.4
 // PFLOP/s; waiting for fewer copies, or copying from L2 only, changed 1 and 3-8 %.  The
 // middle sizes (one 96x128 tile per workgroup) wait for copies: from L2 only they ran 12
 // % faster.  Tried without gain: four waves of 128x128 each (fewer LDS reads per matrix
-// instruction, but the accumulators take half of the registers and the rest spills:
-// 3-8 % slower), only half of the waves copying, more of a stage's copies put off into
-// the next one, loads that pull the next stage into L2, a later barrier, raised wave
+// instruction, but the accumulators take half of the registers and the rest spills: 3-8
+// % slower), only half of the waves copying, more of a stage's copies put off into the
+// next one, loads that pull the next stage into L2, a later barrier, raised wave
 // priority, other raster bands, a 256x224 tile.
 #include <algorithm>
 #include <cstdio>
@@ -90,7 +92,7 @@ struct MxTile {
   // copies of a stage issued in the next stage's first K block, so that they spread over
   // both: with four column blocks half of them (4096 x 4096 x 7168 on 128x256 75 -> 69
   // us), with eight, or a ring of two slots, two (more come late: 3 % slower)
-  static constexpr int LATE = NT == 8 || (KG == 2 && R == 2) ? 2 : NT == 4 ? 4 : 1;
+  static constexpr int LATE = NT == 8 || (KG > 1 && R == 2) ? 2 : NT == 4 ? 4 : 1;
   // One instance of the stage's code for a unit's first stage and the others, or two (the
   // first one's sums start from a constant).  With two the 256x256 tile runs out of
   // registers: 24 a lane go to memory as it starts (4001 x 4096 x 7168 63.3 us, 60.7 with
@@ -99,7 +101,8 @@ struct MxTile {
   static constexpr bool ONE = MT * NT == 32;
   static constexpr int LDS = KG * RING + (ONE ? 1024 : 0);   // and 1 KB that is written and not read
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
-  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && (KG == 1 || (KG == 2 && NT % 4 == 0)), "tile shape");
+  static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && NSTORE % KG == 0 && (KG == 1 || KG * BM * BN * 4 <= LDS),
+                "tile shape");
 };
 
 // Chunk swizzles of an A and a B row.  A 16-byte LDS read serves lanes {0-3, 12-15,
@@ -451,32 +454,31 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
     keep_late(0);
     static_for<T::LATE>([&](auto i) { issue_late(i); });
 
-    int np0 = 0, np1 = NT / 2;   // the pairs of column blocks this group stores
-    if constexpr (T::KG == 2) {
-      // the groups' sums meet: each hands the other's half of its column blocks over in
-      // LDS (one unit per workgroup: the rings are done with)
+    // the pairs of column blocks (mt, np) that this group stores: every KG-th share of them
+    auto mine = [&](int mt, int np) { return T::KG == 1 || (mt * (NT / 2) + np) / (T::NSTORE / T::KG) == grp; };
+    if constexpr (T::KG > 1) {
+      // the groups' sums meet: each hands the others' pairs over in LDS, and adds theirs to
+      // its own in order (one unit per workgroup: the rings are done with)
       wait_vmcnt<0>();
       wait_lgkmcnt0();
       block_barrier();
-      constexpr int NH = NT / 2;
-      v4f* xch = reinterpret_cast<v4f*>(smem_all) + wave * 64 + lane;   // [group][MT][NH][wave][lane]
+      v4f* xch = reinterpret_cast<v4f*>(smem_all) + wave * 64 + lane;   // [group][MT][NT][wave][lane]
+      auto at = [&](int g, int mt, int nt) -> v4f& { return xch[((g * MT + mt) * NT + nt) * (T::NW * 64)]; };
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NH; ++nt)
-          xch[((grp * MT + mt) * NH + nt) * (T::NW * 64)] = grp ? acc[mt][nt] : acc[mt][NH + nt];
+        for (int nt = 0; nt < NT; ++nt)
+          if (!mine(mt, nt >> 1)) at(grp, mt, nt) = acc[mt][nt];
       wait_lgkmcnt0();
       block_barrier();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NH; ++nt) {
-          const v4f o = xch[(((1 - grp) * MT + mt) * NH + nt) * (T::NW * 64)];
-          if (grp) acc[mt][NH + nt] += o;
-          else acc[mt][nt] += o;
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!mine(mt, nt >> 1)) continue;
+#pragma unroll
+          for (int g = 1; g < T::KG; ++g) acc[mt][nt] += at((grp + g) % T::KG, mt, nt);
         }
-      np0 = grp * (NT / 4);
-      np1 = np0 + NT / 4;
     }
     const int ln = T::ONE ? lane_here() : lane;
     if (cur.part >= 0) {
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (nt < 2 * np0 || nt >= 2 * np1) continue;
+          if (!mine(mt, nt >> 1)) continue;
           const v4i w = {__float_as_int(acc[mt][nt][0]), __float_as_int(acc[mt][nt][1]),
                          __float_as_int(acc[mt][nt][2]), __float_as_int(acc[mt][nt][3])};
           dg_raw_buffer_store_v4i32(w, rsW, at, (mt * 16 * T::BN + (nt >> 1) * 32 + (nt & 1) * 4) * 4, 0);
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
         const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + (ln & 15);
 #pragma unroll
         for (int np = 0; np < NT / 2; ++np) {
-          if (np < np0 || np >= np1) continue;
+          if (!mine(mt, np)) continue;
           const int col = cur.n0 + wave_n * NT * 16 + np * 32 + (ln >> 4) * 8;
           const uint32_t off = row < M && col < N ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u : kBufferOutOfRange;
           v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
@@ -532,7 +534,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
   X(2, 2, 4, 4, 2, 4, 1)  \
   X(3, 2, 2, 2, 4, 6, 1)  \
   X(4, 2, 4, 2, 2, 3, 2)  \
-  X(5, 3, 4, 2, 2, 2, 2)
+  X(5, 3, 4, 2, 2, 2, 2)  \
+  X(6, 2, 2, 2, 2, 4, 2)  \
+  X(7, 4, 4, 2, 2, 2, 2)
 
 struct Mxfp4TileInfo {
   int bm, bn, kg;
@@ -659,8 +663,7 @@ __global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Mxfp
 // id, MT, pairs in flight per wave
 #define DG_MXFP4_SKINNY(X) \
   X(0, 1, 4)               \
-  X(1, 2, 4)               \
-  X(2, 4, 2)
+  X(1, 2, 4)
 constexpr int kMxSkinnyIdBase = 100;   // in DG_FORCE_MXFP4
 
 static int skinny_rows(int id) {
@@ -717,23 +720,24 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
   return pl;
 }
 
-// Few rows: the streaming kernel reads all of A once per 16 columns, so it is taken
+// Up to 32 rows: the streaming kernel reads all of A once per 16 columns, so it is taken
 // while row blocks x columns stay small (measured against the best tile: 1 x 4096 x 7168
-// 6.1 against 11.8 us, 16 x 7168 x 2048 6.0 / 6.7, 32 x 4096 x 7168 9.9 / 12.0; past the
-// limit 1 x 24576 x 1536 10.7 / 7.6, 32 x 7168 x 16384 30.9 / 19.6).  Otherwise the tile
+// 6.0 against 9.7 us, 16 x 7168 x 2048 5.9 / 5.7, 32 x 4096 x 7168 8.5 / 9.9; past the
+// limit 1 x 24576 x 1536 10.7 / 7.5, 32 x 7168 x 16384 28.8 / 19.7).  Otherwise the tile
 // with the least estimated time in microseconds: rounds of units, each its stages at the
 // tile's pace and a fixed share (pipeline fill, D); a split plan's partials' round trip
 // and second launch; and the rate at which the units' CUs stream B.  The constants fit
 // 247 shapes, M 1 to 8192, 512 x 2048 to 32768 x 512 and 7168 x 16384 (geometric mean
-// 0.4 % over the best tile of each; worst 128 x 7168 x 16384, 33 %).
+// 0.2 % over the best tile of each; worst 64 x 7168 x 16384, 18 %).
 static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.75, 1.17, 0.76, 0.64, 0.60, 0.81}, kUnit[] = {4.6, 2.0, 1.0, 1.0, 1.9, 1.9};
-  constexpr double kSplit = 5.5, kPartialRate = 3.4e6, kStreamRate = 40.0e3;   // us, bytes per us
+  constexpr double kStage[] = {1.85, 1.12, 0.76, 0.69, 0.57, 0.81, 0.52, 1.05};
+  constexpr double kUnit[] = {4.5, 2.0, 1.0, 1.0, 1.8, 1.9, 1.6, 2.5};
+  constexpr double kSplit = 5.7, kPartialRate = 3.6e6, kStreamRate = 40.0e3;   // us, bytes per us
   constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
   int force = -1;
   if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
   int skinny = -1;
-  const int mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 0;
+  const int mt = m <= 16 ? 1 : m <= 32 ? 2 : 0;
   if (mt && (long long)mt * n <= 8192) skinny = mt >> 1;
   if (force >= 0) skinny = force >= kMxSkinnyIdBase && skinny_rows(force - kMxSkinnyIdBase) >= m ? force - kMxSkinnyIdBase : -1;
   Mxfp4Plan best{};
