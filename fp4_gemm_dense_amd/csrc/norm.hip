@@ -47,12 +47,26 @@ static NormShape norm_shape(int k) {
 }
 constexpr int NORM_MAX_K = 32768, NORM_MAX_WAVES = 16;
 
+template <int O>
+__device__ __forceinline__ float lane_swap(float v) {
+  return __uint_as_float(lane_swap<O>(__float_as_uint(v)));
+}
+template <int O>
+__device__ __forceinline__ double lane_swap(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)lane_swap<O>((uint32_t)(b >> 32)) << 32 | lane_swap<O>((uint32_t)b)));
+}
+
 // Sum of v over the workgroup, in a fixed order; every thread gets it.  One barrier: a
 // caller that sums again passes another buffer.
 template <typename F>
 __device__ __forceinline__ F block_sum(F v, F* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  v += lane_swap<1>(v);
+  v += lane_swap<2>(v);
+  v += lane_swap<4>(v);
+  v += lane_swap<8>(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
   const int waves = blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
