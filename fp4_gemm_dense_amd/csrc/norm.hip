@@ -10,8 +10,8 @@
 //
 // Bound: HBM (forward 7 bytes per element with a residual, backward 8).  Measured (one
 // MI355X, inputs not in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168
-// 71 us MXFP4, 74 UE8M0, 77 fp32 scales (5.4-5.6 TB/s), 3 x 7168 3.9 us, of which the
-// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 3.6 us.
+// 71 us MXFP4, 74 UE8M0, 76 fp32 scales (5.4-5.6 TB/s), 3 x 7168 3.7 us, of which the
+// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 3.5 us.
 #include <algorithm>
 #include <cmath>
 
@@ -442,6 +442,8 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
         misaligned(q, 16) || misaligned(sf, 4) || misaligned(rstd, 4))
       return DG_ERR_INVALID_ARG;
     if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
+    // (a launch has fewer than 2^32 threads, and a row's workgroup at most this many)
+    if ((long long)m * std::min(1024, (k / 8 + 63) / 64 * 64) >= 1LL << 32) return DG_ERR_UNSUPPORTED;
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
     NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k};

@@ -8,9 +8,9 @@
 //
 // Bound: HBM.  A bf16 element costs 2 bytes of reading and 17/32 of writing per
 // direction.  Measured (one MI355X, inputs not in the caches; a 1 GiB copy runs at 5.1
-// TB/s): 4096 x 7168 bf16 along the rows 16.1 us (4.6 TB/s), transposed 17.2 (4.3), both
-// 23.7 (3.8); 16384 x 7168 both 83 (4.3); 2 x 4096 x 7168 fp32 rows and values 71 (5.4);
-// 5 x 7168 is the launch.
+// TB/s): 4096 x 7168 bf16 along the rows 16.0 us (4.7 TB/s), transposed 17.1 (4.3), both
+// 22.5 (4.0); 16384 x 7168 both 82 (4.4); 2 x 4096 x 7168 fp32 rows and values 71 (5.4);
+// 5 x 7168 2.7, the launch.
 #include <algorithm>
 
 #include "../../include/dg.h"

@@ -451,7 +451,8 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *   x, residual [m, k]  bf16; weight [k] bf16
  *   h           [m, k]  bf16 output, or NULL; may be x or residual itself (in place)
  *   rstd        [m]     fp32 output r, or NULL (the backward pass needs it)
- * Requirements: m, k > 0, eps > 0 and finite; k % 128 == 0 and k <= 32768 (else
+ * Requirements: m, k > 0, eps > 0 and finite; k % 128 == 0, k <= 32768 and m times the
+ *   threads of a row (k/8 rounded up to 64, at most 1024) below 2^32 (else
  *   DG_ERR_UNSUPPORTED); 16-byte aligned tensors (sf and rstd: 4).
  */
 typedef enum dg_quant_format { DG_QUANT_E4M3_F32 = 0, DG_QUANT_E4M3_UE8M0 = 1, DG_QUANT_MXFP4 = 2 } dg_quant_format;
@@ -469,7 +470,7 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
  *   dx      [m, k] bf16 (may be dy or dh itself); dweight [k] fp32
  *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned;
  *           may be NULL when that is 0 (up to 1024 rows)
- * Requirements: as dg_add_rms_norm's.
+ * Requirements: as dg_add_rms_norm's, for any m.
  */
 int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                              const float* rstd, uint16_t* dx, float* dweight, int m, int k, void* workspace,

@@ -70,6 +70,7 @@ def test_gemm_workspace_query_is_host_only_and_zero_for_invalid_sizes():
     (dict(eps=float("inf")), 1), (dict(x=A + 2), 1), (dict(residual=A + 8), 1), (dict(weight=A + 8), 1),
     (dict(h=A + 8), 1), (dict(q=A + 8), 1), (dict(sf=A + 2), 1), (dict(rstd=A + 2), 1),
     (dict(k=64), 2), (dict(k=320), 2), (dict(k=32768 + 128), 2),
+    (dict(m=1 << 26, k=128), 2), (dict(m=1 << 22, k=32768), 2),
 ])
 def test_norm_refusals(change, status):
     v = dict(x=A, residual=A, weight=A, h=A, q=A, sf=A, fmt=0, rstd=A, m=8, k=256, eps=1e-6)
