@@ -76,6 +76,12 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
   return s;
 }
 
+// Bounds of max |h * weight| within which a block's quotients are formed from the
+// products themselves (2^-100 .. 2^100: no step leaves fp32's normal range; an element
+// whose product is subnormal beside them has code 0), and of max |y| for a scale of
+// 2^-126 or more (448 * 2^-126).
+constexpr uint32_t kExactLo = 27u << 23, kExactHi = 227u << 23, kNormalScale = 0x04e00000u;
+
 // One row per workgroup.  (Measured against 2, 4 and 8 rows per workgroup, with the
 // next row loaded ahead and the K-block-major scales leaving in longer runs, and
 // against 2 to 8 persistent workgroups per CU: one row was the fastest at 8192 x 7168
@@ -127,41 +133,60 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
     float y[8], w[8];
     unpack_bf16x8(hv[i], y);
     unpack_bf16x8(wv[i], w);
-    uint32_t amax = 0;
+    uint32_t pmax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = y[e] * w[e] * r;
-      amax = umax(amax, abs_bits(y[e]));
+      y[e] *= w[e];
+      pmax = umax(pmax, abs_bits(y[e]));
     }
     const int kb = j >> 4;
     if constexpr (FMT == DG_QUANT_MXFP4) {
-      const uint32_t byte = ue8m0_byte<false>(group_max<4>(amax));
+      pmax = group_max<4>(pmax);
+      const uint32_t byte = ue8m0_byte<false>(abs_bits(__uint_as_float(pmax) * r));
       const uint32_t word = scale_word(byte);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= r;
       if (in) {
         static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
         if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
       }
     } else {
-      amax = group_max<16>(amax);
-      float inv;
+      pmax = group_max<16>(pmax);
+      const float top = __uint_as_float(pmax) * r;   // max |y|: rounding keeps the order
+      const uint32_t amax = abs_bits(top);
       if constexpr (FMT == DG_QUANT_E4M3_F32) {
-        float s = __uint_as_float(amax) / 448.0f;
-        s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(s, 0x1p-126f));
-        inv = fminf(448.0f / __uint_as_float(amax), 0x1p126f);   // (a NaN scale: the codes are NaN by y)
-        if (amax == 0 || amax >= 0x7f800000u) inv = s;
+        const float s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(top / 448.0f, 0x1p-126f));
         if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
+        // y / s is 448 (h w) / max |h w| wherever s is not at its least: r cancels, both
+        // products have 16 bits, and ties between two codes are common (1 in 2600 on normal
+        // data).  The quotient by a reciprocal is corrected by its remainder, which is exact:
+        // a tie comes out as itself and goes to the even code.  (y / s in fp32 decides one
+        // tie in six by the roundings of y and s.)
+        if (pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u) {
+          const float t = __uint_as_float(pmax), it = __builtin_amdgcn_rcpf(t);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float n = y[e] * 448.0f, q0 = n * it;
+            y[e] = fmaf(fmaf(-q0, t, n), it, q0);
+          }
+        } else {
+          const float inv = amax == 0 || amax >= 0x7f800000u ? s : fminf(448.0f / top, 0x1p126f);   // (NaN: so are the codes)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * inv;
+        }
       } else {
         // the wave's four blocks make one word (past the end: 2^0)
         const uint32_t byte = in ? ue8m0_byte<true>(amax) : 127u;
-        inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);   // 2^(127 - byte)
+        const float inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);   // 2^(127 - byte)
         uint32_t word = byte << (8 * ((tid >> 4) & 3));
         word |= (uint32_t)__shfl_xor((int)word, 16, 64);
         word |= (uint32_t)__shfl_xor((int)word, 32, 64);
         if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * inv;
       }
       if (in)
-        static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                               (int)e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
+        static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0], y[1], y[2], y[3]), (int)e4m3x4(y[4], y[5], y[6], y[7])};
     }
   }
 }

@@ -439,8 +439,9 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *   y = h * r * weight                     fp32, not rounded before it is quantised
  * and y is quantised in the format the GEMM behind it reads:
  *   DG_QUANT_E4M3_F32    q [m, k] e4m3, sf [k/128, m] fp32: s = max|y| / 448 per 1x128 block (at
- *                        least 2^-126; 1 where the block is all zeros), code = e4m3(y / s): A of
- *                        dg_fp8_gemm_nt and the other fp32-scale forms
+ *                        least 2^-126; 1 where the block is all zeros), code = e4m3 nearest to
+ *                        448 * y / max|y| (y / s before s is rounded to fp32), ties to the even
+ *                        code: A of dg_fp8_gemm_nt and the other fp32-scale forms
  *   DG_QUANT_E4M3_UE8M0  q [m, k] e4m3, sf [m, ceil(k/512)] int32: the smallest power of two
  *                        with 448 * 2^e >= max|y| per 1x128 block (2^0 for zeros and for the
  *                        unused bytes of the last word): A of the _ue8m0 forms, x of the FFN

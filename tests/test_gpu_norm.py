@@ -370,3 +370,23 @@ def test_two_calls_at_once_on_two_streams(dg, m):
     for i, b, f in got:
         assert torch.equal(b[0], want[i][0]) and torch.equal(b[1], want[i][1])
         assert all(torch.equal(u, v) for u, v in zip(f, fwd[i]))
+
+
+@pytest.mark.parametrize("m,k", [(3, 7168), (200, 2048), (64, 16384), (70, 640)])
+def test_fp32_scale_codes_and_ties(dg, m, k):
+    """The codes of the fp32-scale format are those of 448 y / max|y| exactly, ties to the even code: the row's r
+    cancels, and 448 (h w) / max|h w| is a ratio of integers of at most 25 bits, so that float64's quotient is a midpoint
+    of two codes if and only if the exact one is.  The scale is max|y| / 448 in fp32 of the kernel's own r."""
+    x, res, w = bf(90 + m, m, k, scale=2.0), bf(91, m, k), f64_to_bf16_bits(1 + 0.2 * np.random.default_rng(2).standard_normal(k))
+    q, sf, hb, rstd = run_norm(dg, x, res, w, F32)
+    p = bf16_bits_to_f64(hb) * bf16_bits_to_f64(w)                       # exact
+    blocks = np.abs(p).reshape(m, k // 128, 128)
+    amax = blocks.max(axis=2)
+    v = (blocks * 448 / amax[..., None]).reshape(m, k)
+    if m * k >= 200 * 2048:                                              # the inputs meet ties
+        mids = (X.E4M3_GRID[1:] + X.E4M3_GRID[:-1]) / 2
+        assert np.isin(v, mids).sum() >= 20
+    want = X.nearest_code(v, X.E4M3_GRID).astype(np.uint8) | (np.signbit(p).astype(np.uint8) << 7)
+    assert np.array_equal(q, want), f"{np.count_nonzero(q != want)} of {q.size} codes differ"
+    top = amax.astype(np.float32) * rstd.astype(np.float32)[:, None]
+    assert np.array_equal(sf.T, top / np.float32(448))
