@@ -76,11 +76,28 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
   return s;
 }
 
-// Bounds of max |h * weight| within which a block's quotients are formed from the
-// products themselves (2^-100 .. 2^100: no step leaves fp32's normal range; an element
-// whose product is subnormal beside them has code 0), and of max |y| for a scale of
-// 2^-126 or more (448 * 2^-126).
+// Bounds of max |h * weight|, 2^-100 .. 2^100.  From the lower one on the products of a
+// block are exact (one that is subnormal beside the largest has code 0); within both no
+// step of the fp32-scale format's quotients leaves fp32's normal range.  And of max |y| for
+// a scale of 2^-126 or more (448 * 2^-126).
 constexpr uint32_t kExactLo = 27u << 23, kExactHi = 227u << 23, kNormalScale = 0x04e00000u;
+
+// y = h * weight * r of one vector where the product may have left fp32's range (or the
+// block is zeros or not finite): the 40-bit product is exact in fp64 and rounded once.
+// Returns the pattern of max |y| over the block's LANES lanes, which all take part.
+template <int LANES>
+__device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, float r, float (&y)[8]) {
+  float a[8], w[8];
+  unpack_bf16x8(h, a);
+  unpack_bf16x8(weight, w);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = (float)((double)a[e] * (double)w[e] * (double)r);
+    amax = umax(amax, abs_bits(y[e]));
+  }
+  return group_max<LANES>(amax);
+}
 
 // One row per workgroup.  (Measured against 2, 4 and 8 rows per workgroup, with the
 // next row loaded ahead and the K-block-major scales leaving in longer runs, and
@@ -140,21 +157,28 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
       pmax = umax(pmax, abs_bits(y[e]));
     }
     const int kb = j >> 4;
-    if constexpr (FMT == DG_QUANT_MXFP4) {
-      pmax = group_max<4>(pmax);
-      const uint32_t byte = ue8m0_byte<false>(abs_bits(__uint_as_float(pmax) * r));
-      const uint32_t word = scale_word(byte);
+    pmax = group_max<FMT == DG_QUANT_MXFP4 ? 4 : 16>(pmax);
+    uint32_t amax = abs_bits(__uint_as_float(pmax) * r);   // of max |y|: rounding keeps the order
+    bool exact = false;   // y holds the products, and they are as exact as the quotients need
+    if constexpr (FMT == DG_QUANT_E4M3_F32) {
+      exact = pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u;
+      if (!exact) amax = y_by_fp64<16>(hv[i], wv[i], r, y);
+    } else if (pmax >= kExactLo && pmax < 0x7f800000u) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] *= r;
+    } else {
+      amax = y_by_fp64<FMT == DG_QUANT_MXFP4 ? 4 : 16>(hv[i], wv[i], r, y);
+    }
+    if constexpr (FMT == DG_QUANT_MXFP4) {
+      const uint32_t byte = ue8m0_byte<false>(amax);
+      const uint32_t word = scale_word(byte);
       if (in) {
         static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
         if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
       }
     } else {
-      pmax = group_max<16>(pmax);
-      const float top = __uint_as_float(pmax) * r;   // max |y|: rounding keeps the order
-      const uint32_t amax = abs_bits(top);
       if constexpr (FMT == DG_QUANT_E4M3_F32) {
+        const float top = __uint_as_float(amax);
         const float s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(top / 448.0f, 0x1p-126f));
         if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
         // y / s is 448 (h w) / max |h w| wherever s is not at its least: r cancels, both
@@ -162,7 +186,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
         // data).  The quotient by a reciprocal is corrected by its remainder, which is exact:
         // a tie comes out as itself and goes to the even code.  (y / s in fp32 decides one
         // tie in six by the roundings of y and s.)
-        if (pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u) {
+        if (exact) {
           const float t = __uint_as_float(pmax), it = __builtin_amdgcn_rcpf(t);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -172,7 +196,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
         } else {
           const float inv = amax == 0 || amax >= 0x7f800000u ? s : fminf(448.0f / top, 0x1p126f);   // (NaN: so are the codes)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * inv;
+          for (int e = 0; e < 8; ++e) y[e] *= inv;
         }
       } else {
         // the wave's four blocks make one word (past the end: 2^0)
@@ -183,7 +207,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
         word |= (uint32_t)__shfl_xor((int)word, 32, 64);
         if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * inv;
+        for (int e = 0; e < 8; ++e) y[e] *= inv;
       }
       if (in)
         static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0], y[1], y[2], y[3]), (int)e4m3x4(y[4], y[5], y[6], y[7])};

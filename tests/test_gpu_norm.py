@@ -390,3 +390,16 @@ def test_fp32_scale_codes_and_ties(dg, m, k):
     assert np.array_equal(q, want), f"{np.count_nonzero(q != want)} of {q.size} codes differ"
     top = amax.astype(np.float32) * rstd.astype(np.float32)[:, None]
     assert np.array_equal(sf.T, top / np.float32(448))
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+@pytest.mark.parametrize("he,we,eps", [(55, 75, 1e-6), (-80, -60, 2.0 ** -120), (-100, -60, 2.0 ** -126), (-30, -40, 1e-6)])
+def test_norm_products_outside_fp32(dg, fmt, he, we, eps):
+    """h * weight leaves fp32's range (to infinity, to subnormals, to 0) where y = h * r * weight does not; in one row of
+    blocks or in some of its blocks only.  One rounding to fp32 is within the bound on y."""
+    m, k = 6, 1024
+    x, w = bf(100, m, k, scale=2.0 ** he), bf(101, k, scale=2.0 ** we)
+    x[1, :512] = bf(102, 512, scale=2.0 ** (he // 2))
+    x[2, 7::64] = 0
+    w[128:256] = bf(103, 128)
+    check_norm(run_norm(dg, x, None, w, fmt, eps=eps), x, None, w, fmt, eps)
