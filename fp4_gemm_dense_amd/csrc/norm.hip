@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, fl
 // Few rows: one launch and no workspace.  dweight needs no row's sum (n = h * rstd), so
 // the first k / 64 workgroups read 64 columns of dy and h once more and add them up, 8
 // threads (8 columns each) across and the others down the rows; one workgroup more for
-// each row forms dx.  first: the workgroup to start at (dx written over dy: two launches,
-// dweight's and then the rows').
+// each row forms dx.  first: the workgroup to start at (dx written over dy or h: two
+// launches, dweight's and then the rows').
 template <int V, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_backward_few_kernel(NormBackParams p, float* dweight, int first) {
   __shared__ float sums[NORM_MAX_WAVES][64];
@@ -530,7 +530,7 @@ int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
     hipError_t e;
     if (norm_few(m)) {
       const int dw = k / 64;
-      if (dx == dy) {
+      if (dx == dy || dx == h) {
         e = launch_norm_backward_few(p, dweight, 0, dw, hs);
         if (e == hipSuccess) e = launch_norm_backward_few(p, dweight, dw, m, hs);
       } else {

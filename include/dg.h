@@ -468,7 +468,8 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
  *   dy      [m, k] bf16, the gradient of y; dh [m, k] bf16, the gradient that arrives at h from
  *           the residual stream, or NULL
  *   h       [m, k] bf16, weight [k] bf16, rstd [m] fp32 from the forward pass
- *   dx      [m, k] bf16 (may be dy or dh itself); dweight [k] fp32
+ *   dx      [m, k] bf16 (may be dy, dh or h itself; otherwise the outputs overlap
+ *           nothing); dweight [k] fp32
  *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned;
  *           may be NULL when that is 0 (up to 1024 rows)
  * Requirements: as dg_add_rms_norm's, for any m.

@@ -403,3 +403,14 @@ def test_norm_products_outside_fp32(dg, fmt, he, we, eps):
     x[2, 7::64] = 0
     w[128:256] = bf(103, 128)
     check_norm(run_norm(dg, x, None, w, fmt, eps=eps), x, None, w, fmt, eps)
+
+
+@pytest.mark.parametrize("m,k", [(1, 2048), (70, 2048), (1000, 1152), (1300, 2048), (1030, 20480)])
+@pytest.mark.parametrize("with_dh", [False, True])
+def test_backward_into_h(dg, m, k, with_dh):
+    """dx written over h: the workgroups that sum dweight have read h before a row of it is overwritten."""
+    a = back_inputs(m, k, with_dh, seed=7)
+    want = run_back(dg, *a)
+    for _ in range(4):
+        got = run_back(dg, *a, into="h")
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
