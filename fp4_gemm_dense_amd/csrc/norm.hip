@@ -430,6 +430,9 @@ __global__ void __launch_bounds__(THREADS) rms_norm_backward_few_kernel(NormBack
 // 2400 x 7168 41 / 34): each column is read by one workgroup.
 static bool norm_few(int m) { return m <= 1024; }
 
+// (a workgroup's next row, up to 1024 further, is an int)
+static bool norm_backward_fits(int m, int k) { return k % 128 == 0 && k <= NORM_MAX_K && m <= 0x7fffffff - 1024; }
+
 // Workgroups of the backward kernel, each with one partial row of dweight: one of up to
 // eight waves per CU of the whole chip, or up to four smaller ones (more would write and
 // read more partial rows than they overlap: 4096 x 7168 takes 49 us with 256, 54 with
@@ -507,7 +510,7 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 }
 
 size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k) {
-  if (m <= 0 || k <= 0 || k % 128 != 0 || k > NORM_MAX_K) return 0;
+  if (m <= 0 || k <= 0 || !norm_backward_fits(m, k)) return 0;
   return norm_few(m) ? 0 : (size_t)norm_parts(m, k) * k * sizeof(float);
 }
 
@@ -520,7 +523,7 @@ int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
     if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(h, 16) || misaligned(weight, 16) ||
         misaligned(dx, 16) || misaligned(dweight, 16) || misaligned(rstd, 4))
       return DG_ERR_INVALID_ARG;
-    if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
+    if (!norm_backward_fits(m, k)) return DG_ERR_UNSUPPORTED;
     const size_t need = dg_add_rms_norm_backward_workspace_bytes(m, k);
     if (need && (!workspace || workspace_bytes < need || misaligned(workspace, 16))) return DG_ERR_INVALID_ARG;
     DeviceInfo di = current_device_info();

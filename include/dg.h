@@ -472,7 +472,8 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
  *           nothing); dweight [k] fp32
  *   workspace: at least dg_add_rms_norm_backward_workspace_bytes(m, k) bytes, 16-byte aligned;
  *           may be NULL when that is 0 (up to 1024 rows)
- * Requirements: as dg_add_rms_norm's, for any m.
+ * Requirements: as dg_add_rms_norm's on k and alignment (dweight: 16); m > 0, m at most
+ *   2^31 - 1025 (else DG_ERR_UNSUPPORTED).
  */
 int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                              const float* rstd, uint16_t* dx, float* dweight, int m, int k, void* workspace,

@@ -124,3 +124,13 @@ def test_binding_checks_tensors():
         dgm.dg_add_rms_norm_backward(x, None, x, x[0].clone(), torch.zeros(4, dtype=f32), x, torch.zeros(256, dtype=f32),
                                      torch.zeros(8, dtype=u8))
     assert isinstance(dgm.lib(), ctypes.CDLL)
+
+
+def test_norm_backward_refuses_rows_whose_successor_passes_int():
+    """A workgroup steps from row to row by up to 1024: the last row it tests has to be an int."""
+    def call(m):
+        need = dgm.dg_add_rms_norm_backward_workspace_bytes(m, 128)
+        return need, dgm.lib().dg_add_rms_norm_backward(A, A, A, A, A, A, A, m, 128, A, need, None)
+    assert call(0x7fffffff) == (0, 2) and call(0x7fffffff - 1023) == (0, 2)
+    need, status = call(0x7fffffff - 1024)
+    assert need > 0 and status in OK
