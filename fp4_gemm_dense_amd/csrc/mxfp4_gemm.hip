@@ -450,9 +450,13 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(Mxfp4Params p
       stage(std::false_type{}, first);
       first = 0;
     }
-    // (the last stage's late copies go out ahead of the stores)
+    // The last stage's late copies go out ahead of the stores: the next unit's first wait
+    // counts the stores as younger (a store that moved ahead of a copy would let that stage
+    // read LDS before the copy has landed).
     keep_late(0);
     static_for<T::LATE>([&](auto i) { issue_late(i); });
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 
     // the pairs of column blocks (mt, np) that this group stores: every KG-th share of them
     auto mine = [&](int mt, int np) { return T::KG == 1 || (mt * (NT / 2) + np) / (T::NSTORE / T::KG) == grp; };
@@ -749,7 +753,7 @@ static Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
   for (int id = 0; id < kTiles; ++id) {
     const int kg = kMxTiles[id].kg;
     const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
-    if (kg > 1 && pl.units > cus) continue;   // one unit per workgroup
+    if (kg > 1 && pl.units > cus) continue;   // one unit per workgroup (a pinned one is passed over, too)
     const int whole = ((k / 128 + 1) / 2 + kg - 1) / kg;
     double t = (double)((pl.full_tiles + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
     if (pl.splits > 1)
@@ -810,9 +814,9 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
       if (pl.skinny >= 0)
         std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> streaming kernel, %d rows\n", m, n, k, skinny_rows(pl.skinny));
       else
-        std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> tile %dx%d, %d tiles (%d whole, the rest x %d K slices), "
+        std::fprintf(stderr, "[dg] mxfp4_gemm_nt m=%d n=%d k=%d -> tile %dx%d, %d K group%s, %d tiles (%d whole, the rest x %d K slices), "
                      "%d workgroups, workspace %zu bytes\n", m, n, k, kMxTiles[pl.tile].bm, kMxTiles[pl.tile].bn,
-                     pl.tiles_m * pl.tiles_n, pl.full_tiles, pl.splits, pl.grid, pl.ws_bytes);
+                     kMxTiles[pl.tile].kg, kMxTiles[pl.tile].kg > 1 ? "s" : "", pl.tiles_m * pl.tiles_n, pl.full_tiles, pl.splits, pl.grid, pl.ws_bytes);
     }
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = pl.skinny >= 0 ? launch_mxfp4_skinny(p, pl.skinny, hs) : launch_mxfp4_tile(p, pl.tile, pl.grid, hs);
