@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantParams p) {
   const T* x = static_cast<const T*>(p.x);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int kb_n = p.k >> 7;
-  const uint32_t cb = (uint32_t)(p.k + QR_COLS - 1) / QR_COLS, rb = (uint32_t)(p.m + QR_ROWS - 1) / QR_ROWS;
+  const uint32_t cb = ((uint32_t)p.k + QR_COLS - 1) / QR_COLS, rb = ((uint32_t)p.m + QR_ROWS - 1) / QR_ROWS;
   const long long total = (long long)cb * rb * p.groups;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
     const uint32_t row_block = (uint32_t)(t / cb), c0 = (uint32_t)(t - (long long)row_block * cb) * QR_COLS;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(QuantParams p) {
   __shared__ __attribute__((aligned(4))) uint8_t bytes[128][4];
   const T* x = static_cast<const T*>(p.x);
   const int tid = threadIdx.x;
-  const uint32_t kb_n = (uint32_t)p.k >> 7, mb_n = (uint32_t)(p.m + 127) >> 7;
+  const uint32_t kb_n = (uint32_t)p.k >> 7, mb_n = ((uint32_t)p.m + 127) >> 7;
   const size_t mp = (size_t)mb_n * 128;
   const long long total = (long long)p.groups * mb_n * kb_n;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
@@ -275,7 +275,7 @@ extern "C" int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t*
       else
         hipLaunchKernelGGL(quantize_tiles_kernel<float>, dim3(grid), dim3(256), 0, hs, p);
     } else {
-      const long long tiles = (long long)num_groups * ((m + QR_ROWS - 1) / QR_ROWS) * ((k + QR_COLS - 1) / QR_COLS);
+      const long long tiles = (long long)num_groups * ((m + QR_ROWS - 1) / QR_ROWS) * (((long long)k + QR_COLS - 1) / QR_COLS);
       const int grid = (int)std::min<long long>(tiles, (long long)cus * 64);
       if (x_type == DG_BF16)
         hipLaunchKernelGGL(quantize_rows_kernel<uint16_t>, dim3(grid), dim3(256), 0, hs, p);

@@ -348,3 +348,16 @@ def test_quantized_weights_feed_the_expert_ffn(dg):
         gen += [torch.stack(p).cuda(), dg.dg_transform_fp4_weight_sf(torch.stack(s).cuda())]
     assert all(torch.equal(a, b) for a, b in zip(own, gen))
     assert torch.equal(dg.fp8_fp4_expert_ffn(*t, *own), dg.fp8_fp4_expert_ffn(*t, *gen))
+
+
+@pytest.mark.parametrize("k", [2 ** 31 - 512, 2 ** 31 - 384, 2 ** 31 - 128])
+def test_quantize_longest_row(dg, k):
+    """The longest rows: codes and scales equal those of the row quantised piece by piece."""
+    x = torch.randn(k // 16, device="cuda").to(torch.bfloat16).repeat(16).view(1, k)
+    x[0, k - 77] = 1000.0
+    q, sf = dg.quantize_mxfp4(x)
+    step = 1 << 27
+    for a in range(0, k, step):
+        b = min(a + step, k)
+        pq, psf = dg.quantize_mxfp4(x[:, a:b])
+        assert torch.equal(q[:, a // 2:b // 2], pq) and torch.equal(sf[a // 128:b // 128], psf), a
