@@ -454,18 +454,16 @@ _X_TYPES = {**{t: 0 for t in _BF}, torch.float32: 1}
 QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4 = 0, 1, 2
 
 
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-
-
 def _call(name, index, *args):
     """The C entry point on device `index` and torch's current stream there.  (A decode step makes many calls of a few
-    microseconds: these wrappers read the raw stream and device index, and pass addresses as plain integers.)"""
-    f = getattr(_lib or load_library(), name)
-    if index == _current_device():
-        st = f(*args, _raw_stream(index))
+    microseconds: these wrappers read the raw stream and device index, and pass addresses as plain integers.  A torch
+    without the device backend has neither of the two, so they are looked up here.)"""
+    f, c = getattr(_lib or load_library(), name), torch._C
+    if index == c._cuda_getDevice():
+        st = f(*args, c._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = f(*args, _raw_stream(index))
+            st = f(*args, c._cuda_getCurrentRawStream(index))
     if st:
         raise DgError(name, st)
 

@@ -2,12 +2,16 @@
 and the binding checks its tensors (no compute is launched; these tests run without a GPU)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import fp4_gemm_dense_amd as dgm
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x10000      # a fake aligned address, never dereferenced on the host
 BIG = 1 << 30
 OK = (0, 4)      # passed validation; without a gfx950 device the call stops at the device check
@@ -134,3 +138,25 @@ def test_norm_backward_refuses_rows_whose_successor_passes_int():
     assert call(0x7fffffff) == (0, 2) and call(0x7fffffff - 1023) == (0, 2)
     need, status = call(0x7fffffff - 1024)
     assert need > 0 and status in OK
+
+
+def test_host_only_uses_without_the_device_backend():
+    """A torch built without the device backend has neither of the functions that the launching calls read the device and
+    stream with: importing the binding, plans, workspace queries and refusals have to work there."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import fp4_gemm_dense_amd as dgm
+assert dgm.dg_mxfp4_gemm_workspace_bytes(512, 512, 8192, 256) >= 0
+assert dgm.dg_add_rms_norm_backward_workspace_bytes(1025, 128) > 0
+try:
+    dgm.quantize_mxfp4(torch.zeros(4, 256, dtype=torch.bfloat16))
+except ValueError as e:
+    assert "must be a device tensor" in str(e)
+else:
+    raise AssertionError
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
