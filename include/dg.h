@@ -394,8 +394,9 @@ int dg_k_grouped_fp8_gemm_tn_contiguous(const uint8_t* a, const float* sfa, cons
  *   qt     [num_groups, k, mp/2]         E2M1 pairs along m
  *   sft    [num_groups, mp/128, k]       int32
  *   values [num_groups, m, k]            bf16, optional: what q and sf stand for, code * 2^e,
- *                                        exactly (a NaN block: NaN), for a forward pass that
- *                                        trains through the rounding
+ *                                        exactly (a NaN block: NaN; 2^128, which an |x| of
+ *                                        1.75 * 2^127 or more rounds to: infinity), for a
+ *                                        forward pass that trains through the rounding
  * At least one of q, qt and values is given; x is read once.
  * Requirements: num_groups, m, k > 0; k % 128 == 0 and num_groups * m, m + 127 at
  *   most 2^31 - 1 (else DG_ERR_UNSUPPORTED).  Outputs must not overlap x or each other.

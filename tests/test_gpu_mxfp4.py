@@ -361,3 +361,20 @@ def test_quantize_longest_row(dg, k):
         b = min(a + step, k)
         pq, psf = dg.quantize_mxfp4(x[:, a:b])
         assert torch.equal(q[:, a // 2:b // 2], pq) and torch.equal(sf[a // 128:b // 128], psf), a
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_near_the_largest_number(dg, dtype):
+    """Blocks with a magnitude above 1.5 * 2^127 have the exponent 126; from 1.75 * 2^127 on the nearest code is 4, which
+    stands for 2^128: infinity in the bf16 values, the largest finite exponent in the scale."""
+    x = values(17, 40, 256)
+    top = np.float32(2.0) ** 127
+    for i, f in enumerate((1.5, 1.5078125, 1.7421875, 1.75, 1.7578125, 1.9921875)):
+        x[i, 32 * i] = f * top
+        x[i + 10, 32 * i + 5] = -f * top
+    x[30, 3] = np.finfo(np.float32).max if dtype == torch.float32 else 1.9921875 * top
+    t, x64 = to_dev(x, dtype)
+    assert np.isfinite(x64).all()
+    check_quantize(dg, t, x64)
+    v = dg.quantize_mxfp4(t, values=True)[2].double().cpu().numpy()
+    assert np.array_equal(np.isinf(v), np.abs(x64) >= 1.75 * 2.0 ** 127) and not np.isnan(v).any()
