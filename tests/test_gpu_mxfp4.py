@@ -378,3 +378,16 @@ def test_quantize_near_the_largest_number(dg, dtype):
     check_quantize(dg, t, x64)
     v = dg.quantize_mxfp4(t, values=True)[2].double().cpu().numpy()
     assert np.array_equal(np.isinf(v), np.abs(x64) >= 1.75 * 2.0 ** 127) and not np.isnan(v).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("want", [("rows",), ("cols",), ("values",), ("rows", "values"), ("rows", "cols", "values")])
+@pytest.mark.parametrize("shape", [(3, 257, 640), (1500, 1152), (2, 40, 4224)])
+def test_quantize_more_tiles_than_workgroups(dg, shape, want, dtype):
+    """Several tiles per workgroup: the LDS areas are used again and later tiles' groups, rows and columns decoded."""
+    x, x64 = to_dev(values(sum(shape), *shape), dtype)
+    dg.dg_set_num_cus(1)                                  # 8 workgroups of tiles, 64 of row blocks
+    try:
+        check_quantize(dg, x, x64, want)
+    finally:
+        dg.dg_set_num_cus(0)
