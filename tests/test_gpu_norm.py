@@ -414,3 +414,76 @@ def test_backward_into_h(dg, m, k, with_dh):
     for _ in range(4):
         got = run_back(dg, *a, into="h")
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+@pytest.mark.parametrize("k", [384, 1536, 7168, 16384])
+def test_norm_rows_do_not_depend_on_the_batch(dg, k, fmt):
+    """The kernel is a function of k and the format: a row's outputs are bit for bit the same in any batch."""
+    m = 1500
+    x, res, w = bf(10, m, k), bf(11, m, k), bf(12, k)
+    big = run_norm(dg, x, res, w, fmt)
+    for rows in (slice(0, 1), slice(3, 43), slice(700, 1500)):
+        q, sf, h, r = run_norm(dg, x[rows], res[rows], w, fmt)
+        assert np.array_equal(q, big[0][rows]) and np.array_equal(h, big[2][rows]) and np.array_equal(r, big[3][rows])
+        assert np.array_equal(sf, big[1][rows] if fmt == UE8M0 else big[1][:, rows])
+
+
+@pytest.mark.parametrize("m,k", [(3, 128), (40, 2048), (9, 7168), (5, 32768)])
+def test_norm_rstd(dg, m, k):
+    """A thread adds at most 32 squares (8 up to k = 2048, 16 up to 8192) in fp32, each addition off by half a step of a
+    sum that is at most the whole: 32 * 2^-24 of it, half of that in 1/sqrt, and r's own rounding; the sum between
+    threads is in 64 bits."""
+    per = 8 if k <= 2048 else 16 if k <= 8192 else 32
+    x, res, w = bf(110, m, k, scale=3.0), bf(111, m, k), bf(112, k)
+    _, _, hb, rstd = run_norm(dg, x, res, w, UE8M0)
+    r = 1 / np.sqrt(np.mean(bf16_bits_to_f64(hb) ** 2, axis=1) + float(np.float32(1e-6)))
+    assert (np.abs(rstd - r) <= (per / 2 + 1) * 2.0 ** -24 * (1 + 2.0 ** -20) * r).all()
+
+
+def test_block_of_calls_keeps_rstd_and_feeds_the_fp32_scale_gemm(dg):
+    """Norm -> MXFP4 GEMM -> norm with fp32 scales -> FP8 GEMM, each stage on the operands that the one before it made:
+    both rstd are the kernel's own, and the products hold to (K/8 + 1) 2^-23 of their magnitudes."""
+    import synth
+    from oracle import ref as R
+    from tests.helpers import check_parity
+    m, k, n = 70, 512, 768
+    x, res, w1, w2 = bf(60, m, k), bf(61, m, k), bf(62, k), bf(63, n)
+    wq, wsf = dg.quantize_mxfp4(torch.randn(n, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)))
+    g = synth.gen_dense(16, 256, n, seed=1, with_c=False)
+    b2, sfb2 = g["b"].cuda(), g["sfb"].cuda()
+    q, sf, h, rstd = dg.add_rms_norm(dev(x), dev(res), dev(w1), 1e-6, dg.QUANT_MXFP4)
+    y = dg.mxfp4_gemm_nt(q, sf, wq, wsf)
+    q2, sf2, h2, rstd2 = dg.add_rms_norm(y, None, dev(w2), 1e-6, dg.QUANT_E4M3_F32)
+    d = torch.empty(m, 256, dtype=torch.bfloat16, device="cuda")
+    dg.dg_fp8_gemm_nt(q2, sf2, b2, sfb2, None, d)
+    n_ = lambda t: t.cpu().numpy()                                                      # noqa: E731
+    check_norm((n_(q), n_(sf), bits(h), n_(rstd).astype(np.float64)), x, res, w1, MX)
+    a_, b_ = X.dequant_mxfp4(n_(q), n_(sf)), X.dequant_mxfp4(n_(wq), n_(wsf))
+    ref, s = a_ @ b_.T, np.abs(a_) @ np.abs(b_).T
+    assert (np.abs(bf16_bits_to_f64(bits(y)) - ref) <= 2.0 ** -8 * np.abs(ref) + (k / 8 + 1) * 2.0 ** -23 * (1 + 2.0 ** -8) * s).all()
+    check_norm((n_(q2), n_(sf2), bits(h2), n_(rstd2).astype(np.float64)), bits(y), None, w2, F32)
+    check_parity(bits(d), R.fp8_gemm_nt(n_(q2), n_(sf2), n_(b2), n_(sfb2)), what="fp8 gemm on the norm's codes")
+
+
+def test_training_step_with_the_weight_gradient(dg):
+    """The layer's dw = qt(dy) . qt(y)^T behind a norm: y leaves the norm as codes with blocks along k only, so the
+    caller forms it again in bf16 from h and rstd; all three products to (K/8 + 1) 2^-23 of their magnitudes."""
+    T, K, N = 150, 384, 256
+    x, res, wn = bf(80, T, K), bf(81, T, K), f64_to_bf16_bits(1 + 0.3 * np.random.default_rng(82).standard_normal(K))
+    w, dy, dh = bf(83, N, K), bf(84, T, N), bf(85, T, K)
+    q, sf, h, rstd = dg.add_rms_norm(dev(x), dev(res), dev(wn), 1e-6, dg.QUANT_MXFP4)
+    y = (h.float() * rstd[:, None] * dev(wn).float()).to(torch.bfloat16)
+    _, _, yt, yst = dg.quantize_mxfp4(y, transposed=True)
+    wq, wsf, wqt, wsft = dg.quantize_mxfp4(dev(w), transposed=True)
+    dyq, dysf, dyt, dyst = dg.quantize_mxfp4(dev(dy), transposed=True)
+    out, dn, dw = dg.mxfp4_gemm_nt(q, sf, wq, wsf), dg.mxfp4_gemm_nt(dyq, dysf, wqt, wsft), dg.mxfp4_gemm_nt(dyt, dyst, yt, yst)
+    dx, dweight = dg.add_rms_norm_backward(dn, dev(dh), h, dev(wn), rstd)
+    n_ = lambda t: t.cpu().numpy()                                                      # noqa: E731
+    for got, a, asf, b, bsf, k in ((out, q, sf, wq, wsf, K), (dn, dyq, dysf, wqt, wsft, N), (dw, dyt, dyst, yt, yst, 256)):
+        a_, b_ = X.dequant_mxfp4(n_(a), n_(asf)), X.dequant_mxfp4(n_(b), n_(bsf))
+        ref, s = a_ @ b_.T, np.abs(a_) @ np.abs(b_).T
+        assert (np.abs(bf16_bits_to_f64(bits(got)) - ref) <= 2.0 ** -8 * np.abs(ref) + (k / 8 + 1) * 2.0 ** -23 * (1 + 2.0 ** -8) * s).all()
+    ty, tsy = X.quantize_mxfp4_transposed(bf16_bits_to_f64(bits(y)))
+    assert np.array_equal(n_(yt), ty) and np.array_equal(n_(yst), tsy)
+    check_back((bits(dx), n_(dweight).astype(np.float64)), bits(dn), dh, bits(h), wn, n_(rstd))
