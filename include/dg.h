@@ -419,7 +419,7 @@ int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t* sf, uint8_
  * The products of a linear layer's training step are all of this form, on the
  * operands that dg_quantize_mxfp4 makes from x [T, K], w [N, K] and dy [T, N]:
  * y = q(x) . q(w)^T, dx = q(dy) . qt(w)^T, dw = qt(dy) . qt(x)^T.
- * An exponent byte 255 gives NaN results; sums below 2^-126 are flushed to zero.
+ * An exponent byte 255 gives NaN results.  Subnormal products, sums and results are kept.
  * Requirements: m, n, k > 0; k % 128 == 0; n % 16 == 0; m*k/2, n*k/2, 2*m*n and the scales'
  *   bytes m*k/32 and n*k/32 at most 2^31, else DG_ERR_UNSUPPORTED.
  */

@@ -108,3 +108,22 @@ def test_split_calls_on_two_streams(dg, monkeypatch):
     torch.cuda.synchronize()
     for i, g in got:
         assert torch.equal(g, want[i])
+
+
+@pytest.mark.parametrize("kernel,m,n,k", [(100, 9, 48, 640), (101, 30, 48, 640), (0, 300, 272, 384), (1, 140, 272, 640), (2, 512, 528, 8192),
+                                          (3, 70, 144, 384), (4, 70, 144, 640), (5, 100, 144, 640), (6, 70, 144, 384), (7, 130, 144, 640)])
+@pytest.mark.parametrize("e", [-138, -143, -148])
+def test_subnormal_sums_are_kept(dg, monkeypatch, kernel, m, n, k, e):
+    """Integers times 2^e: products, sums and C below 2^-126 are exact down to fp32's last bit, 2^-149, and D is their
+    rounding to bf16, whose own last bit is 2^-133 (also through split K's partial sums: kernel 2)."""
+    monkeypatch.setenv("DG_FORCE_MXFP4", str(kernel))
+    assert kernel != 2 or dg.dg_mxfp4_gemm_workspace_bytes(m, n, k) > 0
+    a, sa, b, sb, _ = integers(k + m, m, n, k, False)
+    one = lambda t, by: (t.view(np.uint8) + np.uint8(by % 256)).view(np.int32)     # noqa: E731  (both bytes stay in range)
+    sa, sb = one(sa, -60), one(sb, e + 60)
+    rng = np.random.default_rng(m)
+    c = rng.integers(0, 256, (m, n)).astype(np.uint16) | (rng.integers(0, 2, (m, n)).astype(np.uint16) << 15)
+    want = X.mxfp4_gemm_nt(a, sa, b, sb, c)
+    small = (np.abs(want) < 2.0 ** -126) & (want != 0)
+    assert small.mean() > 0.2
+    check_bit_exact(run_gemm(dg, a, sa, b, sb, c), want, f"{kernel} {e}")
