@@ -82,18 +82,60 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
 // a scale of 2^-126 or more (448 * 2^-126).
 constexpr uint32_t kExactLo = 27u << 23, kExactHi = 227u << 23, kNormalScale = 0x04e00000u;
 
+// y is rounded twice, to fp32 and to its code.  So that the second rounding goes to the
+// nearer side, the first one goes to odd: toward zero, with the last bit set where anything
+// was cut off (midpoints of codes and borders between scales have five significant bits
+// at most, so that an odd y is never one of them).  r is the sum of two fp32 numbers, which
+// leaves 2^-48 of y; lo is not 0, so that no product is exact but 0, which becomes 2^-149
+// of its sign and has code 0 all the same.  (With fp32 roundings of r and y one code in
+// four million differed from y's in 64 bits; 8192 x 7168 74.3 us, UE8M0, 74.8 without.)
+struct TwoFloats {
+  float hi, lo;
+};
+__device__ __forceinline__ float odd(float truncated) { return __uint_as_float(__float_as_uint(truncated) | 1u); }
+__device__ __forceinline__ void times_odd(const float (&product)[9], TwoFloats r, float (&y)[9]) {
+  float t[9];
+#pragma unroll
+  for (int e = 0; e < 9; ++e) t[e] = product[e] * r.lo;
+  // (the rounding mode of fp32 is set within the block, which the compiler cannot enter)
+  asm("s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 3\n\t"
+      "v_fma_f32 %0, %9, %18, %19\n\t"
+      "v_fma_f32 %1, %10, %18, %20\n\t"
+      "v_fma_f32 %2, %11, %18, %21\n\t"
+      "v_fma_f32 %3, %12, %18, %22\n\t"
+      "v_fma_f32 %4, %13, %18, %23\n\t"
+      "v_fma_f32 %5, %14, %18, %24\n\t"
+      "v_fma_f32 %6, %15, %18, %25\n\t"
+      "v_fma_f32 %7, %16, %18, %26\n\t"
+      "v_fma_f32 %8, %17, %18, %27\n\t"
+      "s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 0"
+      : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7]), "=&v"(y[8])
+      : "v"(product[0]), "v"(product[1]), "v"(product[2]), "v"(product[3]), "v"(product[4]), "v"(product[5]), "v"(product[6]),
+        "v"(product[7]), "v"(product[8]), "v"(r.hi), "v"(t[0]), "v"(t[1]), "v"(t[2]), "v"(t[3]), "v"(t[4]), "v"(t[5]), "v"(t[6]),
+        "v"(t[7]), "v"(t[8]));
+#pragma unroll
+  for (int e = 0; e < 9; ++e) y[e] = odd(y[e]);
+}
+__device__ __forceinline__ float fp64_to_odd(double v) {
+  const float f = (float)v;
+  const uint32_t u = __float_as_uint(f);
+  if ((double)f == v || f == 0.f || !(fabsf(f) < INFINITY)) return f;   // (below fp32's least: 0)
+  return odd(__uint_as_float(fabs((double)f) > fabs(v) ? u - 1 : u));
+}
+
 // y = h * weight * r of one vector where the product may have left fp32's range (or the
-// block is zeros or not finite): the 40-bit product is exact in fp64 and rounded once.
-// Returns the pattern of max |y| over the block's LANES lanes, which all take part.
-template <int LANES>
-__device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, float r, float (&y)[8]) {
+// block is zeros or not finite), in fp64, rounded to odd (ODD) or to nearest.  Returns the
+// pattern of max |y| over the block's LANES lanes, which all take part.
+template <int LANES, bool ODD>
+__device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, double r, float (&y)[9]) {
   float a[8], w[8];
   unpack_bf16x8(h, a);
   unpack_bf16x8(weight, w);
   uint32_t amax = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    y[e] = (float)((double)a[e] * (double)w[e] * (double)r);
+    const double v = (double)a[e] * (double)w[e] * r;
+    y[e] = ODD ? fp64_to_odd(v) : (float)v;
     amax = umax(amax, abs_bits(y[e]));
   }
   return group_max<LANES>(amax);
@@ -121,7 +163,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
       wv[i] = reinterpret_cast<const v4i*>(p.weight)[j];
     }
   }
-  float ss = 0.f;
+  double ss = 0;   // (the squares of bf16 numbers are exact in fp64, and its range holds them)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int j = i * nt + tid;
@@ -137,43 +179,51 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
     }
     if (p.h && j < nv) reinterpret_cast<v4i*>(p.h)[base + j] = hv[i];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+    for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
   }
-  // the sum between threads and r in 64 bits, rounded once: a code near a border follows
-  // y = (h * weight) * r, whose first product is exact (two bf16 values)
-  const float r = (float)(1.0 / sqrt(block_sum((double)ss, red) * p.inv_k + (double)p.eps));
+  // the sum and r in 64 bits: a code near a border follows y = (h * weight) * r, whose first
+  // product is exact (two bf16 values)
+  const double r64 = 1.0 / sqrt(block_sum(ss, red) * p.inv_k + (double)p.eps);
+  const float r = (float)r64;
+  const TwoFloats r2 = {r, (float)(r64 - (double)r)};
+  const bool two = r >= 0x1p-100f && r2.lo != 0.f;   // (r in one number, or subnormal: by way of fp64)
   if (p.rstd && tid == 0) p.rstd[row] = r;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int j = i * nt + tid;   // (j >= nv: whole groups of 16 lanes; their vectors are zeros)
     const bool in = j < nv;
-    float y[8], w[8];
-    unpack_bf16x8(hv[i], y);
+    float hf[8], w[8], prod[9], y[9];   // (the ninth: the block's largest)
+    unpack_bf16x8(hv[i], hf);
     unpack_bf16x8(wv[i], w);
     uint32_t pmax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] *= w[e];
-      pmax = umax(pmax, abs_bits(y[e]));
+      prod[e] = hf[e] * w[e];
+      pmax = umax(pmax, abs_bits(prod[e]));
     }
     const int kb = j >> 4;
-    pmax = group_max<FMT == DG_QUANT_MXFP4 ? 4 : 16>(pmax);
-    uint32_t amax = abs_bits(__uint_as_float(pmax) * r);   // of max |y|: rounding keeps the order
-    bool exact = false;   // y holds the products, and they are as exact as the quotients need
+    constexpr int LANES = FMT == DG_QUANT_MXFP4 ? 4 : 16;
+    pmax = group_max<LANES>(pmax);
+    const float ptop = __uint_as_float(pmax);
+    bool exact = false;   // the fp32-scale format's quotients are formed from the products
+    uint32_t amax;        // of max |y|: rounding keeps the order
     if constexpr (FMT == DG_QUANT_E4M3_F32) {
+      amax = abs_bits(ptop * r);
       exact = pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u;
-      if (!exact) amax = y_by_fp64<16>(hv[i], wv[i], r, y);
-    } else if (pmax >= kExactLo && pmax < 0x7f800000u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= r;
+      if (__builtin_expect(!exact, 0)) amax = y_by_fp64<LANES, false>(hv[i], wv[i], r64, y);
+    } else if (__builtin_expect(pmax >= kExactLo && pmax < 0x7f800000u && ptop * r >= 0x1p-126f && two, 1)) {
+      prod[8] = ptop;
+      times_odd(prod, r2, y);
+      amax = abs_bits(y[8]);
     } else {
-      amax = y_by_fp64<FMT == DG_QUANT_MXFP4 ? 4 : 16>(hv[i], wv[i], r, y);
+      amax = y_by_fp64<LANES, true>(hv[i], wv[i], r64, y);
     }
     if constexpr (FMT == DG_QUANT_MXFP4) {
       const uint32_t byte = ue8m0_byte<false>(amax);
       const uint32_t word = scale_word(byte);
+      const float v8[8] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
       if (in) {
-        static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
+        static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(v8, ue8m0_value(byte));
         if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
       }
     } else {
@@ -186,12 +236,12 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
         // data).  The quotient by a reciprocal is corrected by its remainder, which is exact:
         // a tie comes out as itself and goes to the even code.  (y / s in fp32 decides one
         // tie in six by the roundings of y and s.)
-        if (exact) {
-          const float t = __uint_as_float(pmax), it = __builtin_amdgcn_rcpf(t);
+        if (__builtin_expect(exact, 1)) {
+          const float it = __builtin_amdgcn_rcpf(ptop);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float n = y[e] * 448.0f, q0 = n * it;
-            y[e] = fmaf(fmaf(-q0, t, n), it, q0);
+            const float n = prod[e] * 448.0f, q0 = n * it;
+            y[e] = fmaf(fmaf(-q0, ptop, n), it, q0);
           }
         } else {
           const float inv = amax == 0 || amax >= 0x7f800000u ? s : fminf(448.0f / top, 0x1p126f);   // (NaN: so are the codes)

@@ -436,8 +436,8 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  * RMS norm with the residual's addition and a quantised output, the step in front
  * of a layer's GEMM.  Per row:
  *   h = bf16(x + residual)                 (residual NULL: h = x)
- *   r = 1 / sqrt(mean(h^2) + eps)          fp32
- *   y = h * r * weight                     fp32, not rounded before it is quantised
+ *   r = 1 / sqrt(mean(h^2) + eps)
+ *   y = h * r * weight
  * and y is quantised in the format the GEMM behind it reads:
  *   DG_QUANT_E4M3_F32    q [m, k] e4m3, sf [k/128, m] fp32: s = max|y| / 448 per 1x128 block (at
  *                        least 2^-126; 1 where the block is all zeros), code = e4m3 nearest to
@@ -447,12 +447,13 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *                        with 448 * 2^e >= max|y| per 1x128 block (2^0 for zeros and for the
  *                        unused bytes of the last word): A of the _ue8m0 forms, x of the FFN
  *   DG_QUANT_MXFP4       q [m, k/2], sf [k/128, m] int32 as dg_quantize_mxfp4: A of dg_mxfp4_gemm_nt
- * A block of y with a NaN or an infinity gets a NaN scale; its codes are NaN (e4m3)
- * or 0 (E2M1).  Squares are formed and first added in fp32: a row whose squares pass
- * its range gives r = 0.
+ * Neither r nor y is rounded to fewer than 46 bits before codes and power-of-two scales
+ * are taken from it: they are those of the exact y.  (Magnitudes of y up to 2^-150 count
+ * as 0.)  A block of y with a NaN, an infinity or a number that passes fp32's range gets a
+ * NaN scale; its codes are NaN (e4m3) or 0 (E2M1).
  *   x, residual [m, k]  bf16; weight [k] bf16
  *   h           [m, k]  bf16 output, or NULL; may be x or residual itself (in place)
- *   rstd        [m]     fp32 output r, or NULL (the backward pass needs it)
+ *   rstd        [m]     fp32 output, r rounded, or NULL (the backward pass needs it)
  * Requirements: m, k > 0, eps > 0 and finite; k % 128 == 0, k <= 32768 and m times the
  *   threads of a row (k/8 rounded up to 64, at most 1024) below 2^32 (else
  *   DG_ERR_UNSUPPORTED); 16-byte aligned tensors (sf and rstd: 4).

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from oracle import mx as X
-from oracle.formats import bf16_bits_to_f64, decode_e4m3, f64_to_bf16_bits
+from oracle.formats import bf16_bits_to_f64, decode_e4m3, f64_to_bf16_bits, pow2_scale_exponent
 from tests.helpers import bits
 from tests.test_gpu_mxfp4 import guarded
 
@@ -431,14 +431,11 @@ def test_norm_rows_do_not_depend_on_the_batch(dg, k, fmt):
 
 @pytest.mark.parametrize("m,k", [(3, 128), (40, 2048), (9, 7168), (5, 32768)])
 def test_norm_rstd(dg, m, k):
-    """A thread adds at most 32 squares (8 up to k = 2048, 16 up to 8192) in fp32, each addition off by half a step of a
-    sum that is at most the whole: 32 * 2^-24 of it, half of that in 1/sqrt, and r's own rounding; the sum between
-    threads is in 64 bits."""
-    per = 8 if k <= 2048 else 16 if k <= 8192 else 32
+    """r is formed in 64 bits (squares of bf16 numbers are exact there) and rounded once: half a place, 2^-24 of it."""
     x, res, w = bf(110, m, k, scale=3.0), bf(111, m, k), bf(112, k)
     _, _, hb, rstd = run_norm(dg, x, res, w, UE8M0)
     r = 1 / np.sqrt(np.mean(bf16_bits_to_f64(hb) ** 2, axis=1) + float(np.float32(1e-6)))
-    assert (np.abs(rstd - r) <= (per / 2 + 1) * 2.0 ** -24 * (1 + 2.0 ** -20) * r).all()
+    assert (np.abs(rstd - r) <= 2.0 ** -24 * (1 + 2.0 ** -20) * r).all()
 
 
 def test_block_of_calls_keeps_rstd_and_feeds_the_fp32_scale_gemm(dg):
@@ -487,3 +484,35 @@ def test_training_step_with_the_weight_gradient(dg):
     ty, tsy = X.quantize_mxfp4_transposed(bf16_bits_to_f64(bits(y)))
     assert np.array_equal(n_(yt), ty) and np.array_equal(n_(yst), tsy)
     check_back((bits(dx), n_(dweight).astype(np.float64)), bits(dn), dh, bits(h), wn, n_(rstd))
+
+
+@pytest.mark.parametrize("fmt", [UE8M0, MX])
+@pytest.mark.parametrize("m,k", [(3, 7168), (300, 7168), (1000, 2048), (40, 32768)])
+def test_power_of_two_scales_and_codes_are_the_nearest(dg, m, k, fmt):
+    """Codes and scales are bit for bit those of y in float64: an r of 48 bits moves y by 2^-48 of itself, float64 by 2^-51,
+    and of these few million values none lies as near as 2^-40 to a midpoint of two codes (asserted).  The roundings of
+    r and y to fp32 would decide one code in some two million."""
+    x, res, w = bf(120 + m, m, k, scale=2.0), bf(121, m, k), f64_to_bf16_bits(1 + 0.2 * np.random.default_rng(3).standard_normal(k))
+    q, sf, hb, _ = run_norm(dg, x, res, w, fmt)
+    h = bf16_bits_to_f64(hb)
+    y = h * (1 / np.sqrt(np.mean(h * h, axis=1, keepdims=True) + float(np.float32(1e-6)))) * bf16_bits_to_f64(w)
+    blk, grid = (32, X.E2M1_GRID) if fmt == MX else (128, X.E4M3_GRID)
+    b = np.abs(y).reshape(m, k // blk, blk)
+    e = pow2_scale_exponent(b.max(axis=2), grid[-1])
+    assert np.array_equal(block_scales(sf, fmt, m, k), np.exp2(e))
+    v = np.ldexp(b, -e[..., None]).reshape(m, k)
+    mids = (grid[1:] + grid[:-1]) / 2
+    near = np.abs(v - mids[np.minimum(np.searchsorted(mids, v), len(mids) - 1)])
+    assert (np.minimum(near, np.abs(v - mids[np.maximum(np.searchsorted(mids, v) - 1, 0)])) > 2.0 ** -40 * v).all()
+    want = X.nearest_code(v, grid).astype(np.uint8)
+    got = np.stack([q & 15, q >> 4], axis=-1).reshape(m, k) if fmt == MX else q
+    assert np.array_equal(got & (7 if fmt == MX else 127), want), f"{np.count_nonzero((got & (7 if fmt == MX else 127)) != want)} codes"
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+def test_norm_squares_outside_fp32(dg, fmt):
+    """Rows whose squares pass fp32's range, at either end."""
+    m, k = 4, 1024
+    x, w = bf(130, m, k), f64_to_bf16_bits(1 + 0.2 * np.random.default_rng(3).standard_normal(k))
+    x[1], x[2], x[3] = bf(131, k, scale=2.0 ** 100), bf(132, k, scale=2.0 ** 122), bf(133, k, scale=2.0 ** -90)
+    check_norm(run_norm(dg, x, None, w, fmt, eps=2.0 ** -126), x, None, w, fmt, 2.0 ** -126)
