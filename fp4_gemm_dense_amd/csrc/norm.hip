@@ -78,9 +78,11 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
 
 // Bounds of max |h * weight|, 2^-100 .. 2^100.  From the lower one on the products of a
 // block are exact (one that is subnormal beside the largest has code 0); within both no
-// step of the fp32-scale format's quotients leaves fp32's normal range.  And of max |y| for
-// a scale of 2^-126 or more (448 * 2^-126).
+// step of the fp32-scale format's quotients leaves fp32's normal range.  And of max |y|: for
+// a scale of 2^-126 or more (448 * 2^-126), and 2^-126 .. 2^127, where truncating it leaves
+// neither 0 nor the largest number for what is past them.
 constexpr uint32_t kExactLo = 27u << 23, kExactHi = 227u << 23, kNormalScale = 0x04e00000u;
+constexpr uint32_t kNormalLo = 1u << 23, kNormalHi = 254u << 23;
 
 // y is rounded twice, to fp32 and to its code.  So that the second rounding goes to the
 // nearer side, the first one goes to odd: toward zero, with the last bit set where anything
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
       amax = abs_bits(ptop * r);
       exact = pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u;
       if (__builtin_expect(!exact, 0)) amax = y_by_fp64<LANES, false>(hv[i], wv[i], r64, y);
-    } else if (__builtin_expect(pmax >= kExactLo && pmax < 0x7f800000u && ptop * r >= 0x1p-126f && two, 1)) {
+    } else if (__builtin_expect((pmax >= kExactLo) & (abs_bits(ptop * r) - kNormalLo < kNormalHi - kNormalLo) & two, 1)) {
       prod[8] = ptop;
       times_odd(prod, r2, y);
       amax = abs_bits(y[8]);

@@ -516,3 +516,24 @@ def test_norm_squares_outside_fp32(dg, fmt):
     x, w = bf(130, m, k), f64_to_bf16_bits(1 + 0.2 * np.random.default_rng(3).standard_normal(k))
     x[1], x[2], x[3] = bf(131, k, scale=2.0 ** 100), bf(132, k, scale=2.0 ** 122), bf(133, k, scale=2.0 ** -90)
     check_norm(run_norm(dg, x, None, w, fmt, eps=2.0 ** -126), x, None, w, fmt, 2.0 ** -126)
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+def test_norm_values_past_fp32(dg, fmt):
+    """A y past fp32's range makes its block's scale NaN; the largest y that is inside it does not."""
+    m, k = 3, 512
+    x = bf(140, m, k, scale=2.0 ** -10)                                 # (h * weight stays inside)
+    w = f64_to_bf16_bits(np.ones(k))
+    w[200], w[300] = 0x7f7f, 0x7f7f                                     # 3.39e38
+    x[:, 200], x[:, 300] = f64_to_bf16_bits(np.float64(3 / 1024)), f64_to_bf16_bits(np.float64(0.5 / 1024))
+    q, sf, _, _ = run_norm(dg, x, None, w, fmt)
+    y = X.add_rms_norm(x, None, w, 1e-6)[2]
+    assert (np.abs(y[:, 200]) > 3.5e38).all() and (np.abs(y[:, 300]) < 3e38).all()
+    blk = 32 if fmt == MX else 128
+    nan = np.zeros((m, k // blk), dtype=bool)
+    nan[:, 200 // blk] = True
+    assert np.array_equal(np.isnan(block_scales(sf, fmt, m, k)), nan)
+    v = X.unpack_e2m1(q) if fmt == MX else decode_e4m3(q)
+    bad = np.repeat(nan, blk, axis=1)
+    assert (v[bad] == 0).all() if fmt == MX else np.isnan(v[bad]).all()
+    assert (np.abs(v[:, 300]) > (2 if fmt == MX else 200)).all()
