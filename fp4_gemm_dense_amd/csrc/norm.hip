@@ -78,9 +78,9 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
 
 // Bounds of max |h * weight|, 2^-100 .. 2^100.  From the lower one on the products of a
 // block are exact (one that is subnormal beside the largest has code 0); within both no
-// step of the fp32-scale format's quotients leaves fp32's normal range.  And of max |y|: for
-// a scale of 2^-126 or more (448 * 2^-126), and 2^-126 .. 2^127, where truncating it leaves
-// neither 0 nor the largest number for what is past them.
+// step of a quotient by them leaves fp32's normal range.  And of max |y|: for a scale of
+// 2^-126 or more (448 * 2^-126), and 2^-126 .. 2^127, where truncating it leaves neither 0
+// nor the largest number for what is past them.
 constexpr uint32_t kExactLo = 27u << 23, kExactHi = 227u << 23, kNormalScale = 0x04e00000u;
 constexpr uint32_t kNormalLo = 1u << 23, kNormalHi = 254u << 23;
 
@@ -90,46 +90,51 @@ constexpr uint32_t kNormalLo = 1u << 23, kNormalHi = 254u << 23;
 // at most, so that an odd y is never one of them).  r is the sum of two fp32 numbers, which
 // leaves 2^-48 of y; lo is not 0, so that no product is exact but 0, which becomes 2^-149
 // of its sign and has code 0 all the same.  (With fp32 roundings of r and y one code in
-// four million differed from y's in 64 bits; 8192 x 7168 74.3 us, UE8M0, 74.8 without.)
+// four million differed from y's in 64 bits.  It costs some 1 % of a long row and 5 % of a
+// short one, a third of it for the squares in fp64: 8192 x 7168 with UE8M0 scales 72.3 ->
+// 73.0 us, 8192 x 512 7.5 -> 7.9, 65536 x 128, which the vector ALUs bound, 22.6 -> 25.4.)
 struct TwoFloats {
   float hi, lo;
 };
-__device__ __forceinline__ float odd(float truncated) { return __uint_as_float(__float_as_uint(truncated) | 1u); }
-__device__ __forceinline__ void times_odd(const float (&product)[9], TwoFloats r, float (&y)[9]) {
-  float t[9];
+__device__ __forceinline__ void times_odd(const float (&product)[8], TwoFloats r, float (&y)[8]) {
+  float t[8];
 #pragma unroll
-  for (int e = 0; e < 9; ++e) t[e] = product[e] * r.lo;
+  for (int e = 0; e < 8; ++e) t[e] = product[e] * r.lo;
   // (the rounding mode of fp32 is set within the block, which the compiler cannot enter)
   asm("s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 3\n\t"
-      "v_fma_f32 %0, %9, %18, %19\n\t"
-      "v_fma_f32 %1, %10, %18, %20\n\t"
-      "v_fma_f32 %2, %11, %18, %21\n\t"
-      "v_fma_f32 %3, %12, %18, %22\n\t"
-      "v_fma_f32 %4, %13, %18, %23\n\t"
-      "v_fma_f32 %5, %14, %18, %24\n\t"
-      "v_fma_f32 %6, %15, %18, %25\n\t"
-      "v_fma_f32 %7, %16, %18, %26\n\t"
-      "v_fma_f32 %8, %17, %18, %27\n\t"
+      "v_fma_f32 %0, %8, %16, %17\n\t"
+      "v_fma_f32 %1, %9, %16, %18\n\t"
+      "v_fma_f32 %2, %10, %16, %19\n\t"
+      "v_fma_f32 %3, %11, %16, %20\n\t"
+      "v_fma_f32 %4, %12, %16, %21\n\t"
+      "v_fma_f32 %5, %13, %16, %22\n\t"
+      "v_fma_f32 %6, %14, %16, %23\n\t"
+      "v_fma_f32 %7, %15, %16, %24\n\t"
       "s_setreg_imm32_b32 hwreg(HW_REG_MODE, 0, 2), 0"
-      : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7]), "=&v"(y[8])
+      : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7])
       : "v"(product[0]), "v"(product[1]), "v"(product[2]), "v"(product[3]), "v"(product[4]), "v"(product[5]), "v"(product[6]),
-        "v"(product[7]), "v"(product[8]), "v"(r.hi), "v"(t[0]), "v"(t[1]), "v"(t[2]), "v"(t[3]), "v"(t[4]), "v"(t[5]), "v"(t[6]),
-        "v"(t[7]), "v"(t[8]));
+        "v"(product[7]), "v"(r.hi), "v"(t[0]), "v"(t[1]), "v"(t[2]), "v"(t[3]), "v"(t[4]), "v"(t[5]), "v"(t[6]), "v"(t[7]));
 #pragma unroll
-  for (int e = 0; e < 9; ++e) y[e] = odd(y[e]);
+  for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(__float_as_uint(y[e]) | 1u);
+}
+// The pattern of one positive product's y to odd, from its rounding to nearest.
+__device__ __forceinline__ uint32_t times_odd(float product, TwoFloats r) {
+  const float t = product * r.lo, y = fmaf(product, r.hi, t);
+  const float err = fmaf(product, r.hi, -y) + t;
+  return (__float_as_uint(y) - (__float_as_uint(err) >> 31)) | 1u;
 }
 __device__ __forceinline__ float fp64_to_odd(double v) {
   const float f = (float)v;
   const uint32_t u = __float_as_uint(f);
   if ((double)f == v || f == 0.f || !(fabsf(f) < INFINITY)) return f;   // (below fp32's least: 0)
-  return odd(__uint_as_float(fabs((double)f) > fabs(v) ? u - 1 : u));
+  return __uint_as_float((fabs((double)f) > fabs(v) ? u - 1 : u) | 1u);
 }
 
 // y = h * weight * r of one vector where the product may have left fp32's range (or the
 // block is zeros or not finite), in fp64, rounded to odd (ODD) or to nearest.  Returns the
 // pattern of max |y| over the block's LANES lanes, which all take part.
 template <int LANES, bool ODD>
-__device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, double r, float (&y)[9]) {
+__device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, double r, float (&y)[8]) {
   float a[8], w[8];
   unpack_bf16x8(h, a);
   unpack_bf16x8(weight, w);
@@ -188,82 +193,84 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
   const double r64 = 1.0 / sqrt(block_sum(ss, red) * p.inv_k + (double)p.eps);
   const float r = (float)r64;
   const TwoFloats r2 = {r, (float)(r64 - (double)r)};
-  const bool two = r >= 0x1p-100f && r2.lo != 0.f;   // (r in one number, or subnormal: by way of fp64)
+  // the products that the two numbers serve (none where r is one number, or subnormal)
+  const uint32_t span = r >= 0x1p-100f && r2.lo != 0.f ? kExactHi - kExactLo : 0u;
   if (p.rstd && tid == 0) p.rstd[row] = r;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int j = i * nt + tid;   // (j >= nv: whole groups of 16 lanes; their vectors are zeros)
     const bool in = j < nv;
-    float hf[8], w[8], prod[9], y[9];   // (the ninth: the block's largest)
-    unpack_bf16x8(hv[i], hf);
+    float y[8], w[8], prod[8];
+    unpack_bf16x8(hv[i], y);
     unpack_bf16x8(wv[i], w);
     uint32_t pmax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      prod[e] = hf[e] * w[e];
+      prod[e] = y[e] * w[e];
       pmax = umax(pmax, abs_bits(prod[e]));
     }
     const int kb = j >> 4;
     constexpr int LANES = FMT == DG_QUANT_MXFP4 ? 4 : 16;
     pmax = group_max<LANES>(pmax);
     const float ptop = __uint_as_float(pmax);
-    bool exact = false;   // the fp32-scale format's quotients are formed from the products
-    uint32_t amax;        // of max |y|: rounding keeps the order
+    // amax: of max |y| (rounding keeps the order)
     if constexpr (FMT == DG_QUANT_E4M3_F32) {
-      amax = abs_bits(ptop * r);
-      exact = pmax >= kExactLo && pmax <= kExactHi && amax >= kNormalScale && amax < 0x7f800000u;
-      if (__builtin_expect(!exact, 0)) amax = y_by_fp64<LANES, false>(hv[i], wv[i], r64, y);
-    } else if (__builtin_expect((pmax >= kExactLo) & (abs_bits(ptop * r) - kNormalLo < kNormalHi - kNormalLo) & two, 1)) {
-      prod[8] = ptop;
-      times_odd(prod, r2, y);
-      amax = abs_bits(y[8]);
-    } else {
-      amax = y_by_fp64<LANES, true>(hv[i], wv[i], r64, y);
-    }
-    if constexpr (FMT == DG_QUANT_MXFP4) {
-      const uint32_t byte = ue8m0_byte<false>(amax);
-      const uint32_t word = scale_word(byte);
-      const float v8[8] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
-      if (in) {
-        static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(v8, ue8m0_value(byte));
-        if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
-      }
-    } else {
-      if constexpr (FMT == DG_QUANT_E4M3_F32) {
-        const float top = __uint_as_float(amax);
-        const float s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(top / 448.0f, 0x1p-126f));
-        if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
-        // y / s is 448 (h w) / max |h w| wherever s is not at its least: r cancels, both
-        // products have 16 bits, and ties between two codes are common (1 in 2600 on normal
-        // data).  The quotient by a reciprocal is corrected by its remainder, which is exact:
-        // a tie comes out as itself and goes to the even code.  (y / s in fp32 decides one
-        // tie in six by the roundings of y and s.)
-        if (__builtin_expect(exact, 1)) {
-          const float it = __builtin_amdgcn_rcpf(ptop);
+      uint32_t amax = abs_bits(ptop * r);
+      const bool exact = pmax - kExactLo < kExactHi - kExactLo && amax - kNormalScale < 0x7f800000u - kNormalScale;
+      if (__builtin_expect(!exact & in, 0)) amax = y_by_fp64<LANES, false>(hv[i], wv[i], r64, y);
+      const float top = __uint_as_float(amax);
+      const float s = amax == 0 ? 1.0f : (amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fmaxf(top / 448.0f, 0x1p-126f));
+      if (in && (tid & 15) == 0) static_cast<float*>(p.sf)[(size_t)kb * p.m + row] = s;
+      // y / s is 448 (h w) / max |h w| wherever s is not at its least: r cancels, both
+      // products have 16 bits, and ties between two codes are common (1 in 2600 on normal
+      // data).  The quotient by a reciprocal is corrected by its remainder, which is exact:
+      // a tie comes out as itself and goes to the even code.  (y / s in fp32 decides one
+      // tie in six by the roundings of y and s.)
+      if (__builtin_expect(exact, 1)) {
+        const float it = __builtin_amdgcn_rcpf(ptop);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float n = prod[e] * 448.0f, q0 = n * it;
-            y[e] = fmaf(fmaf(-q0, ptop, n), it, q0);
-          }
-        } else {
-          const float inv = amax == 0 || amax >= 0x7f800000u ? s : fminf(448.0f / top, 0x1p126f);   // (NaN: so are the codes)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= inv;
+        for (int e = 0; e < 8; ++e) {
+          const float n = prod[e] * 448.0f, q0 = n * it;
+          y[e] = fmaf(fmaf(-q0, ptop, n), it, q0);
         }
       } else {
-        // the wave's four blocks make one word (past the end: 2^0)
-        const uint32_t byte = in ? ue8m0_byte<true>(amax) : 127u;
-        const float inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);   // 2^(127 - byte)
-        uint32_t word = byte << (8 * ((tid >> 4) & 3));
-        word |= (uint32_t)__shfl_xor((int)word, 16, 64);
-        word |= (uint32_t)__shfl_xor((int)word, 32, 64);
-        if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
+        const float inv = amax == 0 || amax >= 0x7f800000u ? s : fminf(448.0f / top, 0x1p126f);   // (NaN: so are the codes)
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] *= inv;
       }
+    } else {
+      uint32_t amax = times_odd(ptop, r2), byte;
+      const bool two = ((pmax - kExactLo < span) & (amax - kNormalLo < kNormalHi - kNormalLo)) | !in;
+      if constexpr (FMT == DG_QUANT_MXFP4) {
+        if (__builtin_expect(two, 1)) times_odd(prod, r2, y);
+        else amax = y_by_fp64<LANES, true>(hv[i], wv[i], r64, y);
+        byte = ue8m0_byte<false>(amax);
+        const uint32_t word = scale_word(byte);
+        if (in) {
+          static_cast<uint32_t*>(p.q)[base + j] = byte == 255u ? 0u : e2m1x8(y, ue8m0_value(byte));
+          if ((tid & 15) == 0) static_cast<uint32_t*>(p.sf)[(size_t)kb * p.m + row] = word;
+        }
+        continue;
+      }
+      if (__builtin_expect(two, 1)) {
+        byte = in ? ue8m0_byte<true>(amax) : 127u;
+        const float inv = __uint_as_float((254u - byte) << 23);             // 2^(127 - byte)
+        times_odd(prod, TwoFloats{r2.hi * inv, r2.lo * inv}, y);            // (both products are exact)
+      } else {
+        byte = ue8m0_byte<true>(y_by_fp64<LANES, true>(hv[i], wv[i], r64, y));
+        const float inv = ue8m0_value(byte == 255u ? 255u : 254u - byte);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inv;
+      }
+      // the wave's four blocks make one word (past the end: 2^0)
+      uint32_t word = byte << (8 * ((tid >> 4) & 3));
+      word |= (uint32_t)__shfl_xor((int)word, 16, 64);
+      word |= (uint32_t)__shfl_xor((int)word, 32, 64);
+      if (in && (tid & 63) == 0) static_cast<uint32_t*>(p.sf)[(size_t)row * ((kb_n + 3) >> 2) + (kb >> 2)] = word;
+    }
+    if constexpr (FMT != DG_QUANT_MXFP4)
       if (in)
         static_cast<v2i*>(p.q)[base + j] = v2i{(int)e4m3x4(y[0], y[1], y[2], y[3]), (int)e4m3x4(y[4], y[5], y[6], y[7])};
-    }
   }
 }
 
