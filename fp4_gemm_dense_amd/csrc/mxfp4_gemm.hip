@@ -28,21 +28,28 @@
 //     (a stage's chain of barrier, reads and products is 0.5-0.6 us however small; 200 x
 //     4096 x 7168 18.4 us on 64x128 with one group, 12.6 with two, 10.7 on 64x64).
 //
-// Measured (one MI355X, operands not in L2): 8192 x 8192 x 8192 247-252 us (4.4
-// PFLOP/s), 4096 x 7168 x 16384 222-238 us, 4096 x 4096 x 7168 58-65 us, all on 256x256;
-// 1111 x 2112 x 7168 19 us on 96x128; 200 x 4096 x 7168 10.8 us on 64x64.  What bounds
-// the large ones is power: on random codes the clock holds 1.8-2.0 GHz with the matrix
-// cores 49-61 % busy, and the same call on zeros runs at 2.4 GHz (4096 x 7168 x 16384
-// 178 us; matrix instructions alone reach 6.8 PFLOP/s on random codes and 9.6 on zeros).
+// Measured (one MI355X, a kernel trace on quantised normal values, operands not in L2; such
+// times differ by 5 % from card to card): 8192 x 8192 x 8192 247-260 us (4.2-4.5 PFLOP/s),
+// 4096 x 7168 x 16384 235-265, 4096 x 4096 x 7168 58-62, all on 256x256; 1111 x 2112 x 7168
+// 19.5-20.5 on 96x128; 200 x 4096 x 7168 11.5-12 on 64x64.  What bounds the large ones is
+// the schedule first and power second: the matrix cores are busy in half of the cycles
+// whatever the codes, at 1.8-2.0 GHz on normal values and at 2.3 GHz on zeros (4096 x 7168
+// x 16384 200 us there), while matrix instructions alone reach 6.8 PFLOP/s on random codes
+// at the clock that power leaves them and 9.6 on zeros (100 us).  A short K pays the end of
+// a unit besides: 4.5 us of a 256x256 one, its stores waited for one stage after their
+// issue by all CUs at once (4096 x 24576 x 1536 105 us, its products alone 45).
 // Timing copies without the stage copies ran 20 % faster, without the barrier 6 %,
 // without the scales 6 %, without the fragment reads 11 %, without any of them 6.4
 // PFLOP/s; waiting for fewer copies, or copying from L2 only, changed 1 and 3-8 %.  The
 // middle sizes (one 96x128 tile per workgroup) wait for copies: from L2 only they ran 12
-// % faster.  Tried without gain: four waves of 128x128 each (fewer LDS reads per matrix
+// % faster; and where tiles fill just over half of the CUs the others have nothing to do
+// (4096 x 2112 x 7168, 144 tiles, 51 us; split_rule takes no K slices there).
+// Tried without gain: four waves of 128x128 each (fewer LDS reads per matrix
 // instruction, but the accumulators take half of the registers and the rest spills: 3-8
 // % slower), only half of the waves copying, more of a stage's copies put off into the
 // next one, loads that pull the next stage into L2, a later barrier, raised wave
-// priority, other raster bands, a 256x224 tile.
+// priority, other raster bands, a 256x224 tile.  Not tried: non-temporal stores of D,
+// stages of one K block in more slots, tiles of 128x192 and 192x192.
 #include <algorithm>
 #include <cstdio>
 #include <cstdlib>
@@ -574,8 +581,8 @@ static hipError_t launch_mxfp4_tile(const Mxfp4Params& p, int id, int grid, hipS
 // of 16); its four waves split K between them, pair of K blocks by pair (a 128-byte
 // line of each row), with fragments and scale words loaded straight into registers, P
 // pairs ahead.  The waves' sums meet in LDS, added in wave order, so no second launch
-// and no workspace is needed.  (1 x 4096 x 7168: 5.9 us, 2.7 of them the launch, at 4.9
-// TB/s of B in between; 32 x 4096 x 7168 8.3 us; eight waves and 32 columns measured 4-40 % slower.)
+// and no workspace is needed.  (1 x 4096 x 7168: 6.1 us, 2.7 of them the launch, at 4.6
+// TB/s of B in between; 32 x 4096 x 7168 8.3-8.5 us, 32 x 1024 x 8192 8.5-9, on 64 workgroups; eight waves and 32 columns measured 4-40 % slower.)
 // ---------------------------------------------------------------------------
 extern "C" __device__ int dg_raw_buffer_load_i32_mx(v4i rsrc, int voffset, int soffset,
                                                     int aux) __asm("llvm.amdgcn.raw.buffer.load.i32");

@@ -8,10 +8,13 @@
 // Backward, with n = h * r and g = dy * weight: dx = dh + r (g - n mean(g n)),
 // dweight = sum over rows of dy * n.
 //
-// Bound: HBM (forward 7 bytes per element with a residual, backward 8).  Measured (one
-// MI355X, inputs not in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168
-// 71 us MXFP4, 74 UE8M0, 76 fp32 scales (5.4-5.6 TB/s), 3 x 7168 3.7 us, of which the
-// launch is 2.7; backward 4096 x 7168 49 us (4.8 TB/s), 130 x 2048 3.5 us.
+// Bound: HBM (forward 7 bytes per element with a residual, backward 8); rows of up to some
+// 512 by the waves they take, one or two of them a row.  Measured (one MI355X, inputs not
+// in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168 70 us MXFP4, 74 UE8M0,
+// 76 fp32 scales (5.4-5.6 TB/s), 8192 x 512 7.8-8.3 (floor 5.5), 65536 x 128 26-27 (floor
+// 11: 16 of a wave's 64 lanes have values), 3 x 7168 3.9, of which the launch is 2.7;
+// backward 4096 x 7168 46.5 us in both kernels (5.1 TB/s), 8192 x 512 15, 65536 x 128 51
+// (floors 6.5 and 13: at most 1024 workgroups walk the rows), 130 x 2048 3.9.
 #include <algorithm>
 #include <cmath>
 

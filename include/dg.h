@@ -418,7 +418,10 @@ int dg_quantize_mxfp4(const void* x, int x_type, uint8_t* q, int32_t* sf, uint8_
  *         16-byte aligned; may be NULL when that is 0.
  * The products of a linear layer's training step are all of this form, on the
  * operands that dg_quantize_mxfp4 makes from x [T, K], w [N, K] and dy [T, N]:
- * y = q(x) . q(w)^T, dx = q(dy) . qt(w)^T, dw = qt(dy) . qt(x)^T.
+ * y = q(x) . q(w)^T, dx = q(dy) . qt(w)^T, dw = qt(dy) . qt(x)^T.  (Behind
+ * dg_add_rms_norm x is the norm's y, which leaves it as codes along K only: for dw the
+ * caller forms h * rstd * weight and quantises that.)  D is bf16, dw too: adding up
+ * micro-batches through c rounds their sum to bf16 each time.
  * An exponent byte 255 gives NaN results.  Subnormal products, sums and results are kept.
  * Requirements: m, n, k > 0; k % 128 == 0; n % 16 == 0; m*k/2, n*k/2, 2*m*n and the scales'
  *   bytes m*k/32 and n*k/32 at most 2^31, else DG_ERR_UNSUPPORTED.
@@ -449,8 +452,9 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *   DG_QUANT_MXFP4       q [m, k/2], sf [k/128, m] int32 as dg_quantize_mxfp4: A of dg_mxfp4_gemm_nt
  * Neither r nor y is rounded to fewer than 46 bits before codes and power-of-two scales
  * are taken from it: they are those of the exact y.  (Magnitudes of y up to 2^-150 count
- * as 0.)  A block of y with a NaN, an infinity or a number that passes fp32's range gets a
- * NaN scale; its codes are NaN (e4m3) or 0 (E2M1).
+ * as 0; fp32-scale codes of a block whose largest |h * weight| is outside 2^-100 .. 2^100
+ * are those of a quotient within 2^-22.)  A block of y with a NaN, an infinity or a
+ * number that passes fp32's range gets a NaN scale; its codes are NaN (e4m3) or 0 (E2M1).
  *   x, residual [m, k]  bf16; weight [k] bf16
  *   h           [m, k]  bf16 output, or NULL; may be x or residual itself (in place)
  *   rstd        [m]     fp32 output, r rounded, or NULL (the backward pass needs it)
@@ -464,7 +468,7 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 
 /*
  * Its backward pass; the gradient passes straight through the quantisation.  With
- * n = h * r and g = dy * weight:
+ * n = h * r and g = dy * weight, in fp32 (a g past its range is an infinity):
  *   dx[i]      = bf16( dh[i] + r * (g[i] - n[i] * mean(g * n)) )   the gradient of x and of residual alike
  *   dweight[i] = sum over rows of dy[i] * n[i]                     fp32, summed in a fixed order
  *   dy      [m, k] bf16, the gradient of y; dh [m, k] bf16, the gradient that arrives at h from
