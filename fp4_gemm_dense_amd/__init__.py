@@ -52,6 +52,9 @@ _SIGNATURES = {
     "dg_add_rms_norm": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P]),
     "dg_add_rms_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
     "dg_add_rms_norm_backward_workspace_bytes": (_SZ, [_I, _I]),
+    "dg_sandwich_norm": (_I, [_P] * 8 + [_I, _P, _P, _I, _I, _I, ctypes.c_float, ctypes.c_float, _P]),
+    "dg_sandwich_norm_backward": (_I, [_P] * 14 + [_I, _I, _I, ctypes.c_float, _P, _SZ, _P]),
+    "dg_sandwich_norm_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "dg_fp8_gemm_nt_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "dg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "dg_set_num_cus": (_I, [_I]),
@@ -485,6 +488,13 @@ def _arg(t, dtypes, shape, index, name):
     raise ValueError(f"{name}: on device {t.get_device()}, expected {index}")
 
 
+def _req_given(t, dtypes, shape, index, name):
+    """_arg for an argument that cannot be None."""
+    if t is None:
+        raise TypeError(f"{name}: expected a tensor, got None")
+    return _arg(t, dtypes, shape, index, name)
+
+
 _empty = torch.empty_strided
 
 
@@ -583,6 +593,53 @@ def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace=Non
           _arg(h, _BF, shape, dev, "h"), _arg(weight, _BF, (k,), dev, "weight"), _arg(rstd, _F32S, (m,), dev, "rstd"),
           _arg(dx, _BF, shape, dev, "dx"), _arg(dweight, _F32S, (k,), dev, "dweight"), m, k,
           _arg(workspace, _U8S, (nbytes,), dev, "workspace"), nbytes)
+
+
+def _gate_shape(gate, gate_rows, m, k):
+    if gate is None:
+        return None
+    if gate_rows < 1:
+        raise ValueError(f"gate_rows: expected 1 or more, got {gate_rows}")
+    return ((m + gate_rows - 1) // gate_rows, k)
+
+
+def dg_sandwich_norm(x, residual, post_weight, gate, weight, h, q, sf, quant_format, rstd_x=None, rstd=None, gate_rows=1,
+                     scale=1.0, eps=1e-6):
+    """h = residual + scale * gate * norm(x) * post_weight; q, sf = quantised h / rms(h) * weight (see include/dg.h).
+    x, residual, h [m, k] bf16; post_weight, weight [k] and gate [ceil(m / gate_rows), k] bf16 (post_weight and gate may
+    be None); q, sf as dg_add_rms_norm; rstd_x, rstd [m] fp32 or None."""
+    m, k = x.shape
+    if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
+        raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
+    shape, dev, gshape = (m, k), x.get_device(), _gate_shape(gate, gate_rows, m, k)
+    sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
+    _call("dg_sandwich_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
+          _arg(post_weight, _BF, (k,), dev, "post_weight"), _arg(gate, _BF, gshape, dev, "gate"),
+          _arg(weight, _BF, (k,), dev, "weight"), _arg(h, _BF, shape, dev, "h"),
+          _arg(q, _U8S, (m, k // 2) if quant_format == QUANT_MXFP4 else shape, dev, "q"),
+          _arg(sf, _F32S if quant_format == QUANT_E4M3_F32 else _I32S, sf_shape, dev, "sf"), quant_format,
+          _arg(rstd_x, _F32S, (m,), dev, "rstd_x"), _arg(rstd, _F32S, (m,), dev, "rstd"), m, k, gate_rows, scale, eps)
+
+
+def dg_sandwich_norm_backward_workspace_bytes(m, k, with_post_weight=True, with_gate=True):
+    return int(lib().dg_sandwich_norm_backward_workspace_bytes(m, k, int(with_post_weight), int(with_gate)))
+
+
+def dg_sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rstd_x, rstd, dx, dresidual, dweight, dpost_weight,
+                              dgate, workspace, gate_rows=1, scale=1.0):
+    """dx, dresidual [m, k] bf16, dweight and dpost_weight [k] and dgate [ceil(m / gate_rows), k] fp32 of dg_sandwich_norm
+    (see include/dg.h); dh may be None, post_weight, rstd_x and dpost_weight together, and gate and dgate.  workspace:
+    uint8 device tensor of at least dg_sandwich_norm_backward_workspace_bytes(...) bytes."""
+    m, k = dy.shape
+    shape, dev, gshape = (m, k), dy.get_device(), _gate_shape(gate, gate_rows, m, k)
+    nbytes = workspace.numel()
+    _call("dg_sandwich_norm_backward", dev, _arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"),
+          _arg(x, _BF, shape, dev, "x"), _arg(h, _BF, shape, dev, "h"), _arg(post_weight, _BF, (k,), dev, "post_weight"),
+          _arg(gate, _BF, gshape, dev, "gate"), _arg(weight, _BF, (k,), dev, "weight"),
+          _arg(rstd_x, _F32S, (m,), dev, "rstd_x"), _arg(rstd, _F32S, (m,), dev, "rstd"), _arg(dx, _BF, shape, dev, "dx"),
+          _arg(dresidual, _BF, shape, dev, "dresidual"), _arg(dweight, _F32S, (k,), dev, "dweight"),
+          _arg(dpost_weight, _F32S, (k,), dev, "dpost_weight"), _arg(dgate, _F32S, gshape, dev, "dgate"), m, k, gate_rows,
+          scale, _arg(workspace, _U8S, (nbytes,), dev, "workspace"), nbytes)
 
 
 def dg_get_mk_alignment_for_contiguous_layout():
@@ -738,6 +795,50 @@ def add_rms_norm_backward(dy, dh, h, weight, rstd):
         wp = ws.data_ptr()
     _call("dg_add_rms_norm_backward", index, *ins, dx.data_ptr(), dweight.data_ptr(), m, k, wp, nbytes)
     return dx, dweight
+
+
+def sandwich_norm(x, residual, post_weight, gate, weight, scale=1.0, gate_rows=None, eps=1e-6,
+                  quant_format=QUANT_E4M3_F32):
+    """(q, sf, h, rstd_x, rstd): h = residual + scale * gate * norm(x) * post_weight and its quantised norm.  gate:
+    [ceil(m / gate_rows), k] (gate_rows None: one row for all rows of x), or None; post_weight None: x is not normed, and
+    rstd_x None."""
+    m, k = x.shape
+    gate_rows = max(m, 1) if gate_rows is None else gate_rows
+    shape, index, dev, gshape = (m, k), x.get_device(), x.device, _gate_shape(gate, gate_rows, m, k)
+    ins = (_arg(x, _BF, shape, index, "x"), _req_given(residual, _BF, shape, index, "residual"),
+           _arg(post_weight, _BF, (k,), index, "post_weight"), _arg(gate, _BF, gshape, index, "gate"),
+           _req_given(weight, _BF, (k,), index, "weight"))
+    q = _new((m, k // 2) if quant_format == QUANT_MXFP4 else shape, _U8, dev)
+    if quant_format == QUANT_E4M3_UE8M0:
+        sf = _new((m, _kw(k)), torch.int32, dev)
+    else:
+        sf = _new((k // 128, m), torch.float32 if quant_format == QUANT_E4M3_F32 else torch.int32, dev)
+    h, rstd = torch.empty_like(x), _new((m,), torch.float32, dev)
+    rstd_x = None if post_weight is None else _new((m,), torch.float32, dev)
+    _call("dg_sandwich_norm", index, *ins, h.data_ptr(), q.data_ptr(), sf.data_ptr(), quant_format,
+          None if rstd_x is None else rstd_x.data_ptr(), rstd.data_ptr(), m, k, gate_rows, scale, eps)
+    return q, sf, h, rstd_x, rstd
+
+
+def sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rstd_x, rstd, scale=1.0, gate_rows=None):
+    """(dx, dresidual, dweight, dpost_weight, dgate) of sandwich_norm: dx and dresidual bf16, the others fp32
+    (dpost_weight and dgate None where post_weight and gate are)."""
+    m, k = dy.shape
+    gate_rows = max(m, 1) if gate_rows is None else gate_rows
+    shape, index, dev, gshape = (m, k), dy.get_device(), dy.device, _gate_shape(gate, gate_rows, m, k)
+    ins = (_arg(dy, _BF, shape, index, "dy"), _arg(dh, _BF, shape, index, "dh"), _req_given(x, _BF, shape, index, "x"),
+           _req_given(h, _BF, shape, index, "h"), _arg(post_weight, _BF, (k,), index, "post_weight"),
+           _arg(gate, _BF, gshape, index, "gate"), _req_given(weight, _BF, (k,), index, "weight"),
+           _arg(rstd_x, _F32S, (m,), index, "rstd_x"), _req_given(rstd, _F32S, (m,), index, "rstd"))
+    dx, dresidual, dweight = torch.empty_like(dy), torch.empty_like(dy), _new((k,), torch.float32, dev)
+    dpost = None if post_weight is None else _new((k,), torch.float32, dev)
+    dgate = None if gate is None else _new(gshape, torch.float32, dev)
+    nbytes = (_lib or load_library()).dg_sandwich_norm_backward_workspace_bytes(m, k, dpost is not None, dgate is not None)
+    ws = _new((nbytes,), _U8, dev)
+    _call("dg_sandwich_norm_backward", index, *ins, dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(),
+          None if dpost is None else dpost.data_ptr(), None if dgate is None else dgate.data_ptr(), m, k, gate_rows, scale,
+          ws.data_ptr(), nbytes)
+    return dx, dresidual, dweight, dpost, dgate
 
 
 def dg_status_string(status):

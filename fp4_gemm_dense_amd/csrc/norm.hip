@@ -8,6 +8,13 @@
 // Backward, with n = h * r and g = dy * weight: dx = dh + r (g - n mean(g n)),
 // dweight = sum over rows of dy * n.
 //
+// The norms around a block (dg_sandwich_norm) differ in h alone:
+//   h = bf16(residual + scale * gate * (x * rx * post_weight)),   rx = 1 / sqrt(mean(x^2) + eps),
+// which costs one more sum over the row.  Backward, with D the gradient of h in full (dx
+// above), nx = x * rx, v = scale * gate * D and u = v * post_weight:
+//   dresidual = D,  dx = rx (u - nx mean(u nx)),  dpost_weight = sum over rows of v * nx,
+//   dgate = sum over the gate's rows of scale * post_weight * D * nx.
+//
 // Bound: HBM (forward 7 bytes per element with a residual, backward 8); rows of up to some
 // 512 by the waves they take, one or two of them a row.  Measured (one MI355X, inputs not
 // in the caches; a 1 GiB copy runs at 5.1 TB/s): forward 8192 x 7168 70 us MXFP4, 74 UE8M0,
@@ -17,6 +24,7 @@
 // (floors 6.5 and 13: at most 1024 workgroups walk the rows), 130 x 2048 3.9.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/dg.h"
 #include "dg_internal.hpp"
@@ -35,6 +43,15 @@ struct NormParams {
   int m, k;
   float eps;
   double inv_k;
+};
+
+// The norms around a block: x is the block's output.
+struct SandwichParams : NormParams {
+  const uint16_t* post_weight;   // or null: the branch is not normed
+  const uint16_t* gate;          // [ceil(m / gate_rows)][k], or null
+  float* rstd_x;
+  int gate_rows;
+  float scale;
 };
 
 // A row is spread over a workgroup of 64 .. 1024 threads (whole waves), V vectors of 8
@@ -151,12 +168,68 @@ __device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, d
   return group_max<LANES>(amax);
 }
 
+// h of the norms around a block, in place of x in xv; rv holds the residual.  x * post_weight
+// * gate is exact in fp32 (three bf16 numbers) wherever it keeps to fp32's range; the product
+// with scale * rx and the residual's addition are one fp64 step, so that h is the bf16 rounding
+// of its fp32 one whatever the order of the row's sum.
+template <int V>
+__device__ __forceinline__ void block_output(const SandwichParams& p, int row, v4i (&xv)[V], const v4i (&rv)[V]) {
+  __shared__ double red[NORM_MAX_WAVES];
+  const int tid = threadIdx.x, nt = blockDim.x, nv = p.k >> 3;
+  v4i pv[V], gv[V];
+  const v4i one = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+  const size_t gate_at = p.gate ? (size_t)(row / p.gate_rows) * nv : 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = i * nt + tid;
+    pv[i] = p.post_weight && j < nv ? reinterpret_cast<const v4i*>(p.post_weight)[j] : one;
+    gv[i] = p.gate && j < nv ? reinterpret_cast<const v4i*>(p.gate)[gate_at + j] : one;
+  }
+  double c = p.scale;
+  if (p.post_weight) {   // (uniform)
+    double ss = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float a[8];
+      unpack_bf16x8(xv[i], a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
+    }
+    const double r = 1.0 / sqrt(block_sum(ss, red) * p.inv_k + (double)p.eps);
+    if (p.rstd_x && tid == 0) p.rstd_x[row] = (float)r;
+    c *= r;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float x[8], w[8], g[8], r[8], prod[8];
+    unpack_bf16x8(xv[i], x);
+    unpack_bf16x8(pv[i], w);
+    unpack_bf16x8(gv[i], g);
+    unpack_bf16x8(rv[i], r);
+    uint32_t pmax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      prod[e] = x[e] * w[e] * g[e];
+      pmax = umax(pmax, abs_bits(prod[e]));
+    }
+    if (__builtin_expect((pmax - kExactLo < kExactHi - kExactLo) | (i * nt + tid >= nv), 1)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = (float)fma((double)prod[e], c, (double)r[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = (float)fma((double)x[e] * (double)w[e] * (double)g[e], c, (double)r[e]);
+    }
+    xv[i] = pack_bf16x8(r);
+  }
+}
+
 // One row per workgroup.  (Measured against 2, 4 and 8 rows per workgroup, with the
 // next row loaded ahead and the K-block-major scales leaving in longer runs, and
 // against 2 to 8 persistent workgroups per CU: one row was the fastest at 8192 x 7168
 // in every format, 70-75 us against 73-84.)
-template <int FMT, int V>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormParams p) {
+template <int FMT, int V, typename P>
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) {
+  constexpr bool BLOCK = std::is_same_v<P, SandwichParams>;
   __shared__ double red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3, kb_n = p.k >> 7;
@@ -173,13 +246,14 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(NormP
       wv[i] = reinterpret_cast<const v4i*>(p.weight)[j];
     }
   }
+  if constexpr (BLOCK) block_output<V>(p, row, hv, rv);
   double ss = 0;   // (the squares of bf16 numbers are exact in fp64, and its range holds them)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int j = i * nt + tid;
     float a[8];
     unpack_bf16x8(hv[i], a);
-    if (p.residual) {
+    if (!BLOCK && p.residual) {
       float b[8];
       unpack_bf16x8(rv[i], b);
 #pragma unroll
@@ -373,18 +447,20 @@ __global__ void __launch_bounds__(THREADS) rms_norm_backward_kernel(NormBackPara
   }
 }
 
-// dweight from the partial rows: a workgroup sums 32 columns, 8 threads (4 columns
-// each) across and 32 down, each every 32nd row; their sums meet in LDS in order.
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, float* dweight, int parts, int k) {
+// Sums of `rows` partial rows, `stride` floats apart: a workgroup of 256 sums 32 columns,
+// 8 threads (4 columns each) across and 32 down, each every 32nd row; their sums meet in
+// LDS in order.  first: where row 0 lies apart, its distance from its place.
+__device__ __forceinline__ void sum_rows(const float* part, int stride, int rows, float* out, int first = 0) {
   __shared__ v4f sums[32][8];
   const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
   const float* src = part + (size_t)blockIdx.x * 32 + cx * 4;
   v4f s = {0.f, 0.f, 0.f, 0.f};
-  for (int i = ry; i < parts; i += 8 * 32) {
+  for (int i = ry; i < rows; i += 8 * 32) {
     v4f t[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      t[u] = i + u * 32 < parts ? *reinterpret_cast<const v4f*>(src + (size_t)(i + u * 32) * k) : v4f{0.f, 0.f, 0.f, 0.f};
+      t[u] = i + u * 32 < rows ? *reinterpret_cast<const v4f*>(src + (size_t)(i + u * 32) * stride + (i + u * 32 ? 0 : first))
+                               : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += t[u];
   }
@@ -394,8 +470,13 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, fl
     v4f t = sums[0][threadIdx.x];
 #pragma unroll
     for (int y = 1; y < 32; ++y) t += sums[y][threadIdx.x];
-    *reinterpret_cast<v4f*>(dweight + (size_t)blockIdx.x * 32 + threadIdx.x * 4) = t;
+    *reinterpret_cast<v4f*>(out + (size_t)blockIdx.x * 32 + threadIdx.x * 4) = t;
   }
+}
+
+// dweight from the partial rows.
+__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* part, float* dweight, int parts, int k) {
+  sum_rows(part, k, parts, dweight);
 }
 
 // Few rows: one launch and no workspace.  dweight needs no row's sum (n = h * rstd), so
@@ -487,6 +568,193 @@ __global__ void __launch_bounds__(THREADS) rms_norm_backward_few_kernel(NormBack
   }
 }
 
+struct SandwichBackParams {
+  const uint16_t* dy;
+  const uint16_t* dh;            // or null
+  const uint16_t* x;
+  const uint16_t* h;
+  const uint16_t* post_weight;   // or null
+  const uint16_t* gate;          // or null
+  const uint16_t* weight;
+  const float* rstd_x;
+  const float* rstd;
+  uint16_t* dx;
+  uint16_t* dresidual;
+  float* dgate;      // [groups][k]
+  float* part;       // [workgroups][k] of dweight
+  float* part_post;  // [workgroups][k] of dpost_weight (when post_weight is set)
+  float* part_gate;  // [workgroups][2][k] of dgate (when gate is set)
+  int m, k, rows;    // rows per workgroup
+  int gate_rows;     // (m without a gate)
+  float scale;
+};
+
+// A workgroup takes `rows` rows side by side; a thread keeps its columns' share of the weight
+// gradients in registers over them.  Over the rows of one gate the sum S of D * nx serves
+// both gradients behind it: dgate = scale * post_weight * S, and dpost_weight adds up scale *
+// gate * S.  A gate's sum that lies in one workgroup is final; the first and the last gate of
+// a workgroup may go on in its neighbours, and leave as its partial rows 0 and 1 (0 where
+// the two are one).
+template <int V, bool AHEAD>
+__global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBackParams p) {
+  __shared__ float red[2][2][NORM_MAX_WAVES];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int nv = p.k >> 3;
+  const float inv_k = 1.0f / (float)p.k;
+  const v4i none = {0, 0, 0, 0}, one = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+  auto at = [&](const uint16_t* t, int row, int i) -> v4i {
+    const int j = i * nt + tid;
+    return j < nv ? reinterpret_cast<const v4i*>(t)[(size_t)row * nv + j] : none;
+  };
+  auto store = [&](float* t, int i, const float (&v)[8]) {
+    const int j = i * nt + tid;
+    if (j >= nv) return;
+    v4f* o = reinterpret_cast<v4f*>(t + (size_t)j * 8);
+    o[0] = v4f{v[0], v[1], v[2], v[3]};
+    o[1] = v4f{v[4], v[5], v[6], v[7]};
+  };
+  float dw[V][8], dpw[V][8], sum[V][8];
+  v4i wv[V], pv[V], gv[V], dyn[V], hn[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    wv[i] = at(p.weight, 0, i);
+    pv[i] = p.post_weight ? at(p.post_weight, 0, i) : one;
+    gv[i] = one;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = dpw[i][e] = sum[i][e] = 0.f;
+  }
+  const int row0 = blockIdx.x * p.rows, row1 = min(p.m, row0 + p.rows);
+  const int first_gate = row0 / p.gate_rows;
+  int gate = -1, gate_end = row0, turn = 0;
+  float rn = 0.f;
+  auto load_next = [&](int r) {
+    rn = p.rstd[r];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dyn[i] = at(p.dy, r, i);
+      hn[i] = at(p.h, r, i);
+    }
+  };
+  // the rows of a gate are done: what S gives
+  auto end_gate = [&]() {
+    const bool whole = gate * p.gate_rows >= row0 && (gate_end <= row1);
+    float* out = whole ? p.dgate + (size_t)gate * p.k
+                       : p.part_gate + ((size_t)blockIdx.x * 2 + (gate == first_gate ? 0 : 1)) * p.k;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float g[8], w[8], o[8];
+      unpack_bf16x8(gv[i], g);
+      unpack_bf16x8(pv[i], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = p.scale * sum[i][e];
+        dpw[i][e] = fmaf(g[e], t, dpw[i][e]);
+        o[e] = w[e] * t;
+        sum[i][e] = 0.f;
+      }
+      if (p.gate) store(out, i, o);
+    }
+  };
+  if (AHEAD) load_next(row0);
+  for (int row = row0; row < row1; ++row) {
+    if (row >= gate_end) {   // (uniform)
+      if (gate >= 0) end_gate();
+      gate = row / p.gate_rows;
+      gate_end = (int)min((long long)p.m, (long long)(gate + 1) * p.gate_rows);
+      if (p.gate) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) gv[i] = at(p.gate, gate, i);
+      }
+    }
+    v4i dyc[V], hc[V], dhc[V], xc[V];
+    float dot = 0.f;
+    if (!AHEAD) load_next(row);
+    const float r = rn, rx = p.post_weight ? p.rstd_x[row] : 1.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dhc[i] = p.dh ? at(p.dh, row, i) : none;
+      xc[i] = at(p.x, row, i);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dyc[i] = dyn[i];
+      hc[i] = hn[i];
+      float a[8], n[8], w[8];
+      unpack_bf16x8(dyc[i], a);
+      unpack_bf16x8(hc[i], n);
+      unpack_bf16x8(wv[i], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[e] *= r;
+        dw[i][e] = fmaf(a[e], n[e], dw[i][e]);
+        dot = fmaf(a[e] * w[e], n[e], dot);
+      }
+    }
+    if (AHEAD && row + 1 < row1) load_next(row + 1);
+    const float mean = block_sum(dot, red[0][turn]) * inv_k;
+    float u[V][8];   // v * post_weight
+    dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = i * nt + tid;
+      float a[8], n[8], w[8], d[8], x[8], g[8], pw[8];
+      unpack_bf16x8(dyc[i], a);
+      unpack_bf16x8(hc[i], n);
+      unpack_bf16x8(wv[i], w);
+      unpack_bf16x8(dhc[i], d);
+      unpack_bf16x8(xc[i], x);
+      unpack_bf16x8(gv[i], g);
+      unpack_bf16x8(pv[i], pw);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] += r * (a[e] * w[e] - n[e] * r * mean);
+        x[e] *= rx;
+        sum[i][e] = fmaf(d[e], x[e], sum[i][e]);
+        u[i][e] = d[e] * p.scale * g[e] * pw[e];
+        dot = fmaf(u[i][e], x[e], dot);
+      }
+      if (j < nv) reinterpret_cast<v4i*>(p.dresidual)[(size_t)row * nv + j] = pack_bf16x8(d);
+    }
+    const float mean_x = p.post_weight ? block_sum(dot, red[1][turn]) * inv_k : 0.f;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = i * nt + tid;
+      float x[8];
+      unpack_bf16x8(xc[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = rx * (u[i][e] - x[e] * rx * mean_x);
+      if (j < nv) reinterpret_cast<v4i*>(p.dx)[(size_t)row * nv + j] = pack_bf16x8(x);
+    }
+  }
+  end_gate();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    store(p.part + (size_t)blockIdx.x * p.k, i, dw[i]);
+    if (p.post_weight) store(p.part_post + (size_t)blockIdx.x * p.k, i, dpw[i]);
+  }
+}
+
+// The partial rows' sums: y = 0 dweight, 1 dpost_weight, from 2 on one gate each, of those
+// that lie in more than one workgroup.  They are numbered by the gate while there are no more
+// gates than workgroups, otherwise by the workgroup they begin in.
+__global__ void __launch_bounds__(256) sandwich_sums_kernel(SandwichBackParams p, float* dweight, float* dpost_weight, int parts) {
+  const int y = blockIdx.y;
+  if (y == 0) return sum_rows(p.part, p.k, parts, dweight);
+  if (y == 1) {
+    if (p.post_weight) sum_rows(p.part_post, p.k, parts, dpost_weight);
+    return;
+  }
+  const int gates = (p.m - 1) / p.gate_rows + 1;
+  const int gate = gates <= parts ? y - 2 : (min(p.m, (y - 1) * p.rows) - 1) / p.gate_rows;
+  const int w0 = (int)((long long)gate * p.gate_rows / p.rows);
+  const int w1 = (int)((min((long long)p.m, (long long)(gate + 1) * p.gate_rows) - 1) / p.rows);
+  if (w0 == w1 || (gates > parts && w0 != y - 2)) return;
+  // its share of w0 is row 0 where w0 begins with it, that of the others is row 0
+  const int at0 = w0 * p.rows / p.gate_rows == gate ? 0 : 1;
+  sum_rows(p.part_gate + (size_t)w0 * 2 * p.k, 2 * p.k, w1 - w0 + 1, p.dgate + (size_t)gate * p.k, at0 ? p.k : 0);
+}
+
 // One launch pays up to some 1200 rows (130 x 2048 3.6 us, 5.9 with partial rows and a
 // second launch; 600 x 7168 9.9 / 13.5; 1200 x 7168 18.2 / 21.5; 1200 x 2048 9.9 / 10.2;
 // 2400 x 7168 41 / 34): each column is read by one workgroup.
@@ -505,12 +773,12 @@ static int norm_parts(int m, int k) {
   return std::min(m, 256 * std::max(1, std::min(4, 8 / waves)));
 }
 
-template <int FMT>
-static hipError_t launch_norm(const NormParams& p, hipStream_t hs) {
+template <int FMT, typename P>
+static hipError_t launch_norm(const P& p, hipStream_t hs) {
   const NormShape s = norm_shape(p.k);
-  if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1>), dim3(p.m), dim3(s.threads), 0, hs, p);
-  else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2>), dim3(p.m), dim3(s.threads), 0, hs, p);
-  else hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 4>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  else hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 4, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
   return hipGetLastError();
 }
 
@@ -520,6 +788,27 @@ static hipError_t launch_norm_backward(const NormBackParams& p, int grid, hipStr
   else if (s.v == 2) hipLaunchKernelGGL((rms_norm_backward_kernel<2, 512>), dim3(grid), dim3(s.threads), 0, hs, p);
   else if (s.threads <= 512) hipLaunchKernelGGL((rms_norm_backward_kernel<4, 512>), dim3(grid), dim3(s.threads), 0, hs, p);
   else hipLaunchKernelGGL((rms_norm_backward_kernel<4, 1024>), dim3(grid), dim3(s.threads), 0, hs, p);
+  return hipGetLastError();
+}
+
+// The backward pass of the norms around a block: rows per workgroup and workgroups, one per CU
+// of the whole chip or more of shorter rows, as above.  (A function of the sizes alone, too.)
+constexpr int SANDWICH_BACK_MAX_K = 16384;
+static int sandwich_rows(int m, int k) {
+  const int parts = norm_parts(m, k);
+  return (int)(((long long)m + parts - 1) / parts);
+}
+static int sandwich_parts(int m, int k) {
+  const int rows = sandwich_rows(m, k);
+  return (int)(((long long)m + rows - 1) / rows);
+}
+static bool sandwich_backward_fits(int m, int k) { return k % 128 == 0 && k <= SANDWICH_BACK_MAX_K && m <= 1 << 30; }
+
+static hipError_t launch_sandwich_backward(const SandwichBackParams& p, int grid, hipStream_t hs) {
+  const NormShape s = norm_shape(p.k);
+  if (s.v == 1) hipLaunchKernelGGL((sandwich_norm_backward_kernel<1, true>), dim3(grid), dim3(s.threads), 0, hs, p);
+  else if (s.v == 2) hipLaunchKernelGGL((sandwich_norm_backward_kernel<2, true>), dim3(grid), dim3(s.threads), 0, hs, p);
+  else hipLaunchKernelGGL((sandwich_norm_backward_kernel<4, false>), dim3(grid), dim3(s.threads), 0, hs, p);
   return hipGetLastError();
 }
 
@@ -543,29 +832,51 @@ using namespace dg;
 
 static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
+// The checks of a forward call's common arguments.
+static int norm_arguments(const NormParams& p, int format) {
+  if (!p.x || !p.weight || !p.q || !p.sf) return DG_ERR_INVALID_ARG;
+  if (format != DG_QUANT_E4M3_F32 && format != DG_QUANT_E4M3_UE8M0 && format != DG_QUANT_MXFP4) return DG_ERR_INVALID_ARG;
+  if (p.m <= 0 || p.k <= 0 || !(p.eps > 0.f) || !std::isfinite(p.eps)) return DG_ERR_INVALID_ARG;
+  if (misaligned(p.x, 16) || misaligned(p.residual, 16) || misaligned(p.weight, 16) || misaligned(p.h, 16) ||
+      misaligned(p.q, 16) || misaligned(p.sf, 4) || misaligned(p.rstd, 4))
+    return DG_ERR_INVALID_ARG;
+  if (p.k % 128 != 0 || p.k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
+  // (a launch has fewer than 2^32 threads, and a row's workgroup at most this many)
+  if ((long long)p.m * std::min(1024, (p.k / 8 + 63) / 64 * 64) >= 1LL << 32) return DG_ERR_UNSUPPORTED;
+  return current_device_info().ok ? DG_OK : DG_ERR_NO_DEVICE;
+}
+
+template <typename P>
+static int launch_norm_format(const P& p, int format, void* stream) {
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const hipError_t e = format == DG_QUANT_E4M3_F32     ? launch_norm<DG_QUANT_E4M3_F32>(p, hs)
+                       : format == DG_QUANT_E4M3_UE8M0 ? launch_norm<DG_QUANT_E4M3_UE8M0>(p, hs)
+                                                       : launch_norm<DG_QUANT_MXFP4>(p, hs);
+  return e == hipSuccess ? DG_OK : DG_ERR_HIP;
+}
+
 extern "C" {
 
 int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h, void* q,
                     void* sf, int format, float* rstd, int m, int k, float eps, void* stream) {
   try {
-    if (!x || !weight || !q || !sf) return DG_ERR_INVALID_ARG;
-    if (format != DG_QUANT_E4M3_F32 && format != DG_QUANT_E4M3_UE8M0 && format != DG_QUANT_MXFP4)
-      return DG_ERR_INVALID_ARG;
-    if (m <= 0 || k <= 0 || !(eps > 0.f) || !std::isfinite(eps)) return DG_ERR_INVALID_ARG;
-    if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(weight, 16) || misaligned(h, 16) ||
-        misaligned(q, 16) || misaligned(sf, 4) || misaligned(rstd, 4))
-      return DG_ERR_INVALID_ARG;
-    if (k % 128 != 0 || k > NORM_MAX_K) return DG_ERR_UNSUPPORTED;
-    // (a launch has fewer than 2^32 threads, and a row's workgroup at most this many)
-    if ((long long)m * std::min(1024, (k / 8 + 63) / 64 * 64) >= 1LL << 32) return DG_ERR_UNSUPPORTED;
-    DeviceInfo di = current_device_info();
-    if (!di.ok) return DG_ERR_NO_DEVICE;
-    NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k};
-    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const hipError_t e = format == DG_QUANT_E4M3_F32     ? launch_norm<DG_QUANT_E4M3_F32>(p, hs)
-                         : format == DG_QUANT_E4M3_UE8M0 ? launch_norm<DG_QUANT_E4M3_UE8M0>(p, hs)
-                                                         : launch_norm<DG_QUANT_MXFP4>(p, hs);
-    return e == hipSuccess ? DG_OK : DG_ERR_HIP;
+    const NormParams p{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k};
+    const int st = norm_arguments(p, format);
+    return st != DG_OK ? st : launch_norm_format(p, format, stream);
+  } catch (...) {
+    return DG_ERR_HIP;
+  }
+}
+
+int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* post_weight, const uint16_t* gate,
+                     const uint16_t* weight, uint16_t* h, void* q, void* sf, int format, float* rstd_x, float* rstd,
+                     int m, int k, int gate_rows, float scale, float eps, void* stream) {
+  try {
+    if (!residual || !h || (gate && gate_rows <= 0) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
+    if (misaligned(post_weight, 16) || misaligned(gate, 16) || misaligned(rstd_x, 4)) return DG_ERR_INVALID_ARG;
+    const SandwichParams p{{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k}, post_weight, gate, rstd_x, gate_rows, scale};
+    const int st = norm_arguments(p, format);
+    return st != DG_OK ? st : launch_norm_format(p, format, stream);
   } catch (...) {
     return DG_ERR_HIP;
   }
@@ -607,6 +918,47 @@ int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
     e = launch_norm_backward(p, parts, hs);
     if (e != hipSuccess) return DG_ERR_HIP;
     hipLaunchKernelGGL(norm_dweight_kernel, dim3(k / 32), dim3(256), 0, hs, p.part, dweight, parts, k);
+    return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
+  } catch (...) {
+    return DG_ERR_HIP;
+  }
+}
+
+size_t dg_sandwich_norm_backward_workspace_bytes(int m, int k, int with_post_weight, int with_gate) {
+  if (m <= 0 || k <= 0 || !sandwich_backward_fits(m, k)) return 0;
+  return (size_t)sandwich_parts(m, k) * k * sizeof(float) * (1 + (with_post_weight ? 1 : 0) + (with_gate ? 2 : 0));
+}
+
+int dg_sandwich_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* x, const uint16_t* h,
+                              const uint16_t* post_weight, const uint16_t* gate, const uint16_t* weight,
+                              const float* rstd_x, const float* rstd, uint16_t* dx, uint16_t* dresidual, float* dweight,
+                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, float scale,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    if (!dy || !x || !h || !weight || !rstd || !dx || !dresidual || !dweight) return DG_ERR_INVALID_ARG;
+    if (!post_weight != !dpost_weight || (post_weight && !rstd_x) || !gate != !dgate) return DG_ERR_INVALID_ARG;
+    if (m <= 0 || k <= 0 || (gate && gate_rows <= 0) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
+    if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(x, 16) || misaligned(h, 16) || misaligned(post_weight, 16) ||
+        misaligned(gate, 16) || misaligned(weight, 16) || misaligned(dx, 16) || misaligned(dresidual, 16) ||
+        misaligned(dweight, 16) || misaligned(dpost_weight, 16) || misaligned(dgate, 16) || misaligned(rstd_x, 4) ||
+        misaligned(rstd, 4))
+      return DG_ERR_INVALID_ARG;
+    if (!sandwich_backward_fits(m, k)) return DG_ERR_UNSUPPORTED;
+    const size_t need = dg_sandwich_norm_backward_workspace_bytes(m, k, post_weight != nullptr, gate != nullptr);
+    if (!workspace || workspace_bytes < need || misaligned(workspace, 16)) return DG_ERR_INVALID_ARG;
+    DeviceInfo di = current_device_info();
+    if (!di.ok) return DG_ERR_NO_DEVICE;
+    const int parts = sandwich_parts(m, k);
+    float* const part = static_cast<float*>(workspace);
+    const size_t one = (size_t)parts * k;
+    const SandwichBackParams p{dy, dh, x, h, post_weight, gate, weight, rstd_x, rstd, dx, dresidual, dgate,
+                               part, part + one, part + (post_weight ? 2 : 1) * one,
+                               m, k, sandwich_rows(m, k), gate ? gate_rows : m, scale};
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    if (launch_sandwich_backward(p, parts, hs) != hipSuccess) return DG_ERR_HIP;
+    const int gates = gate ? (m - 1) / gate_rows + 1 : 0;
+    const int sums = 2 + (gates == 0 ? 0 : std::min(gates, parts));
+    hipLaunchKernelGGL(sandwich_sums_kernel, dim3(k / 32, sums), dim3(256), 0, hs, p, dweight, dpost_weight, parts);
     return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
   } catch (...) {
     return DG_ERR_HIP;

@@ -487,6 +487,61 @@ int dg_add_rms_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
 /* Bytes of that workspace (0: none; 0 also for invalid sizes).  Host-only. */
 size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k);
 
+/*
+ * The norms around a block (an attention or feed-forward layer) whose output is normed
+ * and gated before it joins the residual stream, in one step with the norm in front of the
+ * next GEMM.  Per row:
+ *   rx = 1 / sqrt(mean(x^2) + eps)
+ *   h  = bf16(residual + scale * gate * (x * rx * post_weight))
+ *   r  = 1 / sqrt(mean(h^2) + eps),  y = h * r * weight
+ * and y is quantised as by dg_add_rms_norm (formats, layouts and exactness are its).  h is
+ * rounded to fp32 and then to bf16 from a sum in fp64.
+ *   x           [m, k] bf16, the block's output; residual [m, k] bf16
+ *   post_weight [k] bf16, or NULL: the block's output is not normed (x * rx * post_weight is x)
+ *   gate        [ceil(m / gate_rows), k] bf16, or NULL (1): row i takes gate row i / gate_rows
+ *               (gate_rows = m or more: one vector for all rows; the rows of a sequence: one for
+ *               each; 1: one for each row).  gate_rows counts where gate is given: >= 1
+ *   weight      [k] bf16
+ *   h           [m, k] bf16 output; may be x or residual itself (in place)
+ *   q, sf, format as dg_add_rms_norm
+ *   rstd_x      [m] fp32 output, rx rounded (not written without post_weight), or NULL
+ *   rstd        [m] fp32 output, r rounded, or NULL
+ * Requirements: as dg_add_rms_norm's; scale finite.
+ */
+int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* post_weight, const uint16_t* gate,
+                     const uint16_t* weight, uint16_t* h, void* q, void* sf, int format, float* rstd_x, float* rstd,
+                     int m, int k, int gate_rows, float scale, float eps, void* stream);
+
+/*
+ * Its backward pass, in fp32; the gradient passes straight through the roundings.  With
+ * n = h * r, nx = x * rx (x without post_weight), a = dy * weight, u = scale * gate * D * post_weight:
+ *   D            = dh + r * (a - n * mean(a * n))             the gradient of h in full
+ *   dresidual    = bf16(D)
+ *   dx           = bf16(rx * (u - nx * mean(u * nx)))         (u without post_weight)
+ *   dweight      = sum over rows of dy * n                    fp32, as the next two
+ *   dpost_weight = sum over rows of scale * gate * D * nx
+ *   dgate[g]     = sum over the rows of gate row g of scale * post_weight * D * nx
+ * every sum in a fixed order.
+ *   dy [m, k] bf16, the gradient of y; dh [m, k] bf16, the gradient that arrives at h from the
+ *           residual stream, or NULL
+ *   x, h, post_weight, gate, weight, gate_rows, scale as in the forward pass, rstd_x (with
+ *           post_weight) and rstd from it
+ *   dx, dresidual [m, k] bf16 (each may be one of dy, dh, x and h itself, not both the same one);
+ *   dweight [k], dpost_weight [k] (given with post_weight), dgate [ceil(m / gate_rows), k] (with
+ *           gate) fp32; the outputs overlap nothing otherwise
+ *   workspace: at least dg_sandwich_norm_backward_workspace_bytes(...) bytes, 16-byte aligned
+ * Requirements: k % 128 == 0, k <= 16384, m <= 2^30 (else DG_ERR_UNSUPPORTED); 16-byte aligned
+ *   tensors (rstd_x and rstd: 4).
+ */
+int dg_sandwich_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* x, const uint16_t* h,
+                              const uint16_t* post_weight, const uint16_t* gate, const uint16_t* weight,
+                              const float* rstd_x, const float* rstd, uint16_t* dx, uint16_t* dresidual, float* dweight,
+                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, float scale,
+                              void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of that workspace (0 for invalid sizes); with_post_weight, with_gate: whether the call gives
+ * them.  Host-only. */
+size_t dg_sandwich_norm_backward_workspace_bytes(int m, int k, int with_post_weight, int with_gate);
+
 /* Row alignment of each group in the contiguous layout (usage guide, 工具函数). Returns 128. */
 int dg_get_mk_alignment_for_contiguous_layout(void);
 

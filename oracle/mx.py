@@ -101,3 +101,24 @@ def add_rms_norm_backward(dy, dh, h, weight, r):
     g = dy * weight
     dx = r[:, None] * (g - n * np.mean(g * n, axis=1, keepdims=True))
     return dx if dh is None else dx + dh, np.sum(dy * n, axis=0)
+
+
+def sandwich_norm(x, residual, post_weight, gate, scale, eps):
+    """float64 arrays, gate [m, k] by row (post_weight and gate may be None) -> (h unrounded [m, k], rx [m])."""
+    rx = 1.0 / np.sqrt(np.mean(x * x, axis=1) + eps) if post_weight is not None else np.ones(len(x))
+    n = x * rx[:, None] * (1.0 if post_weight is None else post_weight)
+    return residual + scale * (1.0 if gate is None else gate) * n, rx
+
+
+def sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rx, r, scale):
+    """float64 arrays, gate [m, k] by row (dh, post_weight and gate may be None; rx is 1 without post_weight) ->
+    (D = dresidual, dx, dy * n, v * nx, scale * post_weight * D * nx); the last three [m, k], to be summed over rows."""
+    n, nx = h * r[:, None], x * rx[:, None]
+    a = dy * weight
+    d = r[:, None] * (a - n * np.mean(a * n, axis=1, keepdims=True))
+    if dh is not None:
+        d = d + dh
+    v = scale * (1.0 if gate is None else gate) * d
+    u = v if post_weight is None else v * post_weight
+    dx = u if post_weight is None else rx[:, None] * (u - nx * np.mean(u * nx, axis=1, keepdims=True))
+    return d, dx, dy * n, v * nx, scale * (1.0 if post_weight is None else post_weight) * d * nx

@@ -1,0 +1,109 @@
+"""Host-side checks of the operators around a block's products: every refusal comes before any HIP call, and the
+binding checks its tensors (no compute is launched; these tests run without a GPU).  The oracle's gradients are held to
+differences of its forward formulas here, too."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_gemm_dense_amd as dgm
+from oracle import mx as X
+
+A = 0x10000      # a fake aligned address, never dereferenced on the host
+OK = (0, 4)      # passed validation; without a gfx950 device the call stops at the device check
+NAN, INF = float("nan"), float("inf")
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses: only where no GPU is visible")
+
+
+def expect(got, status):
+    assert got in status if isinstance(status, tuple) else got == status
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", [
+    ({}, OK), (dict(post_weight=0), OK), (dict(gate=0, gate_rows=0), OK), (dict(rstd_x=0, rstd=0), OK), (dict(fmt=2), OK),
+    (dict(gate_rows=1 << 30), OK), (dict(scale=0.0), OK), (dict(scale=-3.0), OK), (dict(k=32768), OK),
+    (dict(x=0), 1), (dict(residual=0), 1), (dict(weight=0), 1), (dict(h=0), 1), (dict(q=0), 1), (dict(sf=0), 1),
+    (dict(fmt=3), 1), (dict(m=0), 1), (dict(k=0), 1), (dict(gate_rows=0), 1), (dict(gate_rows=-1), 1),
+    (dict(scale=NAN), 1), (dict(scale=INF), 1), (dict(eps=0.0), 1), (dict(eps=NAN), 1),
+    (dict(x=A + 8), 1), (dict(residual=A + 8), 1), (dict(post_weight=A + 8), 1), (dict(gate=A + 8), 1),
+    (dict(weight=A + 8), 1), (dict(h=A + 8), 1), (dict(q=A + 8), 1), (dict(sf=A + 2), 1), (dict(rstd_x=A + 2), 1),
+    (dict(rstd=A + 2), 1), (dict(k=192), 2), (dict(k=32768 + 128), 2), (dict(m=1 << 26, k=128), 2),
+])
+def test_sandwich_norm_refusals(change, status):
+    v = dict(x=A, residual=A, post_weight=A, gate=A, weight=A, h=A, q=A, sf=A, fmt=0, rstd_x=A, rstd=A, m=8, k=256, gate_rows=3,
+             scale=0.5, eps=1e-6)
+    v.update(change)
+    expect(dgm.lib().dg_sandwich_norm(*v.values(), None), status)
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", [
+    ({}, OK), (dict(dh=0), OK), (dict(post_weight=0, dpost=0), OK), (dict(post_weight=0, dpost=0, rstd_x=0), OK),
+    (dict(gate=0, dgate=0, gate_rows=0), OK), (dict(k=16384), OK), (dict(m=1 << 30, k=128, gate_rows=0x7fffffff), OK),
+    (dict(dy=0), 1), (dict(x=0), 1), (dict(h=0), 1), (dict(weight=0), 1), (dict(rstd=0), 1), (dict(rstd_x=0), 1),
+    (dict(dx=0), 1), (dict(dres=0), 1), (dict(dweight=0), 1), (dict(dpost=0), 1), (dict(post_weight=0), 1), (dict(gate=0), 1),
+    (dict(dgate=0), 1), (dict(gate_rows=0), 1), (dict(m=0), 1), (dict(k=-128), 1), (dict(scale=INF), 1),
+    (dict(dy=A + 8), 1), (dict(dh=A + 8), 1), (dict(x=A + 8), 1), (dict(h=A + 8), 1), (dict(dx=A + 8), 1),
+    (dict(dres=A + 8), 1), (dict(dweight=A + 8), 1), (dict(dpost=A + 8), 1), (dict(dgate=A + 4), 1), (dict(ws=0), 1),
+    (dict(ws=A + 8), 1), (dict(less=1), 1), (dict(k=200), 2), (dict(k=16384 + 128), 2), (dict(m=(1 << 30) + 1), 2),
+])
+def test_sandwich_norm_backward_refusals(change, status):
+    v = dict(dy=A, dh=A, x=A, h=A, post_weight=A, gate=A, weight=A, rstd_x=A, rstd=A, dx=A, dres=A, dweight=A, dpost=A, dgate=A,
+             m=8, k=256, gate_rows=3, scale=0.5, ws=A)
+    less = change.get("less", 0)
+    v.update({n: c for n, c in change.items() if n != "less"})
+    need = dgm.dg_sandwich_norm_backward_workspace_bytes(v["m"], v["k"], bool(v["post_weight"]), bool(v["gate"]))
+    expect(dgm.lib().dg_sandwich_norm_backward(*v.values(), need - less, None), status)
+
+
+def test_sandwich_norm_backward_workspace_query():
+    f = dgm.dg_sandwich_norm_backward_workspace_bytes
+    assert f(0, 128) == f(8, 0) == f(8, 100) == f(8, 16384 + 128) == f((1 << 30) + 1, 128) == 0
+    assert f(1, 128, False, False) == 512 and f(1, 128, True, False) == 1024 and f(1, 128, True, True) == 2048
+    assert f(1 << 30, 16384) <= 128 << 20
+
+
+def test_sandwich_binding_checks_tensors():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x: must be a device tensor"):
+        dgm.sandwich_norm(x, x, None, None, x[0].clone())
+    with pytest.raises(ValueError, match="gate_rows: expected"):
+        dgm.sandwich_norm(x, x, None, x, x[0].clone(), gate_rows=0)
+    with pytest.raises(ValueError, match="dy: must be a device tensor"):
+        dgm.sandwich_norm_backward(x, None, x, x, None, None, x[0].clone(), None, x[:, 0].float())
+
+
+@pytest.mark.parametrize("post,gated", [(True, True), (False, True), (True, False), (False, False)])
+def test_oracle_sandwich_gradients_are_those_of_differences(post, gated):
+    """L = sum(dy * y) + sum(dh * h) without roundings: the oracle's gradients against central differences (error of
+    order step^2: 1e-5 of the gradient's size for a step of 1e-4 with some margin for the third derivative)."""
+    rng = np.random.default_rng(5)
+    m, k, scale, eps = 4, 16, 0.7, 1e-3
+    t = dict(x=rng.standard_normal((m, k)), res=rng.standard_normal((m, k)), pw=1 + 0.3 * rng.standard_normal(k),
+             w=1 + 0.3 * rng.standard_normal(k), gate=rng.standard_normal((2, k)))
+    dy, dh = rng.standard_normal((m, k)), rng.standard_normal((m, k))
+
+    def parts(t):
+        g = np.repeat(t["gate"], 2, axis=0) if gated else None
+        h, rx = X.sandwich_norm(t["x"], t["res"], t["pw"] if post else None, g, scale, eps)
+        return g, h, rx, 1 / np.sqrt(np.mean(h * h, axis=1) + eps)
+
+    def loss(t):
+        _, h, _, r = parts(t)
+        return np.sum(dy * h * r[:, None] * t["w"]) + np.sum(dh * h)
+
+    g, h, rx, r = parts(t)
+    d, dx, yn, vn, gn = X.sandwich_norm_backward(dy, dh, t["x"], h, t["pw"] if post else None, g, t["w"], rx, r, scale)
+    want = dict(x=dx, res=d, w=yn.sum(axis=0))
+    if post:
+        want["pw"] = vn.sum(axis=0)
+    if gated:
+        want["gate"] = gn.reshape(2, 2, k).sum(axis=1)
+    for name, grad in want.items():
+        for at in np.ndindex(*t[name].shape):
+            up, dn = ({n: v.copy() for n, v in t.items()} for _ in range(2))
+            up[name][at] += 1e-4
+            dn[name][at] -= 1e-4
+            assert abs((loss(up) - loss(dn)) / 2e-4 - grad[at]) < 1e-5 * (1 + np.abs(grad).max()), (name, at)
