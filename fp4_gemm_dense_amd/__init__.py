@@ -49,6 +49,9 @@ _SIGNATURES = {
     "dg_quantize_mxfp4": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "dg_mxfp4_gemm_nt": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "dg_mxfp4_gemm_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "dg_mxfp4_linear": (_I, [_P] * 5 + [_I] + [_P] * 3 + [_I, _I, _I, _P, _SZ, _P]),
+    "dg_activation_backward": (_I, [_P, _P, _I] + [_P] * 6 + [_I, _I, _P, _SZ, _P]),
+    "dg_activation_backward_workspace_bytes": (_SZ, [_I, _I]),
     "dg_add_rms_norm": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P]),
     "dg_add_rms_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
     "dg_add_rms_norm_backward_workspace_bytes": (_SZ, [_I, _I]),
@@ -562,6 +565,60 @@ def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
     return d
 
 
+# dg_activation (include/dg.h); ACT_GATED is or-ed in
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_GATED = 0, 1, 2, 3, 4, 16
+
+
+def _activation_columns(activation, n):
+    """Columns of the output of a layer whose product has n."""
+    if activation & ~ACT_GATED not in (ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH):
+        raise ValueError(f"activation: expected one of the ACT_ values, ACT_GATED or-ed in or not, got {activation}")
+    if not activation & ACT_GATED:
+        return n
+    if n % 2:
+        raise ValueError(f"activation: a gated one halves the columns, got {n}")
+    return n // 2
+
+
+def dg_mxfp4_linear(a, a_sf, b, b_sf, bias, activation, residual, z, d, workspace=None):
+    """d = residual + act(a . b^T + bias) (see include/dg.h): operands as dg_mxfp4_gemm_nt; bias [N] bf16 or None;
+    residual, d [M, N] bf16 (gated: [M, N/2]), residual None or given; z [M, N] bf16, the pre-activation, or None.
+    workspace: optional uint8 device tensor (allocated here when needed and not given)."""
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    out = (m, _activation_columns(activation, n))
+    ptrs = (_arg(bias, _BF, (n,), index, "bias"), activation, _arg(residual, _BF, out, index, "residual"),
+            _arg(z, _BF, (m, n), index, "z"), _arg(d, _BF, out, index, "d"))
+    if workspace is None:
+        nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
+        if nbytes:
+            workspace = _new((nbytes,), _U8, a.device)
+            wp = workspace.data_ptr()
+    else:
+        nbytes = workspace.numel()
+        wp = _arg(workspace, _U8S, (nbytes,), index, "workspace")
+    _call("dg_mxfp4_linear", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), *ptrs, m, n, k, wp, nbytes)
+    return d
+
+
+def dg_activation_backward_workspace_bytes(m, n):
+    return int(lib().dg_activation_backward_workspace_bytes(m, n))
+
+
+def dg_activation_backward(dy, z, activation, dz=None, q=None, sf=None, qt=None, sft=None, dbias=None, workspace=None):
+    """dz = dy * act'(z) (see include/dg.h) in the forms that are given: dz [m, n] bf16, q [m, n/2] and sf [n/128, m],
+    qt [n, mp/2] and sft [mp/128, n] (mp = m rounded up to 128), and its column sums dbias [n] fp32.  dy [m, n] (gated:
+    [m, n/2]), z [m, n] bf16 (None with ACT_NONE).  workspace: uint8 device tensor of at least
+    dg_activation_backward_workspace_bytes(m, n) bytes (None where that is 0 or dbias is None)."""
+    m, n = (dy if z is None else z).shape
+    index, mb = dy.get_device(), (m + 127) // 128
+    nbytes = 0 if workspace is None else workspace.numel()
+    _call("dg_activation_backward", index, _arg(dy, _BF, (m, _activation_columns(activation, n)), index, "dy"),
+          _arg(z, _BF, (m, n), index, "z"), activation, _arg(dz, _BF, (m, n), index, "dz"),
+          _arg(q, _U8S, (m, n // 2), index, "q"), _arg(sf, _I32S, (n // 128, m), index, "sf"),
+          _arg(qt, _U8S, (n, mb * 64), index, "qt"), _arg(sft, _I32S, (mb, n), index, "sft"),
+          _arg(dbias, _F32S, (n,), index, "dbias"), m, n, _arg(workspace, _U8S, (nbytes,), index, "workspace"), nbytes)
+
+
 def dg_add_rms_norm(x, residual, weight, h, q, sf, eps, quant_format, rstd=None):
     """h = x + residual; q, sf = quantised h / rms(h) * weight (see include/dg.h).  x, residual, h [m, k] bf16 (residual
     and h may be None), weight [k]; q [m, k] uint8 and sf [k/128, m] fp32 (QUANT_E4M3_F32) or [m, ceil(k/512)] int32
@@ -758,6 +815,45 @@ def mxfp4_gemm_nt(a, a_sf, b, b_sf, c=None):
     _call("dg_mxfp4_gemm_nt", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), cp, d.data_ptr(), m, n,
           k, wp, nbytes)
     return d
+
+
+def mxfp4_linear(a, a_sf, b, b_sf, bias=None, activation=ACT_NONE, residual=None, pre_activation=False):
+    """Returns a new bf16 tensor d = residual + act(a . b^T + bias), both operands MXFP4 (activation: an ACT_ value,
+    gated with ACT_GATED or-ed in); with pre_activation, (d, z), z = bf16(a . b^T + bias) for activation_backward."""
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    out, dev = (m, _activation_columns(activation, n)), a.device
+    bp, rp = _arg(bias, _BF, (n,), index, "bias"), _arg(residual, _BF, out, index, "residual")
+    d, z = _new(out, torch.bfloat16, dev), _new((m, n), torch.bfloat16, dev) if pre_activation else None
+    nbytes, wp = (_lib or load_library()).dg_mxfp4_gemm_workspace_bytes(m, n, k, 0), None
+    if nbytes:
+        ws = _new((nbytes,), _U8, dev)
+        wp = ws.data_ptr()
+    _call("dg_mxfp4_linear", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), bp, activation, rp,
+          None if z is None else z.data_ptr(), d.data_ptr(), m, n, k, wp, nbytes)
+    return d if z is None else (d, z)
+
+
+def activation_backward(dy, z, activation, bias=True):
+    """(q, sf, qt, sft, dbias): the gradient of a linear layer's pre-activation z from dy, quantised to MXFP4 along the
+    rows and along the columns of the transposed operand, and its sums over the rows (fp32; None without bias).  z may be
+    None with ACT_NONE."""
+    m, n = (dy if z is None else z).shape
+    index, dev, mb = dy.get_device(), dy.device, (m + 127) // 128
+    yp = _arg(dy, _BF, (m, _activation_columns(activation, n)), index, "dy")
+    zp = _arg(z, _BF, (m, n), index, "z")
+    q, sf = _new((m, n // 2), _U8, dev), _new((n // 128, m), torch.int32, dev)
+    qt, sft = _new((n, mb * 64), _U8, dev), _new((mb, n), torch.int32, dev)
+    dbias, bp, nbytes, wp = None, None, 0, None
+    if bias:
+        dbias = _new((n,), torch.float32, dev)
+        bp = dbias.data_ptr()
+        nbytes = (_lib or load_library()).dg_activation_backward_workspace_bytes(m, n)
+        if nbytes:
+            ws = _new((nbytes,), _U8, dev)
+            wp = ws.data_ptr()
+    _call("dg_activation_backward", index, yp, zp, activation, None, q.data_ptr(), sf.data_ptr(), qt.data_ptr(),
+          sft.data_ptr(), bp, m, n, wp, nbytes)
+    return q, sf, qt, sft, dbias
 
 
 def add_rms_norm(x, residual, weight, eps=1e-6, quant_format=QUANT_E4M3_F32):

@@ -1,0 +1,100 @@
+// MXFP4 linear layer for gfx950: d = residual + act(A.B^T + bias), or with a gated activation
+// d = residual + act(gate) * up, gate and up the two halves of A.B^T + bias; optionally the
+// pre-activation A.B^T + bias itself, for the backward pass.
+//
+// The products are the kernels of mxfp4_tile.hpp on the dense GEMM's plans; the epilogue works
+// on the fp32 accumulators where they are (after the K groups' sums have met, or in the reduce
+// of a plan split along K), so neither u nor act(u) goes to memory between the two.  act reads
+// the unrounded u, whether or not z is stored: the same d either way.
+#include <algorithm>
+
+#include "../../include/dg.h"
+#include "mxfp4_tile.hpp"
+
+namespace dg {
+
+// The split tiles' partial sums in slice order, and the epilogue: a thread takes eight columns
+// of one row (for one launch over the slices of all split tiles).
+template <bool GATED>
+__global__ void __launch_bounds__(256) linear_reduce_kernel(Mxfp4LinearParams<GATED> p, int bm, int bn, int split_tiles) {
+  const int per_row = bn / 8;
+  const long long per_tile = (long long)bm * per_row, total = per_tile * split_tiles;
+  const size_t tile = (size_t)bm * bn;
+  const LinearOut<GATED> out(p);
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
+    const int st = (int)(i / per_tile), q = (int)(i - (long long)st * per_tile);
+    const int r = q / per_row, c8 = q - r * per_row;
+    int tm, tn;
+    raster_tile(p.full_tiles + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    const int row = tm * bm + r, col = tn * bn + c8 * 8;
+    const v4f* w = reinterpret_cast<const v4f*>(p.ws + (size_t)st * p.splits * tile + (size_t)r * bn + c8 * 8);
+    v4f lo = w[0], hi = w[1];
+    for (int s = 1; s < p.splits; ++s) {
+      w += tile / 4;
+      lo += w[0];
+      hi += w[1];
+    }
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    out(row, col, row < p.m && col < p.n, v);
+  }
+}
+
+bool activation_of(int activation, Activation* a) {
+  // 2 sqrt(2 / pi) and 0.044715 times it
+  constexpr float c1 = 1.5957691216057308f, c3 = 0.07135481627260025f;
+  switch (activation & ~DG_ACT_GATED) {
+    case DG_ACT_NONE: *a = {ACT_KIND_CLAMP, -__builtin_inff(), 0.f, 0.f}; return true;
+    case DG_ACT_RELU: *a = {ACT_KIND_CLAMP, 0.f, 0.f, 0.f}; return true;
+    case DG_ACT_SILU: *a = {ACT_KIND_SIGMOID, 0.f, 1.f, 0.f}; return true;
+    case DG_ACT_GELU: *a = {ACT_KIND_ERF, 0.f, 0.f, 0.f}; return true;
+    case DG_ACT_GELU_TANH: *a = {ACT_KIND_SIGMOID, 0.f, c1, c3}; return true;
+  }
+  return false;
+}
+
+template <bool GATED>
+static hipError_t launch_linear(const Mxfp4LinearParams<GATED>& p, const Mxfp4Plan& pl, int cus, hipStream_t hs) {
+  if (pl.skinny >= 0) return launch_mxfp4_skinny(p, pl.skinny, hs);
+  hipError_t e = launch_mxfp4_tile(p, pl.tile, pl.grid, hs);
+  if (e != hipSuccess || !pl.ws_bytes) return e;
+  const Mxfp4TileInfo t = mxfp4_tile_info(pl.tile);
+  const int split_tiles = pl.tiles_m * pl.tiles_n - pl.full_tiles;
+  const int grid = (int)std::min<long long>(((long long)split_tiles * t.bm * (t.bn / 8) + 255) / 256, (long long)cus * 8);
+  hipLaunchKernelGGL(linear_reduce_kernel<GATED>, dim3(grid), dim3(256), 0, hs, p, t.bm, t.bn, split_tiles);
+  return hipGetLastError();
+}
+
+static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" int dg_mxfp4_linear(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
+                               const uint16_t* bias, int activation, const uint16_t* residual, uint16_t* z, uint16_t* d,
+                               int m, int n, int k, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    Activation act;
+    if (!a || !a_sf || !b || !b_sf || !d || !activation_of(activation, &act)) return DG_ERR_INVALID_ARG;
+    if (m <= 0 || n <= 0 || k <= 0) return DG_ERR_INVALID_ARG;
+    if (misaligned(a, 16) || misaligned(b, 16) || misaligned(bias, 16) || misaligned(residual, 16) || misaligned(z, 16) ||
+        misaligned(d, 16) || misaligned(a_sf, 4) || misaligned(b_sf, 4))
+      return DG_ERR_INVALID_ARG;
+    const bool gated = activation & DG_ACT_GATED;
+    if (!mxfp4_sizes_fit(m, n, k) || (gated && n % 32 != 0)) return DG_ERR_UNSUPPORTED;
+    DeviceInfo di = current_device_info();
+    if (!di.ok) return DG_ERR_NO_DEVICE;
+    const int cus = dg_get_num_cus();
+    const Mxfp4Plan pl = plan_mxfp4(m, n, k, cus);
+    if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes || misaligned(workspace, 16))) return DG_ERR_INVALID_ARG;
+    log_mxfp4_plan("mxfp4_linear", m, n, k, pl);
+    const Mxfp4Params p{a, a_sf, b, b_sf, residual, d, static_cast<float*>(workspace), m, n, k,
+                        pl.tiles_m, pl.tiles_n, 8, pl.splits, pl.kb_per_split, pl.full_tiles, pl.units};
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    const hipError_t e = gated ? launch_linear(Mxfp4LinearParams<true>{p, bias, z, act}, pl, cus, hs)
+                               : launch_linear(Mxfp4LinearParams<false>{p, bias, z, act}, pl, cus, hs);
+    return e == hipSuccess ? DG_OK : DG_ERR_HIP;
+  } catch (...) {
+    return DG_ERR_HIP;
+  }
+}

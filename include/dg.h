@@ -436,6 +436,56 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
 size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
 
 /*
+ * MXFP4 linear layer: the dense GEMM with bias, activation and residual in its epilogue.  With
+ * u[i][j] = sum_k A[i][k] * B[j][k] + bias[j] in fp32,
+ *   d[i][j] = bf16( residual[i][j] + act(u[i][j]) )                        d, residual [m, n]
+ * and with a gated activation, whose gate rows are the first n/2 of B and whose up rows the others,
+ *   d[i][j] = bf16( residual[i][j] + act(u[i][j]) * u[i][n/2 + j] )        d, residual [m, n/2]
+ *   a, a_sf, b, b_sf as dg_mxfp4_gemm_nt
+ *   bias      [n] bf16, or NULL
+ *   activation  a dg_activation value, DG_ACT_GATED or-ed in for its gated form:
+ *               DG_ACT_NONE u; DG_ACT_RELU max(u, 0); DG_ACT_SILU u / (1 + exp(-u)); DG_ACT_GELU u * Phi(u), Phi
+ *               the normal distribution; DG_ACT_GELU_TANH u / (1 + exp(-2 sqrt(2/pi) (u + 0.044715 u^3))).
+ *               (DG_ACT_SILU | DG_ACT_GATED is SwiGLU.)  A NaN stays one; u = -infinity gives NaN in the last three.
+ *   residual  bf16, or NULL (0); may be d itself
+ *   z         [m, n] bf16(u), the pre-activation, which the backward pass needs, or NULL.  act takes
+ *             the unrounded u: d is the same with z and without
+ *   workspace as dg_mxfp4_gemm_nt, sized by dg_mxfp4_gemm_workspace_bytes(m, n, k, 0)
+ * An exponent byte 255 gives NaN results.  Requirements: as dg_mxfp4_gemm_nt's; gated: n % 32 == 0.
+ */
+typedef enum dg_activation {
+  DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_SILU = 2, DG_ACT_GELU = 3, DG_ACT_GELU_TANH = 4,
+  DG_ACT_GATED = 16   /* a flag */
+} dg_activation;
+int dg_mxfp4_linear(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
+                    const uint16_t* bias, int activation, const uint16_t* residual, uint16_t* z, uint16_t* d,
+                    int m, int n, int k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass up to the products: the gradient of u from dy, that of d (the residual's is dy
+ * itself), as the operands that they read.
+ *   dz[i][j] = dy[i][j] * act'(z[i][j]), and gated, with g = z[i][j] and p = z[i][n/2 + j],
+ *   dz[i][j] = dy[i][j] * p * act'(g),  dz[i][n/2 + j] = dy[i][j] * act(g)
+ * (ReLU's derivative at 0 is 0), rounded to bf16.
+ *   dy   [m, n] bf16 (gated: [m, n/2])
+ *   z    [m, n] bf16 from the forward pass; may be NULL with DG_ACT_NONE (ungated)
+ *   dz   [m, n] bf16, or NULL (may be z, or ungated dy, itself)
+ *   q, sf, qt, sft   dz as MXFP4 along n, and along m of the transposed operand, in the layouts of
+ *        dg_quantize_mxfp4 with k = n; each pair both or neither.  The layer's gradients are
+ *        dx = q . (w quantised along n)^T and dw = qt . (x quantised along m)^T, two dg_mxfp4_gemm_nt
+ *   dbias [n] fp32, the sums over the rows of dz before it is rounded, in a fixed order; or NULL
+ *   workspace  with dbias, dg_activation_backward_workspace_bytes(m, n) bytes, 16-byte aligned; may
+ *        be NULL when that is 0 (up to 128 rows)
+ * At least one output is given.  Requirements: m, n > 0; n % 128 == 0 (gated: n % 256 == 0) and m + 127
+ *   at most 2^31 - 1 (else DG_ERR_UNSUPPORTED).  Outputs overlap nothing but as said.
+ */
+int dg_activation_backward(const uint16_t* dy, const uint16_t* z, int activation, uint16_t* dz, uint8_t* q, int32_t* sf,
+                           uint8_t* qt, int32_t* sft, float* dbias, int m, int n, void* workspace, size_t workspace_bytes,
+                           void* stream);
+/* Bytes of that workspace (0: none; 0 also for invalid sizes).  Host-only. */
+size_t dg_activation_backward_workspace_bytes(int m, int n);
+
+/*
  * RMS norm with the residual's addition and a quantised output, the step in front
  * of a layer's GEMM.  Per row:
  *   h = bf16(x + residual)                 (residual NULL: h = x)

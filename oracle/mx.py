@@ -5,6 +5,7 @@ TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``).  Written from the definit
 """
 
 import numpy as np
+from scipy.special import ndtr
 
 from .formats import (
     E2M1_TABLE,
@@ -122,3 +123,35 @@ def sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rx, r, scale
     u = v if post_weight is None else v * post_weight
     dx = u if post_weight is None else rx[:, None] * (u - nx * np.mean(u * nx, axis=1, keepdims=True))
     return d, dx, dy * n, v * nx, scale * (1.0 if post_weight is None else post_weight) * d * nx
+
+
+def activation(u, name):
+    """float64 -> (act(u), act'(u)); ReLU's derivative at 0 is 0."""
+    if name == "none":
+        return u, np.ones_like(u)
+    if name == "relu":
+        return np.maximum(u, 0), (u > 0).astype(np.float64)
+    with np.errstate(over="ignore"):
+        if name == "gelu":
+            phi = ndtr(u)
+            return u * phi, phi + u * np.exp(-u * u / 2) / np.sqrt(2 * np.pi)
+        c = np.sqrt(2 / np.pi)
+        w, dw = (u, 1.0) if name == "silu" else (2 * c * (u + 0.044715 * u ** 3), 2 * c * (1 + 3 * 0.044715 * u ** 2))
+        s, not_s = 1 / (1 + np.exp(-w)), 1 / (1 + np.exp(w))
+        return u * s, s + u * s * not_s * dw
+
+
+def linear_epilogue(u, name, gated, residual=None):
+    """u [m, n] float64 -> d unrounded."""
+    half = u.shape[1] // 2
+    y = activation(u[:, :half], name)[0] * u[:, half:] if gated else activation(u, name)[0]
+    return y if residual is None else y + residual
+
+
+def linear_epilogue_backward(dy, z, name, gated):
+    """dz [m, n], unrounded."""
+    if not gated:
+        return dy * activation(z, name)[1]
+    half = z.shape[1] // 2
+    a, d = activation(z[:, :half], name)
+    return np.hstack([dy * z[:, half:] * d, dy * a])

@@ -107,3 +107,74 @@ def test_oracle_sandwich_gradients_are_those_of_differences(post, gated):
             up[name][at] += 1e-4
             dn[name][at] -= 1e-4
             assert abs((loss(up) - loss(dn)) / 2e-4 - grad[at]) < 1e-5 * (1 + np.abs(grad).max()), (name, at)
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", [
+    ({}, OK), (dict(bias=0), OK), (dict(residual=0), OK), (dict(z=0), OK), (dict(act=2 | 16), OK), (dict(act=4), OK),
+    (dict(m=1, n=16, k=128), OK),
+    (dict(a=0), 1), (dict(a_sf=0), 1), (dict(b=0), 1), (dict(b_sf=0), 1), (dict(d=0), 1), (dict(act=5), 1), (dict(act=-1), 1),
+    (dict(act=32), 1), (dict(act=21), 1), (dict(m=0), 1), (dict(n=0), 1), (dict(k=-1), 1),
+    (dict(a=A + 8), 1), (dict(b=A + 8), 1), (dict(bias=A + 8), 1), (dict(residual=A + 8), 1), (dict(z=A + 8), 1),
+    (dict(d=A + 8), 1), (dict(a_sf=A + 2), 1), (dict(b_sf=A + 2), 1),
+    (dict(k=192), 2), (dict(n=24), 2), (dict(n=48, act=16), 2), (dict(m=1 << 22, k=2048), 2), (dict(m=1 << 16, n=(1 << 14) + 32, k=128), 2),
+])
+def test_linear_refusals(change, status):
+    v = dict(a=A, a_sf=A, b=A, b_sf=A, bias=A, act=3, residual=A, z=A, d=A, m=8, n=256, k=256)
+    v.update(change)
+    need = dgm.lib().dg_mxfp4_gemm_workspace_bytes(v["m"], v["n"], v["k"], 256)
+    expect(dgm.lib().dg_mxfp4_linear(*v.values(), A if need else None, need, None), status)
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", [
+    ({}, OK), (dict(dz=0), OK), (dict(q=0, sf=0), OK), (dict(qt=0, sft=0), OK), (dict(dbias=0), OK), (dict(z=0, act=0), OK),
+    (dict(act=18), OK), (dict(m=300, ws=A), OK), (dict(q=0, sf=0, qt=0, sft=0, dz=0), OK), (dict(m=300, dbias=0, ws=0, less=1), OK),
+    (dict(dy=0), 1), (dict(z=0), 1), (dict(z=0, act=16), 1), (dict(q=0), 1), (dict(sf=0), 1), (dict(qt=0), 1), (dict(sft=0), 1),
+    (dict(dz=0, q=0, sf=0, qt=0, sft=0, dbias=0), 1), (dict(act=7), 1), (dict(m=0), 1), (dict(n=-128), 1),
+    (dict(m=300), 1), (dict(m=300, ws=A + 8), 1), (dict(m=300, ws=A, less=1), 1),
+    (dict(dy=A + 8), 1), (dict(z=A + 8), 1), (dict(dz=A + 8), 1), (dict(q=A + 8), 1), (dict(qt=A + 8), 1), (dict(sf=A + 2), 1),
+    (dict(sft=A + 2), 1), (dict(dbias=A + 8), 1),
+    (dict(n=192), 2), (dict(n=128, act=18), 2), (dict(m=0x7fffffff - 126), 2),
+])
+def test_activation_backward_refusals(change, status):
+    v = dict(dy=A, z=A, act=3, dz=A, q=A, sf=A, qt=A, sft=A, dbias=A, m=8, n=256, ws=0)
+    less = change.get("less", 0)
+    v.update({n: c for n, c in change.items() if n != "less"})
+    need = dgm.dg_activation_backward_workspace_bytes(v["m"], v["n"])
+    expect(dgm.lib().dg_activation_backward(*v.values(), need - less, None), status)
+
+
+def test_activation_backward_workspace_query():
+    f = dgm.dg_activation_backward_workspace_bytes
+    assert f(0, 128) == f(8, 0) == f(8, 100) == f(128, 256) == f(0x7fffffff, 128) == 0 and f(129, 256) == 2 * 256 * 4
+
+
+def test_linear_binding_checks_tensors():
+    q, sf = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="a: must be a device tensor"):
+        dgm.mxfp4_linear(q, sf, q, sf)
+    z = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="activation: expected"):
+        dgm.activation_backward(z, z, 9)
+    with pytest.raises(ValueError, match="dy: expected shape"):
+        dgm.activation_backward(z, z, dgm.ACT_SILU | dgm.ACT_GATED)
+    with pytest.raises(ValueError, match="dy: must be a device tensor"):
+        dgm.activation_backward(z, z, dgm.ACT_SILU)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_oracle_activation_gradients_are_those_of_differences(act, gated):
+    """The slope of sum(dy * d) against central differences, away from ReLU's kink."""
+    rng = np.random.default_rng(1)
+    z = rng.standard_normal((5, 16)) * 3
+    z = np.where(np.abs(z) < 0.01, 0.5, z)
+    dy = rng.standard_normal((5, 8 if gated else 16))
+    dz = X.linear_epilogue_backward(dy, z, act, gated)
+    for at in np.ndindex(*z.shape):
+        up, dn = z.copy(), z.copy()
+        up[at] += 1e-4
+        dn[at] -= 1e-4
+        slope = np.sum(dy * (X.linear_epilogue(up, act, gated) - X.linear_epilogue(dn, act, gated))) / 2e-4
+        assert abs(slope - dz[at]) < 1e-6 * (1 + np.abs(dz).max())
