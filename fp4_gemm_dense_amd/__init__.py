@@ -49,6 +49,10 @@ _SIGNATURES = {
     "dg_quantize_mxfp4": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "dg_mxfp4_gemm_nt": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "dg_mxfp4_gemm_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "dg_m_grouped_mxfp4_gemm_nt_ragged": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "dg_k_grouped_mxfp4_gemm_nt_ragged": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "dg_quantize_mxfp4_ragged": (_I, [_P, _I] + [_P] * 5 + [_I] * 3 + [_P]),
+    "dg_mxfp4_ragged_blocks": (_I, [_I, _I]),
     "dg_mxfp4_linear": (_I, [_P] * 5 + [_I] + [_P] * 3 + [_I, _I, _I, _P, _SZ, _P]),
     "dg_activation_backward": (_I, [_P, _P, _I] + [_P] * 6 + [_I, _I, _P, _SZ, _P]),
     "dg_activation_backward_workspace_bytes": (_SZ, [_I, _I]),
@@ -565,6 +569,63 @@ def dg_mxfp4_gemm_nt(a, a_sf, b, b_sf, c, d, workspace=None):
     return d
 
 
+def dg_mxfp4_ragged_blocks(m, num_groups):
+    """Blocks of 128 rows that any m rows in num_groups ragged groups need at most."""
+    return int(lib().dg_mxfp4_ragged_blocks(m, num_groups))
+
+
+def _groups(ms, index):
+    """Checks the groups' row counts; returns their number and address."""
+    if ms.dim() != 1:
+        raise ValueError(f"ms: expected [num_groups], got {tuple(ms.shape)}")
+    return ms.shape[0], _arg(ms, _I32S, ms.shape, index, "ms")
+
+
+def dg_quantize_mxfp4_ragged(x, ms, q=None, sf=None, qt=None, sft=None):
+    """x [m, k] (bf16 or fp32), its rows in groups of ms [G] int32 -> MXFP4 (see include/dg.h): qt [k, 64 B] and sft
+    [B, k] in blocks along each group's rows, B = dg_mxfp4_ragged_blocks(m, G); q [m, k/2] and sf [k/128, m] or None."""
+    m, k = x.shape
+    dev = x.get_device()
+    xp = _arg(x, _X_TYPES, x.shape, dev, "x")
+    G, mp = _groups(ms, dev)
+    blocks = dg_mxfp4_ragged_blocks(m, G)
+    _call("dg_quantize_mxfp4_ragged", dev, xp, _X_TYPES[x.dtype], mp, _arg(q, _U8S, (m, k // 2), dev, "q"),
+          _arg(sf, _I32S, (k // 128, m), dev, "sf"), _arg(qt, _U8S, (k, blocks * 64), dev, "qt"),
+          _arg(sft, _I32S, (blocks, k), dev, "sft"), m, k, G)
+
+
+def _ragged_operands(a, a_sf, b, b_sf, ms):
+    """Checks the operands of dg_m_grouped_mxfp4_gemm_nt_ragged; returns (m, n, k, G, device index, ms' address)."""
+    if b.dim() != 3:
+        raise ValueError(f"b: expected [num_groups, n, k/2], got {tuple(b.shape)}")
+    (m, kh), index = a.shape, a.get_device()
+    G, mp = _groups(ms, index)
+    n, kb = b.shape[1], kh // 64
+    for t, dtypes, shape, name in ((a, _U8S, (m, kh), "a"), (a_sf, _I32S, (kb, m), "a_sf"), (b, _U8S, (G, n, kh), "b"),
+                                   (b_sf, _I32S, (G, kb, n), "b_sf")):
+        _arg(t, dtypes, shape, index, name)
+    return m, n, 2 * kh, G, index, mp
+
+
+def dg_m_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms, d):
+    """d[r] = a[r] . b[g]^T for the rows r of group g, ms [G] int32 rows a group one behind another; a [M, K/2],
+    a_sf [K/128, M], b [G, N, K/2], b_sf [G, K/128, N], d [M, N] bf16 (rows behind the last group's are left)."""
+    m, n, k, G, index, mp = _ragged_operands(a, a_sf, b, b_sf, ms)
+    _call("dg_m_grouped_mxfp4_gemm_nt_ragged", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), mp,
+          _req_given(d, _BF, (m, n), index, "d"), m, n, k, G)
+    return d
+
+
+def dg_k_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms, d):
+    """d[g] = a . b^T over the K blocks of group g: a [M, K/2] and b [N, K/2] with a_sf and b_sf as
+    dg_quantize_mxfp4_ragged's qt and sft, ms [G] int32 the rows that they were made with; d [G, M, N] bf16."""
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    G, mp = _groups(ms, index)
+    _call("dg_k_grouped_mxfp4_gemm_nt_ragged", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), mp,
+          _req_given(d, _BF, (G, m, n), index, "d"), m, n, k, G)
+    return d
+
+
 # dg_activation (include/dg.h); ACT_GATED is or-ed in
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_GATED = 0, 1, 2, 3, 4, 16
 
@@ -814,6 +875,43 @@ def mxfp4_gemm_nt(a, a_sf, b, b_sf, c=None):
         wp = ws.data_ptr()
     _call("dg_mxfp4_gemm_nt", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), cp, d.data_ptr(), m, n,
           k, wp, nbytes)
+    return d
+
+
+def quantize_mxfp4_ragged(x, ms):
+    """(q, sf, qt, sft) of x [m, k] (bf16 or fp32), whose rows lie in groups of ms [G] int32 (on the device): q and sf the
+    operand of m_grouped_mxfp4_gemm_nt_ragged, qt and sft that of k_grouped_mxfp4_gemm_nt_ragged."""
+    (m, k), index, dev = x.shape, x.get_device(), x.device
+    xp = _arg(x, _X_TYPES, x.shape, index, "x")
+    G, mp = _groups(ms, index)
+    blocks = (_lib or load_library()).dg_mxfp4_ragged_blocks(m, G)
+    q, sf = _new((m, k // 2), _U8, dev), _new((k // 128, m), torch.int32, dev)
+    qt, sft = _new((k, blocks * 64), _U8, dev), _new((blocks, k), torch.int32, dev)
+    _call("dg_quantize_mxfp4_ragged", index, xp, _X_TYPES[x.dtype], mp, q.data_ptr(), sf.data_ptr(), qt.data_ptr(),
+          sft.data_ptr(), m, k, G)
+    return q, sf, qt, sft
+
+
+def m_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms, out=None):
+    """d [M, N] bf16 (a new tensor unless out is given): d[r] = a[r] . b[g]^T for the rows r of group g, ms [G] int32 rows
+    a group.  Rows behind the last group's are left as they are (in a new tensor: undefined)."""
+    m, n, k, G, index, mp = _ragged_operands(a, a_sf, b, b_sf, ms)
+    d = _new((m, n), torch.bfloat16, a.device) if out is None else out
+    dp = d.data_ptr() if out is None else _arg(out, _BF, (m, n), index, "out")
+    _call("dg_m_grouped_mxfp4_gemm_nt_ragged", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), mp, dp,
+          m, n, k, G)
+    return d
+
+
+def k_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms, out=None):
+    """d [G, M, N] bf16 (a new tensor unless out is given): d[g] = a . b^T over the rows of group g that qt and sft of
+    quantize_mxfp4_ragged (of dy as a, of x as b, both with this ms) hold."""
+    m, n, k, index = _mxfp4_operands(a, a_sf, b, b_sf)
+    G, mp = _groups(ms, index)
+    d = torch.empty(G, m, n, dtype=torch.bfloat16, device=a.device) if out is None else out
+    dp = d.data_ptr() if out is None else _arg(out, _BF, (G, m, n), index, "out")
+    _call("dg_k_grouped_mxfp4_gemm_nt_ragged", index, a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), mp, dp,
+          m, n, k, G)
     return d
 
 

@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["api.cpp", "planner.cpp", "fp8_gemm.hip", "fp8_gemm_wide.hip", "ffn.hip", "noalloc.hip", "skinny.hip",
-           "quant.hip", "norm.hip", "mxfp4_gemm.hip", "mxfp4_linear.hip", "activation.hip"]
+           "quant.hip", "norm.hip", "mxfp4_gemm.hip", "mxfp4_linear.hip",
+           "mxfp4_grouped.hip", "activation.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 COMMON = [

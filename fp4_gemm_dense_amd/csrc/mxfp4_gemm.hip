@@ -60,14 +60,12 @@
 namespace dg {
 
 static const Mxfp4TileInfo kMxTiles[] = {
-#define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG},
+#define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG, MxTile<MT, NT, WM, WN, R, KG>::LDS},
     DG_MXFP4_TILES(X)
 #undef X
 };
 
 Mxfp4TileInfo mxfp4_tile_info(int id) { return kMxTiles[id]; }
-
-constexpr int kMxSkinnyIdBase = 100;   // in DG_FORCE_MXFP4
 
 static int skinny_rows(int id) {
   switch (id) {
@@ -106,6 +104,21 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
   return pl;
 }
 
+int mxfp4_forced() {
+  const char* f = std::getenv("DG_FORCE_MXFP4");   // (for tuning)
+  return f ? std::atoi(f) : -1;
+}
+
+// Of each tile: a stage of 256 values of K, and a unit's fixed share, in microseconds.
+static constexpr double kStage[] = {1.85, 1.12, 0.76, 0.69, 0.57, 0.81, 0.52, 1.05};
+static constexpr double kUnit[] = {4.5, 2.0, 1.0, 1.0, 1.8, 1.9, 1.6, 2.5};
+static_assert(sizeof(kStage) / sizeof(kStage[0]) == kMxTileCount && sizeof(kMxTiles) / sizeof(kMxTiles[0]) == kMxTileCount, "tiles");
+
+double mxfp4_tile_time(int id, long long units, int kb, int cus) {
+  const int kg = kMxTiles[id].kg, whole = ((kb + 1) / 2 + kg - 1) / kg;
+  return (double)((units + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
+}
+
 // Up to 32 rows: the streaming kernel reads all of A once per 16 columns, so it is taken
 // while row blocks x columns stay small (measured against the best tile: 1 x 4096 x 7168
 // 6.0 against 9.7 us, 16 x 7168 x 2048 5.9 / 5.7, 32 x 4096 x 7168 8.5 / 9.9; past the
@@ -116,12 +129,8 @@ static Mxfp4Plan plan_mxfp4_tile(int m, int n, int k, int cus, int id) {
 // 247 shapes, M 1 to 8192, 512 x 2048 to 32768 x 512 and 7168 x 16384 (geometric mean
 // 0.2 % over the best tile of each; worst 64 x 7168 x 16384, 18 %).
 Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
-  constexpr double kStage[] = {1.85, 1.12, 0.76, 0.69, 0.57, 0.81, 0.52, 1.05};
-  constexpr double kUnit[] = {4.5, 2.0, 1.0, 1.0, 1.8, 1.9, 1.6, 2.5};
   constexpr double kSplit = 5.7, kPartialRate = 3.6e6, kStreamRate = 40.0e3;   // us, bytes per us
-  constexpr int kTiles = (int)(sizeof(kMxTiles) / sizeof(kMxTiles[0]));
-  int force = -1;
-  if (const char* f = std::getenv("DG_FORCE_MXFP4")) force = std::atoi(f);   // pins the kernel (for tuning)
+  const int force = mxfp4_forced();
   int skinny = -1;
   const int mt = m <= 16 ? 1 : m <= 32 ? 2 : 0;
   if (mt && (long long)mt * n <= 8192) skinny = mt >> 1;
@@ -132,12 +141,11 @@ Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus) {
     return best;
   }
   double best_t = 1e30;
-  for (int id = 0; id < kTiles; ++id) {
+  for (int id = 0; id < kMxTileCount; ++id) {
     const int kg = kMxTiles[id].kg;
     const Mxfp4Plan pl = plan_mxfp4_tile(m, n, k, cus, id);
     if (kg > 1 && pl.units > cus) continue;   // one unit per workgroup (a pinned one is passed over, too)
-    const int whole = ((k / 128 + 1) / 2 + kg - 1) / kg;
-    double t = (double)((pl.full_tiles + cus - 1) / cus) * (whole * kStage[id] + kUnit[id]);
+    double t = mxfp4_tile_time(id, pl.full_tiles, k / 128, cus);
     if (pl.splits > 1)
       t += (pl.kb_per_split + 1) / 2 * kStage[id] + kUnit[id] + kSplit + 2.0 * (double)pl.ws_bytes / kPartialRate;
     t = std::max(t, 0.5 * n * k / (kStreamRate * std::min(pl.units, cus)));

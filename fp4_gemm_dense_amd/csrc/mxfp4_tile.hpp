@@ -247,12 +247,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
   const uint32_t Kh = (uint32_t)p.k >> 1;   // bytes of an operand row
   const int KB = p.k >> 7;
 
-  const int G = gridDim.x;
+  int G = gridDim.x;
   read_arguments(p);
-  // Workgroups go round the eight XCDs: one XCD's take units side by side, whose A and B
-  // rows its L2 then holds once.
-  const int xcd = blockIdx.x & 7;
-  const int vb = xcd * (G >> 3) + min(xcd, G & 7) + (int)(blockIdx.x >> 3);
   int units = p.units;
   int* const ends = reinterpret_cast<int*>(smem_all + T::LDS);
   if constexpr (GROUPED) {
@@ -270,7 +266,13 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
         for (size_t i = (size_t)blockIdx.x * T::THREADS + threadIdx.x; i < vecs; i += (size_t)G * T::THREADS) o[i] = v4i{0, 0, 0, 0};
       }
     }
+    G = min(G, units);
+    if ((int)blockIdx.x >= G) return;
   }
+  // Workgroups go round the eight XCDs: one XCD's take units side by side, whose A and B
+  // rows its L2 then holds once.
+  const int xcd = blockIdx.x & 7;
+  const int vb = xcd * (G >> 3) + min(xcd, G & 7) + (int)(blockIdx.x >> 3);
   if (vb >= units) return;
 
   // the lane, for terms formed where they are used
@@ -739,8 +741,9 @@ __device__ __forceinline__ void skinny_linear_out(const Mxfp4LinearParams<GATED>
   *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
 }
 
+// Rows [R0, R1) of A, at most 16 MT, by the B at p.b.
 template <int MT, int P, typename Params>
-__global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Params p) {
+__device__ __forceinline__ void skinny_rows_product(const Params& p, const uint8_t* b, const int32_t* b_sf, int R0, int R1) {
   constexpr MxKind KIND = Params::KIND;
   constexpr int NW = MX_SKINNY_WAVES;
   __shared__ v4f red[NW][64];
@@ -752,16 +755,16 @@ __global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Para
   const int KB = p.k >> 7, PAIRS = (KB + 1) >> 1;
   const int n0 = blockIdx.x * 16;   // (N % 16 == 0: every column is there)
   const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
-  const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
+  const v4i rsB = make_buffer_rsrc(b, (uint32_t)N * Kh);
   const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
-  const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
+  const v4i rsSB = make_buffer_rsrc(b_sf, (uint32_t)KB * (uint32_t)N * 4u);
   // per-lane offsets; a row past the end reads zeros (and its results are not stored)
   uint32_t a_off[MT], sa_off[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int r = i * 16 + lrow;
-    a_off[i] = r < M ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
-    sa_off[i] = r < M ? (uint32_t)r * 4u : kBufferOutOfRange;
+    const int r = R0 + i * 16 + lrow;
+    a_off[i] = r < R1 ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
+    sa_off[i] = r < R1 ? (uint32_t)r * 4u : kBufferOutOfRange;
   }
   // (gated: the gate's eight rows, and then the other half's of the same outputs)
   const int b_row = KIND == MX_GATED ? (lrow >> 3) * (N >> 1) + (n0 >> 1) + (lrow & 7) : n0 + lrow;
@@ -807,8 +810,8 @@ __global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Para
     if (mt > 0) __syncthreads();
     red[wave][lane] = acc[mt];
     __syncthreads();
-    const int row = mt * 16 + lrow;
-    if (wave == 0 && row < M) {
+    const int row = R0 + mt * 16 + lrow;
+    if (wave == 0 && row < R1) {
       v4f v = red[0][lane];
 #pragma unroll
       for (int w = 1; w < NW; ++w) v += red[w][lane];
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Para
         continue;
       }
       const size_t at = (size_t)row * N + n0 + 4 * lgrp;
-      if (p.c) {
+      if (KIND != MX_RAGGED && p.c) {
         const uint2 cv = *reinterpret_cast<const uint2*>(p.c + at);
         v[0] += __uint_as_float(cv.x << 16);
         v[1] += __uint_as_float(cv.x & 0xffff0000u);
@@ -829,8 +832,10 @@ __global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Para
   }
 }
 
-// Groups of one call, and their table in LDS (ends and starts) behind a tile's ring.
-constexpr int kMaxGroups = 1024, kMaxTableBytes = (2 * kMaxGroups + 1) * 4;
+// Groups of one call, and the bytes of their table (ends and starts) in LDS behind a tile's
+// ring; not every ring leaves room for the table of many.
+constexpr int kMaxGroups = 1024, kLdsBytes = 160 * 1024;
+inline size_t group_table_bytes(int groups) { return (size_t)(2 * groups + 1) * 4; }
 
 // id, MT, NT, WM, WN, ring slots, K groups
 #define DG_MXFP4_TILES(X) \
@@ -851,7 +856,7 @@ static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t st
     using T = MxTile<MT, NT, WM, WN, R, KG>;                                                                      \
     static const hipError_t attr =                                                                                \
         hipFuncSetAttribute(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T, P>),                              \
-                            hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS + (P::KIND >= MX_RAGGED ? kMaxTableBytes : 0)); \
+                            hipFuncAttributeMaxDynamicSharedMemorySize, P::KIND >= MX_RAGGED ? kLdsBytes : T::LDS);   \
     if (attr != hipSuccess) return attr;                                                                          \
     hipLaunchKernelGGL((mxfp4_tile_kernel<T, P>), dim3(grid), dim3(T::THREADS), T::LDS + table_bytes, stream, p); \
     return hipGetLastError();                                                                                     \
@@ -862,17 +867,39 @@ static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t st
   return hipErrorInvalidValue;
 }
 
+template <int MT, int P, typename Params>
+__global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Params p) {
+  if constexpr (Params::KIND != MX_RAGGED) {
+    skinny_rows_product<MT, P>(p, p.b, p.b_sf, 0, p.m);
+  } else {
+    // group blockIdx.y: its rows follow those of the groups before it
+    const int g = blockIdx.y, lane = threadIdx.x & 63;
+    long long before = 0;
+    for (int h = lane; h < g; h += 64) before += max(p.ms[h], 0);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o, 64);
+    const int r0 = __builtin_amdgcn_readfirstlane((int)min(before, (long long)p.m));
+    const int r1 = __builtin_amdgcn_readfirstlane((int)min(before + max(p.ms[g], 0), (long long)p.m));
+    const uint8_t* b = p.b + (size_t)g * (size_t)p.n * (size_t)(p.k >> 1);
+    const int32_t* b_sf = p.b_sf + (size_t)g * (size_t)(p.k >> 7) * (size_t)p.n;
+    for (int r = r0; r < r1; r += 16 * MT) {
+      if (r != r0) __syncthreads();   // (the waves' sums are read)
+      skinny_rows_product<MT, P>(p, b, b_sf, r, min(r + 16 * MT, r1));
+    }
+  }
+}
+
 // id, MT, pairs in flight per wave
 #define DG_MXFP4_SKINNY(X) \
   X(0, 1, 4)               \
   X(1, 2, 4)
 
 template <typename Params>
-static hipError_t launch_mxfp4_skinny(const Params& p, int id, hipStream_t stream) {
+static hipError_t launch_mxfp4_skinny(const Params& p, int id, hipStream_t stream, int groups = 1) {
   switch (id) {
 #define X(i, MT, P)                                                                                                       \
   case i:                                                                                                                 \
-    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, P, Params>), dim3(p.n / 16), dim3(MX_SKINNY_WAVES * 64), 0, stream, p); \
+    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, P, Params>), dim3(p.n / 16, groups), dim3(MX_SKINNY_WAVES * 64), 0, stream, p); \
     return hipGetLastError();
     DG_MXFP4_SKINNY(X)
 #undef X
@@ -889,8 +916,12 @@ Mxfp4Plan plan_mxfp4(int m, int n, int k, int cus);
 bool mxfp4_sizes_fit(int m, int n, int k);
 void log_mxfp4_plan(const char* call, int m, int n, int k, const Mxfp4Plan& pl);   // (with DG_LOG=1)
 struct Mxfp4TileInfo {
-  int bm, bn, kg;
+  int bm, bn, kg, lds;
 };
 Mxfp4TileInfo mxfp4_tile_info(int id);
+constexpr int kMxTileCount = 8, kMxSkinnyIdBase = 100;
+int mxfp4_forced();   // the kernel that DG_FORCE_MXFP4 pins (kMxSkinnyIdBase and up: a streaming one), or -1
+// Estimated microseconds of `units` whole tiles of kb K blocks each.
+double mxfp4_tile_time(int id, long long units, int kb, int cus);
 
 }  // namespace dg

@@ -436,6 +436,52 @@ int dg_mxfp4_gemm_nt(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, co
 size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
 
 /*
+ * MXFP4 products grouped by expert with ragged sizes: the rows of the groups lie one behind
+ * another without padding, and ms[g] >= 0, int32 on the device and read only there, counts those
+ * of group g (0 for none).  Negative counts are 0, and the groups' rows are cut at m.
+ *
+ * Along M: d[r][j] = bf16( sum_k A[r][k] * B_g[j][k] ) for every row r of group g.  Rows behind the
+ * last group's are not written.
+ *   a    [m, k/2], a_sf [k/128, m]          as dg_mxfp4_gemm_nt
+ *   b    [num_groups, n, k/2], b_sf [num_groups, k/128, n]   (dg_quantize_mxfp4's q and sf; its
+ *        qt and sft, with the weights' n and k changed about, for the input's gradient)
+ *   d    [m, n] bf16
+ * Requirements: as dg_mxfp4_gemm_nt's (b: per group); num_groups <= 1024, else DG_ERR_UNSUPPORTED.
+ */
+int dg_m_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
+                                      const int32_t* ms, uint16_t* d, int m, int n, int k, int num_groups, void* stream);
+
+/*
+ * The operands of the weights' gradients, whose products sum over a group's rows: x quantised in
+ * blocks of 32 rows of one group, each group's rows counted from its first and filled up with
+ * zeros to a multiple of 128.  Group g has ceil(ms[g] / 128) blocks of 128 rows, behind those of
+ * the groups before it, and B = dg_mxfp4_ragged_blocks(m, num_groups) is room for any sizes.
+ *   x      [m, k]        bf16 (DG_BF16) or fp32 (DG_F32)
+ *   q, sf  [m, k/2], [k/128, m]   as dg_quantize_mxfp4, both or neither; rows behind the last
+ *          group's are not written
+ *   qt     [k, 64 B]     E2M1 pairs along the rows
+ *   sft    [B, k]        int32; blocks behind the last group's are not written (in qt neither)
+ * Values, exponents and rounding as dg_quantize_mxfp4.  Requirements: k % 128 == 0, m + 127 at most
+ * 2^31 - 1, num_groups <= 1024 (else DG_ERR_UNSUPPORTED).
+ */
+int dg_quantize_mxfp4_ragged(const void* x, int x_type, const int32_t* ms, uint8_t* q, int32_t* sf, uint8_t* qt, int32_t* sft,
+                             int m, int k, int num_groups, void* stream);
+/* (m + 127 * num_groups) / 128, rounded down: blocks of 128 rows that any m rows in num_groups groups
+ * need at most.  0 for sizes below 1 and more than 1024 groups.  Host-only. */
+int dg_mxfp4_ragged_blocks(int m, int num_groups);
+
+/*
+ * Along K, on those operands: d[g][i][j] = bf16( sum over the rows r of group g of A[i][r] * B[j][r] )
+ * (a from dy and b from x: the weight gradient of each expert).
+ *   a    [m, k/2], a_sf [k/128, m]; b [n, k/2], b_sf [k/128, n]: qt and sft of two calls with the same
+ *        ms, whose rows are m and n here; k = 128 * dg_mxfp4_ragged_blocks(rows, num_groups)
+ *   d    [num_groups, m, n] bf16, every element written (0 for a group without rows)
+ * Blocks of K are cut at k / 128.  Requirements: as dg_mxfp4_gemm_nt's (d: per group); num_groups <= 1024.
+ */
+int dg_k_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
+                                      const int32_t* ms, uint16_t* d, int m, int n, int k, int num_groups, void* stream);
+
+/*
  * MXFP4 linear layer: the dense GEMM with bias, activation and residual in its epilogue.  With
  * u[i][j] = sum_k A[i][k] * B[j][k] + bias[j] in fp32,
  *   d[i][j] = bf16( residual[i][j] + act(u[i][j]) )                        d, residual [m, n]

@@ -155,3 +155,45 @@ def linear_epilogue_backward(dy, z, name, gated):
     half = z.shape[1] // 2
     a, d = activation(z[:, :half], name)
     return np.hstack([dy * z[:, half:] * d, dy * a])
+
+
+def group_rows(ms, m):
+    """Row counts -> [(first row, end)] of each group: negative counts are 0, rows are cut at m."""
+    ends = np.minimum(np.cumsum(np.maximum(np.asarray(ms, dtype=np.int64), 0)), m)
+    return list(zip(np.concatenate([[0], ends[:-1]]).astype(int), ends.astype(int)))
+
+
+def quantize_mxfp4_ragged(x, ms, blocks):
+    """float64 [m, k] -> (qt [k, 64 blocks], sft [blocks, k], 128-row blocks used): each group's rows quantised along the
+    rows, padded to 128, one group behind another."""
+    m, k = x.shape
+    qt, sft, at = np.zeros((k, blocks * 64), np.uint8), np.zeros((blocks, k), np.int32), 0
+    for s, e in group_rows(ms, m):
+        if e > s:
+            q, sf = quantize_mxfp4_transposed(x[s:e])
+            nb = sf.shape[0]
+            qt[:, at * 64:(at + nb) * 64], sft[at:at + nb], at = q, sf, at + nb
+    return qt, sft, at
+
+
+def m_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms):
+    """[(rows of a group, its D unrounded float64, sum |a b|)]."""
+    av = dequant_mxfp4(a, a_sf)
+    out = []
+    for g, (s, e) in enumerate(group_rows(ms, len(av))):
+        bv = dequant_mxfp4(b[g], b_sf[g]) if e > s else np.zeros((b.shape[1], av.shape[1]))
+        out.append((slice(s, e), av[s:e] @ bv.T, np.abs(av[s:e]) @ np.abs(bv).T))
+    return out
+
+
+def k_grouped_mxfp4_gemm_nt_ragged(a, a_sf, b, b_sf, ms):
+    """(D [G, m, n] unrounded float64, sum |a b|)."""
+    av, bv = dequant_mxfp4(a, a_sf), dequant_mxfp4(b, b_sf)
+    kb, at, d, s = a_sf.shape[0], 0, [], []
+    for rows in ms:
+        end = min(kb, at + (max(int(rows), 0) + 127) // 128)
+        k = slice(at * 128, end * 128)
+        d.append(av[:, k] @ bv[:, k].T)
+        s.append(np.abs(av[:, k]) @ np.abs(bv[:, k]).T)
+        at = end
+    return np.stack(d), np.stack(s)

@@ -178,3 +178,58 @@ def test_oracle_activation_gradients_are_those_of_differences(act, gated):
         dn[at] -= 1e-4
         slope = np.sum(dy * (X.linear_epilogue(up, act, gated) - X.linear_epilogue(dn, act, gated))) / 2e-4
         assert abs(slope - dz[at]) < 1e-6 * (1 + np.abs(dz).max())
+
+
+RAGGED = [
+    ({}, OK), (dict(m=1, n=16, k=128, groups=1), OK), (dict(groups=1024), OK),
+    (dict(a=0), 1), (dict(a_sf=0), 1), (dict(b=0), 1), (dict(b_sf=0), 1), (dict(ms=0), 1), (dict(d=0), 1),
+    (dict(m=0), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(groups=0), 1), (dict(groups=-3), 1),
+    (dict(a=A + 8), 1), (dict(b=A + 8), 1), (dict(d=A + 8), 1), (dict(a_sf=A + 2), 1), (dict(b_sf=A + 2), 1), (dict(ms=A + 2), 1),
+    (dict(k=192), 2), (dict(n=24), 2), (dict(groups=1025), 2), (dict(m=1 << 22, k=2048), 2), (dict(n=1 << 22, k=2048), 2),
+    (dict(m=1 << 16, n=(1 << 14) + 16, k=128), 2),
+]
+
+
+@no_gpu
+@pytest.mark.parametrize("entry", ["dg_m_grouped_mxfp4_gemm_nt_ragged", "dg_k_grouped_mxfp4_gemm_nt_ragged"])
+@pytest.mark.parametrize("change,status", RAGGED)
+def test_ragged_gemm_refusals(entry, change, status):
+    v = dict(a=A, a_sf=A, b=A, b_sf=A, ms=A, d=A, m=8, n=256, k=256, groups=4)
+    v.update(change)
+    expect(getattr(dgm.lib(), entry)(*v.values(), None), status)
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", [
+    ({}, OK), (dict(q=0, sf=0), OK), (dict(x_type=1), OK), (dict(groups=1024), OK),
+    (dict(x=0), 1), (dict(ms=0), 1), (dict(q=0), 1), (dict(sf=0), 1), (dict(qt=0), 1), (dict(sft=0), 1), (dict(x_type=2), 1),
+    (dict(m=0), 1), (dict(k=0), 1), (dict(groups=0), 1), (dict(x=A + 8), 1), (dict(q=A + 8), 1), (dict(qt=A + 8), 1),
+    (dict(sf=A + 2), 1), (dict(sft=A + 2), 1), (dict(ms=A + 1), 1), (dict(k=64), 2), (dict(groups=1025), 2),
+    (dict(m=0x7fffffff - 126), 2),
+])
+def test_quantize_ragged_refusals(change, status):
+    v = dict(x=A, x_type=0, ms=A, q=A, sf=A, qt=A, sft=A, m=8, k=256, groups=4)
+    v.update(change)
+    expect(dgm.lib().dg_quantize_mxfp4_ragged(*v.values(), None), status)
+
+
+def test_ragged_blocks():
+    f = dgm.dg_mxfp4_ragged_blocks
+    assert f(0, 1) == f(1, 0) == f(1, 1025) == 0
+    assert f(1, 1) == 1 and f(128, 1) == 1 and f(129, 1) == 2 and f(2, 2) == 2 and f(100, 100) == 100
+    rng = np.random.default_rng(1)
+    for _ in range(200):
+        ms = rng.integers(0, 400, rng.integers(1, 9))
+        assert sum(-(-int(r) // 128) for r in ms) <= f(max(int(ms.sum()), 1), len(ms))
+
+
+def test_ragged_binding_checks_tensors():
+    q, sf, ms = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="ms: must be a device tensor"):
+        dgm.m_grouped_mxfp4_gemm_nt_ragged(q, sf, q[None].repeat(2, 1, 1), sf[None].repeat(2, 1, 1), ms)
+    with pytest.raises(ValueError, match="b: expected"):
+        dgm.m_grouped_mxfp4_gemm_nt_ragged(q, sf, q, sf, ms)
+    with pytest.raises(ValueError, match="x: must be a device tensor"):
+        dgm.quantize_mxfp4_ragged(torch.zeros(4, 256), ms)
+    with pytest.raises(ValueError, match="a: must be a device tensor"):
+        dgm.k_grouped_mxfp4_gemm_nt_ragged(q, sf, q, sf, ms)
