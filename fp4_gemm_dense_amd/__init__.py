@@ -59,8 +59,8 @@ _SIGNATURES = {
     "dg_add_rms_norm": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P]),
     "dg_add_rms_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
     "dg_add_rms_norm_backward_workspace_bytes": (_SZ, [_I, _I]),
-    "dg_sandwich_norm": (_I, [_P] * 8 + [_I, _P, _P, _I, _I, _I, ctypes.c_float, ctypes.c_float, _P]),
-    "dg_sandwich_norm_backward": (_I, [_P] * 14 + [_I, _I, _I, ctypes.c_float, _P, _SZ, _P]),
+    "dg_sandwich_norm": (_I, [_P] * 8 + [_I, _P, _P, _I, _I, _I, ctypes.c_double, ctypes.c_float, _P]),
+    "dg_sandwich_norm_backward": (_I, [_P] * 14 + [_I, _I, _I, ctypes.c_double, _P, _SZ, _P]),
     "dg_sandwich_norm_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "dg_fp8_gemm_nt_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "dg_get_mk_alignment_for_contiguous_layout": (_I, []),

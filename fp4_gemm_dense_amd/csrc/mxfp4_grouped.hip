@@ -9,8 +9,7 @@
 // the tiles of the groups before each (two scans by one wave, into LDS) and finds a tile's group
 // by comparing its index with 64 ends at a time.  A tile's rows past its group's end belong to
 // the next one: they are read and multiplied, and not stored.  The copies run on from tile to
-// tile over the groups' borders.  Few rows a group: the streaming kernel, one workgroup per 16
-// columns of each group, which reads the weights of the groups that have rows once.
+// tile over the groups' borders.
 #include <algorithm>
 
 #include "../../include/dg.h"
@@ -22,76 +21,53 @@ namespace dg {
 using RaggedParams = Mxfp4GroupedParams<MX_RAGGED>;
 using KGroupParams = Mxfp4GroupedParams<MX_KGROUP>;
 
-// (a launch has fewer than 2^32 threads: 256 and 512 a workgroup)
-constexpr long long kMaxSkinnyGrid = 1LL << 24, kMaxKgGrid = 1LL << 22;
-
-static bool tile_serves(const Mxfp4TileInfo& t, int groups, long long units) {
-  return t.lds + group_table_bytes(groups) <= kLdsBytes && (t.kg == 1 || units <= kMaxKgGrid);
-}
-
 struct GroupedPlan {
-  int skinny, tile, grid;
+  int tile, grid;
 };
 
-// Tiles of the whole call as the host can guess them: groups of equal size, and half a tile
-// more for each where a group has several.
-static long long ragged_units(int m, int groups, int bm, int tiles_n, long long* most) {
-  const int with_rows = std::min(m, groups);
-  const double rows = (double)m / with_rows;
-  *most = ((long long)m / bm + with_rows) * tiles_n;
-  const double tiles = rows <= bm ? 1.0 : rows / bm + 0.5;
-  return std::min(*most, (long long)(with_rows * tiles * tiles_n + 0.5));
-}
-
-static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
+// The tile with the least estimated time.  units(tile): how many of it the call has by the host's
+// guess, and the most it can have.  A ring has to leave room for the table; tiles with K groups
+// take one unit per workgroup; the 256x256 tile runs 15-20 % behind its estimate here
+// (measured over 15 calls).
+template <typename F>
+static GroupedPlan plan_grouped(int groups, int kb, int cus, F units) {
   const int force = mxfp4_forced();
-  GroupedPlan best{-1, 0, 0};
-  if (force >= kMxSkinnyIdBase && (long long)(n / 16) * groups < kMaxSkinnyGrid) {
-    best.skinny = std::min(force - kMxSkinnyIdBase, 1);
-    return best;
-  }
-  const int rows = (m + groups - 1) / groups;
-  if (force < 0 && rows <= 16 && (long long)(n / 16) * groups < kMaxSkinnyGrid) {
-    best.skinny = rows <= 8 ? 0 : 1;
-    return best;
-  }
+  GroupedPlan best{2, 0};
   double best_t = 1e30;
   for (int id = 0; id < kMxTileCount; ++id) {
     const Mxfp4TileInfo t = mxfp4_tile_info(id);
     long long most;
-    const long long units = ragged_units(m, groups, t.bm, (n + t.bn - 1) / t.bn, &most);
-    if (!tile_serves(t, groups, most)) continue;
-    double us = mxfp4_tile_time(id, units, k / 128, cus);
-    if (id == force) us = 0.0;
+    const long long guess = units(t, &most);
+    if (t.lds + group_table_bytes(groups) > kLdsBytes || (t.kg > 1 && most > cus)) continue;
+    const double us = id == force ? 0.0 : mxfp4_tile_time(id, guess, kb, cus) * (t.bm == 256 ? 1.2 : 1.0);
     if (us < best_t - 1e-9) {
       best_t = us;
-      best.tile = id;
-      // (a tile with K groups takes one unit per workgroup)
-      best.grid = (int)(t.kg > 1 ? most : std::min<long long>(most, cus));
+      best = {id, (int)std::min<long long>(most, cus)};
     }
   }
   return best;
 }
 
-// Tiles of every group alike, of which those without K blocks have none.
+// Along M: groups of equal size, and half a tile more for each.  (8192 x 4096 x 7168 in 8 groups
+// 162 us on 128x256, 189 on 128x128, 201 on 256x256; 64 x 4096 x 7168 in 32, the weights' stream,
+// 80 on 128x256, 86 on 128x128, 80 on 64x128, and 111 by a streaming kernel of 16 columns a
+// workgroup, as the dense GEMM has for few rows; 8 rows in 8 groups 26 on 64x128 with two K
+// groups, 34 streaming.)
+static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
+  return plan_grouped(groups, k / 128, cus, [=](const Mxfp4TileInfo& t, long long* most) {
+    const long long tiles_n = (n + t.bn - 1) / t.bn;
+    const int with_rows = std::min(m, groups);
+    *most = ((long long)m / t.bm + with_rows) * tiles_n;
+    const double tiles = std::max(1.0, (double)m / with_rows / t.bm + 0.5);
+    return std::min(*most, (long long)(with_rows * tiles * tiles_n + 0.5));
+  });
+}
+
+// Along K: every group that has rows has the same tiles.
 static GroupedPlan plan_kgroup(int m, int n, int kb, int groups, int cus) {
-  const int force = mxfp4_forced();
-  const int kb_each = std::max(1, kb / groups);
-  GroupedPlan best{-1, 0, 0};
-  double best_t = 1e30;
-  for (int id = 0; id < kMxTileCount; ++id) {
-    const Mxfp4TileInfo t = mxfp4_tile_info(id);
-    const long long units = (long long)((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * groups;
-    if (!tile_serves(t, groups, units)) continue;
-    double us = mxfp4_tile_time(id, units, kb_each, cus);
-    if (id == force) us = 0.0;
-    if (us < best_t - 1e-9) {
-      best_t = us;
-      best.tile = id;
-      best.grid = (int)(t.kg > 1 ? units : std::min<long long>(units, cus));
-    }
-  }
-  return best;
+  return plan_grouped(groups, std::max(1, kb / groups), cus, [=](const Mxfp4TileInfo& t, long long* most) {
+    return *most = (long long)((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * groups;
+  });
 }
 
 template <typename P>
@@ -201,8 +177,7 @@ int dg_m_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, con
     const GroupedPlan pl = plan_ragged(m, n, k, num_groups, dg_get_num_cus());
     const RaggedParams p = grouped_params<RaggedParams>(a, a_sf, b, b_sf, d, m, n, k, mxfp4_tile_info(pl.tile), ms, num_groups);
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const hipError_t e = pl.skinny >= 0 ? launch_mxfp4_skinny(p, pl.skinny, hs, num_groups)
-                                        : launch_mxfp4_tile(p, pl.tile, pl.grid, hs, group_table_bytes(num_groups));
+    const hipError_t e = launch_mxfp4_tile(p, pl.tile, pl.grid, hs, group_table_bytes(num_groups));
     return e == hipSuccess ? DG_OK : DG_ERR_HIP;
   } catch (...) {
     return DG_ERR_HIP;

@@ -741,9 +741,8 @@ __device__ __forceinline__ void skinny_linear_out(const Mxfp4LinearParams<GATED>
   *reinterpret_cast<uint2*>(p.d + at) = uint2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
 }
 
-// Rows [R0, R1) of A, at most 16 MT, by the B at p.b.
 template <int MT, int P, typename Params>
-__device__ __forceinline__ void skinny_rows_product(const Params& p, const uint8_t* b, const int32_t* b_sf, int R0, int R1) {
+__global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Params p) {
   constexpr MxKind KIND = Params::KIND;
   constexpr int NW = MX_SKINNY_WAVES;
   __shared__ v4f red[NW][64];
@@ -755,16 +754,16 @@ __device__ __forceinline__ void skinny_rows_product(const Params& p, const uint8
   const int KB = p.k >> 7, PAIRS = (KB + 1) >> 1;
   const int n0 = blockIdx.x * 16;   // (N % 16 == 0: every column is there)
   const v4i rsA = make_buffer_rsrc(p.a, (uint32_t)M * Kh);
-  const v4i rsB = make_buffer_rsrc(b, (uint32_t)N * Kh);
+  const v4i rsB = make_buffer_rsrc(p.b, (uint32_t)N * Kh);
   const v4i rsSA = make_buffer_rsrc(p.a_sf, (uint32_t)KB * (uint32_t)M * 4u);
-  const v4i rsSB = make_buffer_rsrc(b_sf, (uint32_t)KB * (uint32_t)N * 4u);
+  const v4i rsSB = make_buffer_rsrc(p.b_sf, (uint32_t)KB * (uint32_t)N * 4u);
   // per-lane offsets; a row past the end reads zeros (and its results are not stored)
   uint32_t a_off[MT], sa_off[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int r = R0 + i * 16 + lrow;
-    a_off[i] = r < R1 ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
-    sa_off[i] = r < R1 ? (uint32_t)r * 4u : kBufferOutOfRange;
+    const int r = i * 16 + lrow;
+    a_off[i] = r < M ? (uint32_t)r * Kh + (uint32_t)lgrp * 16u : kBufferOutOfRange;
+    sa_off[i] = r < M ? (uint32_t)r * 4u : kBufferOutOfRange;
   }
   // (gated: the gate's eight rows, and then the other half's of the same outputs)
   const int b_row = KIND == MX_GATED ? (lrow >> 3) * (N >> 1) + (n0 >> 1) + (lrow & 7) : n0 + lrow;
@@ -810,8 +809,8 @@ __device__ __forceinline__ void skinny_rows_product(const Params& p, const uint8
     if (mt > 0) __syncthreads();
     red[wave][lane] = acc[mt];
     __syncthreads();
-    const int row = R0 + mt * 16 + lrow;
-    if (wave == 0 && row < R1) {
+    const int row = mt * 16 + lrow;
+    if (wave == 0 && row < M) {
       v4f v = red[0][lane];
 #pragma unroll
       for (int w = 1; w < NW; ++w) v += red[w][lane];
@@ -820,7 +819,7 @@ __device__ __forceinline__ void skinny_rows_product(const Params& p, const uint8
         continue;
       }
       const size_t at = (size_t)row * N + n0 + 4 * lgrp;
-      if (KIND != MX_RAGGED && p.c) {
+      if (p.c) {
         const uint2 cv = *reinterpret_cast<const uint2*>(p.c + at);
         v[0] += __uint_as_float(cv.x << 16);
         v[1] += __uint_as_float(cv.x & 0xffff0000u);
@@ -867,39 +866,17 @@ static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t st
   return hipErrorInvalidValue;
 }
 
-template <int MT, int P, typename Params>
-__global__ void __launch_bounds__(MX_SKINNY_WAVES * 64) mxfp4_skinny_kernel(Params p) {
-  if constexpr (Params::KIND != MX_RAGGED) {
-    skinny_rows_product<MT, P>(p, p.b, p.b_sf, 0, p.m);
-  } else {
-    // group blockIdx.y: its rows follow those of the groups before it
-    const int g = blockIdx.y, lane = threadIdx.x & 63;
-    long long before = 0;
-    for (int h = lane; h < g; h += 64) before += max(p.ms[h], 0);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o, 64);
-    const int r0 = __builtin_amdgcn_readfirstlane((int)min(before, (long long)p.m));
-    const int r1 = __builtin_amdgcn_readfirstlane((int)min(before + max(p.ms[g], 0), (long long)p.m));
-    const uint8_t* b = p.b + (size_t)g * (size_t)p.n * (size_t)(p.k >> 1);
-    const int32_t* b_sf = p.b_sf + (size_t)g * (size_t)(p.k >> 7) * (size_t)p.n;
-    for (int r = r0; r < r1; r += 16 * MT) {
-      if (r != r0) __syncthreads();   // (the waves' sums are read)
-      skinny_rows_product<MT, P>(p, b, b_sf, r, min(r + 16 * MT, r1));
-    }
-  }
-}
-
 // id, MT, pairs in flight per wave
 #define DG_MXFP4_SKINNY(X) \
   X(0, 1, 4)               \
   X(1, 2, 4)
 
 template <typename Params>
-static hipError_t launch_mxfp4_skinny(const Params& p, int id, hipStream_t stream, int groups = 1) {
+static hipError_t launch_mxfp4_skinny(const Params& p, int id, hipStream_t stream) {
   switch (id) {
 #define X(i, MT, P)                                                                                                       \
   case i:                                                                                                                 \
-    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, P, Params>), dim3(p.n / 16, groups), dim3(MX_SKINNY_WAVES * 64), 0, stream, p); \
+    hipLaunchKernelGGL((mxfp4_skinny_kernel<MT, P, Params>), dim3(p.n / 16), dim3(MX_SKINNY_WAVES * 64), 0, stream, p); \
     return hipGetLastError();
     DG_MXFP4_SKINNY(X)
 #undef X

@@ -52,7 +52,7 @@ struct SandwichParams : NormParams {
   const uint16_t* gate;          // [ceil(m / gate_rows)][k], or null
   float* rstd_x;
   int gate_rows;
-  float scale;
+  double scale;
 };
 
 // A row is spread over a workgroup of 64 .. 1024 threads (whole waves), V vectors of 8
@@ -844,7 +844,7 @@ int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 
 int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* post_weight, const uint16_t* gate,
                      const uint16_t* weight, uint16_t* h, void* q, void* sf, int format, float* rstd_x, float* rstd,
-                     int m, int k, int gate_rows, float scale, float eps, void* stream) {
+                     int m, int k, int gate_rows, double scale, float eps, void* stream) {
   try {
     if (!residual || !h || (gate && gate_rows <= 0) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
     if (misaligned(post_weight, 16) || misaligned(gate, 16) || misaligned(rstd_x, 4)) return DG_ERR_INVALID_ARG;
@@ -906,12 +906,12 @@ size_t dg_sandwich_norm_backward_workspace_bytes(int m, int k, int with_post_wei
 int dg_sandwich_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* x, const uint16_t* h,
                               const uint16_t* post_weight, const uint16_t* gate, const uint16_t* weight,
                               const float* rstd_x, const float* rstd, uint16_t* dx, uint16_t* dresidual, float* dweight,
-                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, float scale,
+                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, double scale,
                               void* workspace, size_t workspace_bytes, void* stream) {
   try {
     if (!dy || !x || !h || !weight || !rstd || !dx || !dresidual || !dweight) return DG_ERR_INVALID_ARG;
     if (!post_weight != !dpost_weight || (post_weight && !rstd_x) || !gate != !dgate) return DG_ERR_INVALID_ARG;
-    if (m <= 0 || k <= 0 || (gate && gate_rows <= 0) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
+    if (m <= 0 || k <= 0 || (gate && gate_rows <= 0) || !std::isfinite((float)scale)) return DG_ERR_INVALID_ARG;
     if (misaligned(dy, 16) || misaligned(dh, 16) || misaligned(x, 16) || misaligned(h, 16) || misaligned(post_weight, 16) ||
         misaligned(gate, 16) || misaligned(weight, 16) || misaligned(dx, 16) || misaligned(dresidual, 16) ||
         misaligned(dweight, 16) || misaligned(dpost_weight, 16) || misaligned(dgate, 16) || misaligned(rstd_x, 4) ||
@@ -927,7 +927,7 @@ int dg_sandwich_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint
     const size_t one = (size_t)parts * k;
     const SandwichBackParams p{dy, dh, x, h, post_weight, gate, weight, rstd_x, rstd, dx, dresidual, dgate,
                                part, part + one, part + (post_weight ? 2 : 1) * one,
-                               m, k, sandwich_rows(m, k), gate ? gate_rows : m, scale};
+                               m, k, sandwich_rows(m, k), gate ? gate_rows : m, (float)scale};
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     if (launch_sandwich_backward(p, parts, hs) != hipSuccess) return DG_ERR_HIP;
     const int gates = gate ? (m - 1) / gate_rows + 1 : 0;

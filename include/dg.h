@@ -606,10 +606,10 @@ size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k);
  */
 int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* post_weight, const uint16_t* gate,
                      const uint16_t* weight, uint16_t* h, void* q, void* sf, int format, float* rstd_x, float* rstd,
-                     int m, int k, int gate_rows, float scale, float eps, void* stream);
+                     int m, int k, int gate_rows, double scale, float eps, void* stream);
 
 /*
- * Its backward pass, in fp32; the gradient passes straight through the roundings.  With
+ * Its backward pass, in fp32 (scale too); the gradient passes straight through the roundings.  With
  * n = h * r, nx = x * rx (x without post_weight), a = dy * weight, u = scale * gate * D * post_weight:
  *   D            = dh + r * (a - n * mean(a * n))             the gradient of h in full
  *   dresidual    = bf16(D)
@@ -626,13 +626,13 @@ int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t
  *   dweight [k], dpost_weight [k] (given with post_weight), dgate [ceil(m / gate_rows), k] (with
  *           gate) fp32; the outputs overlap nothing otherwise
  *   workspace: at least dg_sandwich_norm_backward_workspace_bytes(...) bytes, 16-byte aligned
- * Requirements: k % 128 == 0, k <= 16384, m <= 2^30 (else DG_ERR_UNSUPPORTED); 16-byte aligned
- *   tensors (rstd_x and rstd: 4).
+ * Requirements: k % 128 == 0, k <= 16384, m <= 2^30 (else DG_ERR_UNSUPPORTED); scale finite in fp32;
+ *   16-byte aligned tensors (rstd_x and rstd: 4).
  */
 int dg_sandwich_norm_backward(const uint16_t* dy, const uint16_t* dh, const uint16_t* x, const uint16_t* h,
                               const uint16_t* post_weight, const uint16_t* gate, const uint16_t* weight,
                               const float* rstd_x, const float* rstd, uint16_t* dx, uint16_t* dresidual, float* dweight,
-                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, float scale,
+                              float* dpost_weight, float* dgate, int m, int k, int gate_rows, double scale,
                               void* workspace, size_t workspace_bytes, void* stream);
 /* Bytes of that workspace (0 for invalid sizes); with_post_weight, with_gate: whether the call gives
  * them.  Host-only. */

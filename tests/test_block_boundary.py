@@ -44,7 +44,7 @@ def test_sandwich_norm_refusals(change, status):
     (dict(gate=0, dgate=0, gate_rows=0), OK), (dict(k=16384), OK), (dict(m=1 << 30, k=128, gate_rows=0x7fffffff), OK),
     (dict(dy=0), 1), (dict(x=0), 1), (dict(h=0), 1), (dict(weight=0), 1), (dict(rstd=0), 1), (dict(rstd_x=0), 1),
     (dict(dx=0), 1), (dict(dres=0), 1), (dict(dweight=0), 1), (dict(dpost=0), 1), (dict(post_weight=0), 1), (dict(gate=0), 1),
-    (dict(dgate=0), 1), (dict(gate_rows=0), 1), (dict(m=0), 1), (dict(k=-128), 1), (dict(scale=INF), 1),
+    (dict(dgate=0), 1), (dict(gate_rows=0), 1), (dict(m=0), 1), (dict(k=-128), 1), (dict(scale=INF), 1), (dict(scale=1e39), 1),
     (dict(dy=A + 8), 1), (dict(dh=A + 8), 1), (dict(x=A + 8), 1), (dict(h=A + 8), 1), (dict(dx=A + 8), 1),
     (dict(dres=A + 8), 1), (dict(dweight=A + 8), 1), (dict(dpost=A + 8), 1), (dict(dgate=A + 4), 1), (dict(ws=0), 1),
     (dict(ws=A + 8), 1), (dict(less=1), 1), (dict(k=200), 2), (dict(k=16384 + 128), 2), (dict(m=(1 << 30) + 1), 2),

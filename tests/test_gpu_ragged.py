@@ -67,10 +67,10 @@ def test_m_grouped_sizes(dg, sizes, tail):
     check_m(dg, a, sa, b, sb, sizes)
 
 
-@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7, 100, 101])
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7])
 def test_m_grouped_every_kernel(dg, kernel, monkeypatch):
-    """Each tile and each streaming form pinned, on all CUs and on eight (several tiles of several groups per workgroup,
-    odd and even counts of K blocks, fewer than the ring's slots too); exact integers."""
+    """Each tile pinned, on all CUs and on eight (several tiles of several groups per workgroup, odd and even counts of K
+    blocks, fewer than the ring's slots too); exact integers."""
     monkeypatch.setenv("DG_FORCE_MXFP4", str(kernel))
     for sizes in ([300, 0, 70, 1], [5, 129, 0, 0, 33, 256, 2, 64, 17]):
         for n, k, cap in ((272, 128, 0), (528, 1152, 8), (400, 2176, 8), (784, 256, 4)):
@@ -234,7 +234,7 @@ def test_training_step_of_experts(dg):
             assert np.linalg.norm(got - want) <= 0.25 * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("kernel", [0, 4, 101])
+@pytest.mark.parametrize("kernel", [0, 1, 4])
 def test_graph_replays_follow_new_sizes(dg, kernel, monkeypatch):
     """The sizes are read on the device: a captured step replayed with other sizes in the same buffer computes those."""
     monkeypatch.setenv("DG_FORCE_MXFP4", str(kernel))
@@ -252,8 +252,7 @@ def test_graph_replays_follow_new_sizes(dg, kernel, monkeypatch):
     def step():
         dg.dg_m_grouped_mxfp4_gemm_nt_ragged(*t, ms, d)
         dg.dg_quantize_mxfp4_ragged(x, ms, qt=qt, sft=sft)
-        if kernel < 100:
-            dg.dg_k_grouped_mxfp4_gemm_nt_ragged(qt, sft, qt, sft, ms, dw)
+        dg.dg_k_grouped_mxfp4_gemm_nt_ragged(qt, sft, qt, sft, ms, dw)
 
     step()
     torch.cuda.synchronize()

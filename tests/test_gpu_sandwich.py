@@ -62,7 +62,7 @@ def run(dgm, x, res, pw, gate, w, fmt, gate_rows, scale, eps=1e-6, inplace=None)
 def check(got, rstd_x, x, res, pw, gate, w, fmt, gate_rows, scale, eps=1e-6):
     m, k = x.shape
     f = [None if v is None else bf16_bits_to_f64(v) for v in (x, res, pw)]
-    h, rx = X.sandwich_norm(*f, by_row(gate, gate_rows, m), float(np.float32(scale)), eps)   # (a float argument)
+    h, rx = X.sandwich_norm(*f, by_row(gate, gate_rows, m), scale, eps)
     want = bf16_of_fp32(h)
     bad = got[2] != want
     assert not bad.any(), f"h: {bad.sum()} differ, first at {np.argwhere(bad)[0]}"
