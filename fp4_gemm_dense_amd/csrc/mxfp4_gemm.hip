@@ -60,7 +60,7 @@
 namespace dg {
 
 static const Mxfp4TileInfo kMxTiles[] = {
-#define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG, MxTile<MT, NT, WM, WN, R, KG>::LDS},
+#define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG, MxTile<MT, NT, WM, WN, R, KG>::LDS, NT < 4},
     DG_MXFP4_TILES(X)
 #undef X
 };

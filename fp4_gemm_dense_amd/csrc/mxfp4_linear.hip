@@ -13,29 +13,45 @@
 
 namespace dg {
 
-// The split tiles' partial sums in slice order, and the epilogue: a thread takes eight columns
-// of one row (for one launch over the slices of all split tiles).
-template <bool GATED>
+// The split tiles' partial sums in slice order, and the epilogue: a thread takes W outputs of one
+// row (for one launch over the slices of all split tiles).
+template <bool GATED, int W>
 __global__ void __launch_bounds__(256) linear_reduce_kernel(Mxfp4LinearParams<GATED> p, int bm, int bn, int split_tiles) {
-  const int per_row = bn / 8;
+  const int per_row = bn / (GATED ? 2 * W : W);
   const long long per_tile = (long long)bm * per_row, total = per_tile * split_tiles;
   const size_t tile = (size_t)bm * bn;
-  const LinearOut<GATED> out(p);
+  const int cols = GATED ? p.n >> 1 : p.n;
+  const LinearOut<GATED, W> out(p);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
     const int st = (int)(i / per_tile), q = (int)(i - (long long)st * per_tile);
-    const int r = q / per_row, c8 = q - r * per_row;
+    const int r = q / per_row, at = (q - r * per_row) * W;   // the first output, of the tile's
     int tm, tn;
     raster_tile(p.full_tiles + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
-    const int row = tm * bm + r, col = tn * bn + c8 * 8;
-    const v4f* w = reinterpret_cast<const v4f*>(p.ws + (size_t)st * p.splits * tile + (size_t)r * bn + c8 * 8);
-    v4f lo = w[0], hi = w[1];
-    for (int s = 1; s < p.splits; ++s) {
-      w += tile / 4;
-      lo += w[0];
-      hi += w[1];
+    // the tile's column of the first result, and of the other half's
+    const int c = !GATED ? at : W == 8 ? (at >> 5) * 64 + (at & 31) : at * 2;
+    const int row = tm * bm + r, col = GATED ? gated_output<W>(tn * bn + c) : tn * bn + c;
+    const bool ok = row < p.m && col < cols;
+    const auto cv = out.load_c(out.place(row, col, ok));
+    auto sum = [&](int c, int bias_col, float (&v)[W]) {
+      const float* w = p.ws + (size_t)st * p.splits * tile + (size_t)r * bn + c;
+#pragma unroll
+      for (int e = 0; e < W; e += 4) {
+        v4f t = *reinterpret_cast<const v4f*>(w + e);
+        for (int s = 1; s < p.splits; ++s) t += *reinterpret_cast<const v4f*>(w + s * tile + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[e + j] = t[j];
+      }
+      if (p.bias && ok) add_bf16(v, reinterpret_cast<const int*>(p.bias + bias_col));
+    };
+    float u[W], up[W];
+    sum(c, col, u);
+    if constexpr (GATED) {
+      sum(c + (W == 8 ? 32 : 4), cols + col, up);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) up[e] = 0.f;
     }
-    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    out(row, col, row < p.m && col < p.n, v);
+    out(row, col, ok, u, up, cv);
   }
 }
 
@@ -60,7 +76,13 @@ static hipError_t launch_linear(const Mxfp4LinearParams<GATED>& p, const Mxfp4Pl
   const Mxfp4TileInfo t = mxfp4_tile_info(pl.tile);
   const int split_tiles = pl.tiles_m * pl.tiles_n - pl.full_tiles;
   const int grid = (int)std::min<long long>(((long long)split_tiles * t.bm * (t.bn / 8) + 255) / 256, (long long)cus * 8);
-  hipLaunchKernelGGL(linear_reduce_kernel<GATED>, dim3(grid), dim3(256), 0, hs, p, t.bm, t.bn, split_tiles);
+  if constexpr (GATED) {
+    if (t.narrow) {
+      hipLaunchKernelGGL((linear_reduce_kernel<GATED, 4>), dim3(grid), dim3(256), 0, hs, p, t.bm, t.bn, split_tiles);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((linear_reduce_kernel<GATED, 8>), dim3(grid), dim3(256), 0, hs, p, t.bm, t.bn, split_tiles);
   return hipGetLastError();
 }
 

@@ -83,6 +83,11 @@ struct MxTile {
   // with two).
   static constexpr bool ONE = MT * NT == 32;
   static constexpr int LDS = KG * RING + (ONE ? 1024 : 0);   // and 1 KB that is written and not read
+  // a linear layer's bias: BN values of R + 2 units behind that (with K groups: of one), in whole
+  // copies of 128
+  static constexpr int BIAS_COPIES = (BN + 127) / 128, BIAS_UNIT = BIAS_COPIES * 256;
+  static constexpr int BIAS = (KG > 1 ? 1 : R + 2) * BIAS_UNIT;
+  static_assert(LDS + BIAS <= 160 * 1024, "LDS");
   static_assert(NSA + NSB <= NW, "one scale copy per wave (some waves repeat another's)");
   static_assert(RA >= 1 && RB >= 1 && NT % 2 == 0 && LDS <= 160 * 1024 && NSTORE % KG == 0 && (KG == 1 || KG * BM * BN * 4 <= LDS),
                 "tile shape");
@@ -117,74 +122,80 @@ __device__ __forceinline__ void wait_vmcnt_first(int first) {
       "s_waitcnt vmcnt(%2)" ::"s"(first), "n"(LESS), "n"(MORE) : "memory", "scc");
 }
 
-// Columns of a gated product: the 32 neighbouring ones of a tile are 16 of the gate's and the
-// 16 of the same outputs' of the other half, four by four, so that a lane's eight results are
-// four outputs' pairs.  Tile column c (from the product's first) -> the output's column of a
-// group of four (c % 8 == 0), and B's row of any c.
-__device__ __forceinline__ int gated_column(int c) { return (c >> 5) * 16 + ((c >> 3) & 3) * 4; }
-__device__ __forceinline__ int gated_row(int c, int half) {
-  return ((c >> 2) & 1) * half + (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
+// Columns of a gated product, so that one lane has the gate's and the other half's results of
+// the same outputs.  W = 8 (waves of 64 columns or more): 32 gate columns of a tile and then the
+// 32 of the same outputs' other half, eight a lane in each; W = 4: of 32 tile columns 16 gate
+// columns and 16 of the other half, four by four.  Tile column c (from the product's first) ->
+// its output, and whether it is the gate's (0) or the other half's (1).
+template <int W>
+__device__ __forceinline__ int gated_output(int c) {
+  return W == 8 ? (c >> 6) * 32 + (c & 31) : (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
+}
+template <int W>
+__device__ __forceinline__ int gated_half(int c) {
+  return W == 8 ? (c >> 5) & 1 : (c >> 2) & 1;
 }
 
-// Eight neighbouring columns of a linear layer's product, from column `col` (a multiple of 8)
-// of row `row`, on to d and z.  Every lane takes part; ok: the place lies within the product.
-template <bool GATED>
+template <int N>
+__device__ __forceinline__ void add_bf16(float (&v)[N], const int* w) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    v[e] += __uint_as_float((uint32_t)w[e >> 1] << 16);
+    v[e + 1] += __uint_as_float((uint32_t)w[e >> 1] & 0xffff0000u);
+  }
+}
+
+// W neighbouring outputs of a linear layer from column `out` of row `row`, on to d and z: u is the
+// product with the bias (gated: the gate's, and up the other half's), c the residual as load_c
+// gave it.  Every lane takes part; ok: the place lies within d.
+template <bool GATED, int W>
 struct LinearOut {
-  v4i rsD, rsC, rsZ, rsBias;
+  static_assert(W == 8 || (GATED && W == 4), "outputs a lane");
+  typedef int Vec __attribute__((ext_vector_type(W / 2)));
+  v4i rsD, rsC, rsZ;
   Activation act;
-  int n, has_c, has_z, has_bias;
-  __device__ __forceinline__ LinearOut(const Mxfp4LinearParams<GATED>& p)
-      : act(p.act), n(p.n), has_c(p.c != nullptr), has_z(p.z != nullptr), has_bias(p.bias != nullptr) {
+  int n, has_z;
+  __device__ __forceinline__ LinearOut(const Mxfp4LinearParams<GATED>& p) : act(p.act), n(p.n), has_z(p.z != nullptr) {
     const uint32_t bytes = (uint32_t)p.m * (uint32_t)(GATED ? p.n >> 1 : p.n) * 2u;
     rsD = make_buffer_rsrc(p.d, bytes);
-    rsC = make_buffer_rsrc(p.c, p.c ? bytes : 0u);
+    rsC = make_buffer_rsrc(p.c, p.c ? bytes : 0u);   // (none: reads zeros, and no memory)
     rsZ = make_buffer_rsrc(p.z, p.z ? (uint32_t)p.m * (uint32_t)p.n * 2u : 0u);
-    rsBias = make_buffer_rsrc(p.bias, p.bias ? (uint32_t)p.n * 2u : 0u);
   }
-  static __device__ __forceinline__ void add4(float (&v)[8], int at, v2i w) {
-    v[at] += __uint_as_float((uint32_t)w.x << 16);
-    v[at + 1] += __uint_as_float((uint32_t)w.x & 0xffff0000u);
-    v[at + 2] += __uint_as_float((uint32_t)w.y << 16);
-    v[at + 3] += __uint_as_float((uint32_t)w.y & 0xffff0000u);
-  }
-  static __device__ __forceinline__ v2i pack4(const float (&v)[8], int at) {
-    return v2i{(int)pack_bf16x2_rne(v[at], v[at + 1]), (int)pack_bf16x2_rne(v[at + 2], v[at + 3])};
-  }
-  __device__ __forceinline__ void operator()(int row, int col, bool ok, float (&v)[8]) const {
-    if constexpr (GATED) {
-      const int half = n >> 1, out = gated_column(col);
-      const uint32_t oz = ok ? ((uint32_t)row * (uint32_t)n + (uint32_t)out) * 2u : kBufferOutOfRange;
-      const uint32_t od = ok ? ((uint32_t)row * (uint32_t)half + (uint32_t)out) * 2u : kBufferOutOfRange;
-      if (has_bias) {
-        const int ob = ok ? out * 2 : (int)kBufferOutOfRange;
-        add4(v, 0, dg_raw_buffer_load_v2i32(rsBias, ob, 0, 0));
-        add4(v, 4, dg_raw_buffer_load_v2i32(rsBias, ob, half * 2, 0));
-      }
-      if (has_z) {
-        dg_raw_buffer_store_v2i32(pack4(v, 0), rsZ, (int)oz, 0, 0);
-        dg_raw_buffer_store_v2i32(pack4(v, 4), rsZ, (int)oz, half * 2, 0);
-      }
-      activate<4>(v, act);
+  static __device__ __forceinline__ Vec pack(const float (&v)[W]) {
+    Vec r;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= v[4 + e];
-      if (has_c) add4(v, 0, dg_raw_buffer_load_v2i32(rsC, (int)od, 0, 0));
-      dg_raw_buffer_store_v2i32(pack4(v, 0), rsD, (int)od, 0, 0);
-    } else {
-      const uint32_t o = ok ? ((uint32_t)row * (uint32_t)n + (uint32_t)col) * 2u : kBufferOutOfRange;
-      auto add8 = [&](const v4i& w) {
-        add4(v, 0, v2i{w.x, w.y});
-        add4(v, 4, v2i{w.z, w.w});
-      };
-      auto pack8 = [&]() {
-        const v2i a = pack4(v, 0), b = pack4(v, 4);
-        return v4i{a.x, a.y, b.x, b.y};
-      };
-      if (has_bias) add8(dg_raw_buffer_load_v4i32(rsBias, ok ? col * 2 : (int)kBufferOutOfRange, 0, 0));
-      if (has_z) dg_raw_buffer_store_v4i32(pack8(), rsZ, (int)o, 0, 0);
-      activate<8>(v, act);
-      if (has_c) add8(dg_raw_buffer_load_v4i32(rsC, (int)o, 0, 0));
-      dg_raw_buffer_store_v4i32(pack8(), rsD, (int)o, 0, 0);
+    for (int e = 0; e < W; e += 2) r[e >> 1] = (int)pack_bf16x2_rne(v[e], v[e + 1]);
+    return r;
+  }
+  static __device__ __forceinline__ void store(const Vec& v, const v4i& rs, uint32_t off, int soff) {
+    // (whole 16 bytes non-temporal: 4096 x 24576 x 1536 130 -> 121 us; with 8 they cost more
+    // than they gain)
+    if constexpr (W == 8) dg_raw_buffer_store_v4i32(v, rs, (int)off, soff, kStoreNonTemporal);
+    else dg_raw_buffer_store_v2i32(v, rs, (int)off, soff, 0);
+  }
+  __device__ __forceinline__ uint32_t place(int row, int out, bool ok) const {
+    return ok ? ((uint32_t)row * (uint32_t)(GATED ? n >> 1 : n) + (uint32_t)out) * 2u : kBufferOutOfRange;
+  }
+  __device__ __forceinline__ Vec load_c(uint32_t place) const {
+    if constexpr (W == 8) return dg_raw_buffer_load_v4i32(rsC, (int)place, 0, 0);
+    else return dg_raw_buffer_load_v2i32(rsC, (int)place, 0, 0);
+  }
+  __device__ __forceinline__ void operator()(int row, int out, bool ok, float (&u)[W], const float (&up)[W], const Vec& c) const {
+    if (has_z) {
+      const uint32_t oz = ok ? ((uint32_t)row * (uint32_t)n + (uint32_t)out) * 2u : kBufferOutOfRange;
+      store(pack(u), rsZ, oz, 0);
+      if constexpr (GATED) store(pack(up), rsZ, oz, n);   // (n / 2 columns on)
     }
+    activate<W>(u, act);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) u[e] *= up[e];
+    }
+    int w[W / 2];
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) w[e] = c[e];
+    add_bf16(u, w);
+    store(pack(u), rsD, place(row, out, ok), 0);
   }
 };
 
@@ -236,6 +247,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
   constexpr int MT = T::MT, NT = T::NT, R = T::R;
   constexpr MxKind KIND = P::KIND;
   constexpr bool GROUPED = KIND == MX_RAGGED || KIND == MX_KGROUP;
+  constexpr bool LINEAR = KIND == MX_LINEAR || KIND == MX_GATED;
+  constexpr int W = KIND == MX_GATED && NT % 4 != 0 ? 4 : 8;   // outputs a lane has side by side
   extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -345,16 +358,35 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
   v4i rsS = make_buffer_rsrc(sc_b ? p.b_sf : p.a_sf, (uint32_t)KB * (uint32_t)(sc_b ? N : M) * 4u);
   const uint32_t s_stride = (uint32_t)(sc_b ? N : M) * 4u;   // bytes of one K block's words
   const uint32_t s_dst = sc_b ? T::OFF_SB + (sc - T::NSA) * 1024 : T::OFF_SA + sc * 1024;
+  // B's row of a gated product's column (N: none)
+  auto gated_row = [&](int c) -> int {
+    const int out = gated_output<W>(c), half = N >> 1;
+    return out < half ? gated_half<W>(c) * half + out : N;
+  };
   auto scale_offset = [&](int ln, int m0, int n0, bool odd_end) -> uint32_t {
     const int bt = sc_b ? T::BN : T::BM, rows = sc_b ? N : M, r0 = sc_b ? n0 : m0;
     const int q = (sc_b ? sc - T::NSA : sc) * 256 + ln * 4, half = q / bt;
     int row = r0 + q % bt;
-    if (KIND == MX_GATED && sc_b) row = row < N ? gated_row(row, N >> 1) : N;   // (four rows side by side)
+    if (KIND == MX_GATED && sc_b) row = gated_row(row);   // (four rows side by side)
     // (rows past the end, lanes past the two K blocks, a second K block past the end)
     return row < rows && half < (odd_end ? 1 : 2) ? (uint32_t)half * s_stride + (uint32_t)row * 4u : kBufferOutOfRange;
   };
   int c_m0 = 0, c_n0 = 0;
+  // The bias of a unit's columns, in their order: a copy ahead of the unit's first stage, so that
+  // it has landed with that (and the waits, which do not count it, only wait for more).  The
+  // cursor is at most R units ahead of the slowest wave's unit, and one more at its barrier.
+  uint32_t bias_w = 0, bias_r = 0;   // the places of the cursor's unit, and of the present one
+  auto next_bias = [&](uint32_t at) { return at + T::BIAS_UNIT == T::BIAS ? 0u : at + T::BIAS_UNIT; };
   auto cursor_to = [&](const Unit& w) {
+    if constexpr (LINEAR) {
+      if (p.bias && wave_all < T::BIAS_COPIES) {
+        const int c = w.n0 + wave_all * 128 + 2 * lane_here();
+        const int col = KIND == MX_GATED ? gated_row(c) : c;
+        buf4_to_lds(make_buffer_rsrc(p.bias, (uint32_t)N * 2u), col < N ? (uint32_t)col * 2u : kBufferOutOfRange, 0u,
+                    smem_all + T::LDS + bias_w + wave_all * 256);
+      }
+      bias_w = next_bias(bias_w);
+    }
     c_m0 = w.m0;
     c_n0 = w.n0;
     c_kb = w.kb0 + 2 * grp;
@@ -368,7 +400,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
     for (int j = 0; j < T::RB; ++j) {
       const int row = w.n0 + (wave * T::RB + j) * 8 + (ln >> 3);
       if constexpr (KIND == MX_GATED)
-        off[T::RA + j] = row < N ? (uint32_t)gated_row(row, N >> 1) * Kh + chunk_b(ln, j) : kBufferOutOfRange;
+        off[T::RA + j] = (uint32_t)gated_row(row) * Kh + chunk_b(ln, j);
       else
         off[T::RA + j] = (uint32_t)row * Kh + chunk_b(ln, j);
     }
@@ -557,7 +589,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
       if constexpr (nt == T::BAR - 1) {
         __builtin_amdgcn_sched_barrier(0);
         wait_lgkmcnt0();
-        constexpr int more = (R - 2) * T::LPS, stores = T::KG == 1 ? T::NSTORE : 0;
+        // (a gated lane's eight outputs come of two such pairs of column blocks)
+        constexpr int more = (R - 2) * T::LPS, stores = T::KG > 1 ? 0 : KIND == MX_GATED && W == 8 ? T::NSTORE / 2 : T::NSTORE;
         if constexpr (T::ONE) wait_vmcnt_first<more, more + T::LATE + stores>(first);
         else wait_vmcnt<more + (FIRST ? stores : 0)>();
         block_barrier();
@@ -613,7 +646,10 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
     __builtin_amdgcn_sched_barrier(0);
 
     // the pairs of column blocks (mt, np) that this group stores: every KG-th share of them
-    auto mine = [&](int mt, int np) { return T::KG == 1 || (mt * (NT / 2) + np) / (T::NSTORE / T::KG) == grp; };
+    auto mine = [&](int mt, int np) {
+      if (KIND == MX_GATED && W == 8) return T::KG == 1 || (mt * (NT / 4) + np / 2) % T::KG == grp;
+      return T::KG == 1 || (mt * (NT / 2) + np) / (T::NSTORE / T::KG) == grp;
+    };
     if constexpr (T::KG > 1) {
       // the groups' sums meet: each hands the others' pairs over in LDS, and adds theirs to
       // its own in order (one unit per workgroup: the rings are done with)
@@ -639,6 +675,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
         }
     }
     const int ln = T::ONE ? lane_here() : lane;
+    if (LINEAR && cur.part >= 0) bias_r = next_bias(bias_r);
     if (cur.part >= 0) {
       // fp32 partial tile of this slice: ws[part][BM][BN]
       const v4i rsW = make_buffer_rsrc(p.ws + (size_t)cur.part * (T::BM * T::BN), (uint32_t)(T::BM * T::BN * 4));
@@ -652,20 +689,58 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
                          __float_as_int(acc[mt][nt][2]), __float_as_int(acc[mt][nt][3])};
           dg_raw_buffer_store_v4i32(w, rsW, at, (mt * 16 * T::BN + (nt >> 1) * 32 + (nt & 1) * 4) * 4, 0);
         }
-    } else if constexpr (KIND == MX_LINEAR || KIND == MX_GATED) {
-      const LinearOut<KIND == MX_GATED> out(p);
+    } else if constexpr (LINEAR) {
+      const LinearOut<KIND == MX_GATED, W> out(p);
+      using Vec = typename LinearOut<KIND == MX_GATED, W>::Vec;
+      // items of a lane's W outputs, their residual read PRE items ahead (a load behind a store is
+      // waited for with it; the 256x256 tile has registers for four)
+      constexpr int ITEMS = KIND == MX_GATED && W == 8 ? NT / 4 : NT / 2, STEP = NT / 2 / ITEMS;
+      const int c0 = wave_n * NT * 16 + (ln >> 4) * 8;   // the tile's column of item 0
+      auto column = [&](int i) { return KIND == MX_GATED ? gated_output<W>(cur.n0 + c0 + i * STEP * 32) : cur.n0 + c0 + i * 32; };
+      auto row_of = [&](int mt) { return cur.m0 + wave_m * MT * 16 + mt * 16 + (ln & 15); };
+      const int cols = KIND == MX_GATED ? N >> 1 : N;
+      constexpr int ALL = MT * ITEMS, PRE = ALL < 4 ? ALL : 4;
+      Vec cv[PRE];
+      auto read_c = [&](auto item_tag) {
+        constexpr int mt = decltype(item_tag)::value / ITEMS, i = decltype(item_tag)::value % ITEMS;
+        if (mine(mt, i * STEP))
+          cv[decltype(item_tag)::value % PRE] = out.load_c(out.place(row_of(mt), column(i), row_of(mt) < M && column(i) < cols));
+      };
+      static_for<PRE>([&](auto f) { read_c(f); });
+      const uint8_t* const bias = smem_all + T::LDS + bias_r + c0 * 2;
+      static_for<ALL>([&](auto item_tag) {
+        constexpr int f = decltype(item_tag)::value, mt = f / ITEMS, i = f % ITEMS;
+        const int row = row_of(mt);
+        if (mine(mt, i * STEP)) {
+          auto product = [&](int np) {
+            struct { float v[8]; } r;
+            const v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int row = cur.m0 + wave_m * MT * 16 + mt * 16 + (ln & 15);
+            for (int e = 0; e < 4; ++e) {
+              r.v[e] = lo[e];
+              r.v[4 + e] = hi[e];
+            }
+            if (p.bias) {   // (uniform)
+              const v4i b = *reinterpret_cast<const v4i*>(bias + np * 64);
+              const int w[4] = {b.x, b.y, b.z, b.w};
+              add_bf16(r.v, w);
+            }
+            return r;
+          };
+          auto first = product(i * STEP);
+          float u[W], up[W];
 #pragma unroll
-        for (int np = 0; np < NT / 2; ++np) {
-          if (!mine(mt, np)) continue;
-          const int col = cur.n0 + wave_n * NT * 16 + np * 32 + (ln >> 4) * 8;
-          const v4f lo = acc[mt][2 * np], hi = acc[mt][2 * np + 1];
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          out(row, col, row < M && col < N, v);
+          for (int e = 0; e < W; ++e) u[e] = up[e] = first.v[e];
+          if constexpr (KIND == MX_GATED) {
+            const auto other = STEP == 2 ? product(i * STEP + 1) : first;
+#pragma unroll
+            for (int e = 0; e < W; ++e) up[e] = other.v[W == 8 ? e : 4 + e];
+          }
+          out(row, column(i), row < M && column(i) < cols, u, up, cv[f % PRE]);
         }
-      }
+        if constexpr (f + PRE < ALL) read_c(std::integral_constant<int, f + PRE>{});
+      });
+      bias_r = next_bias(bias_r);
     } else {
       const v4i rsD = make_buffer_rsrc(p.d + (KIND == MX_KGROUP ? (size_t)cur.g * M * N : 0), (uint32_t)M * (uint32_t)N * 2u);
       const v4i rsC = make_buffer_rsrc(p.c, p.c ? (uint32_t)M * (uint32_t)N * 2u : 0u);
@@ -855,9 +930,11 @@ static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t st
     using T = MxTile<MT, NT, WM, WN, R, KG>;                                                                      \
     static const hipError_t attr =                                                                                \
         hipFuncSetAttribute(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T, P>),                              \
-                            hipFuncAttributeMaxDynamicSharedMemorySize, P::KIND >= MX_RAGGED ? kLdsBytes : T::LDS);   \
+                            hipFuncAttributeMaxDynamicSharedMemorySize,                                           \
+                            P::KIND >= MX_RAGGED ? kLdsBytes : P::KIND == MX_DENSE ? T::LDS : T::LDS + T::BIAS);  \
     if (attr != hipSuccess) return attr;                                                                          \
-    hipLaunchKernelGGL((mxfp4_tile_kernel<T, P>), dim3(grid), dim3(T::THREADS), T::LDS + table_bytes, stream, p); \
+    const size_t lds = T::LDS + (P::KIND == MX_LINEAR || P::KIND == MX_GATED ? T::BIAS : table_bytes);           \
+    hipLaunchKernelGGL((mxfp4_tile_kernel<T, P>), dim3(grid), dim3(T::THREADS), lds, stream, p);                  \
     return hipGetLastError();                                                                                     \
   }
     DG_MXFP4_TILES(X)
@@ -894,6 +971,7 @@ bool mxfp4_sizes_fit(int m, int n, int k);
 void log_mxfp4_plan(const char* call, int m, int n, int k, const Mxfp4Plan& pl);   // (with DG_LOG=1)
 struct Mxfp4TileInfo {
   int bm, bn, kg, lds;
+  bool narrow;   // its waves have fewer than 64 columns
 };
 Mxfp4TileInfo mxfp4_tile_info(int id);
 constexpr int kMxTileCount = 8, kMxSkinnyIdBase = 100;
