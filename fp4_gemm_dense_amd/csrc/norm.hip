@@ -24,7 +24,6 @@
 // (floors 6.5 and 13: at most 1024 workgroups walk the rows), 130 x 2048 3.9.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "../../include/dg.h"
 #include "dg_internal.hpp"
@@ -34,6 +33,7 @@
 namespace dg {
 
 struct NormParams {
+  static constexpr bool BLOCK = false;
   const uint16_t* x;
   const uint16_t* residual;
   const uint16_t* weight;
@@ -48,6 +48,7 @@ struct NormParams {
 
 // The norms around a block: x is the block's output.
 struct SandwichParams : NormParams {
+  static constexpr bool BLOCK = true;
   const uint16_t* post_weight;   // or null: the branch is not normed
   const uint16_t* gate;          // [ceil(m / gate_rows)][k], or null
   float* rstd_x;
@@ -95,6 +96,19 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
   F s = 0;
   for (int w = 0; w < waves; ++w) s += red[w];
   return s;
+}
+
+// 1 / sqrt(v), v > 0 within fp64's normal range (infinity: 0): the hardware's estimate, good to some
+// 2^-26, and two Newton steps, whose rounding leaves 2^-51.  (sqrt and a division are three times as
+// long a chain.)
+__device__ __forceinline__ double rsqrt64(double v) {
+  double y = __builtin_amdgcn_rsq(v);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double e = fma(-v * y, y, 1.0);
+    y = fma(0.5 * y, e, y);
+  }
+  return v < __builtin_inf() ? y : v == v ? 0.0 : v;
 }
 
 // Bounds of max |h * weight|, 2^-100 .. 2^100.  From the lower one on the products of a
@@ -196,7 +210,7 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
     }
-    const double r = 1.0 / sqrt(block_sum(ss, red) * p.inv_k + (double)p.eps);
+    const double r = rsqrt64(block_sum(ss, red) * p.inv_k + (double)p.eps);
     if (p.rstd_x && tid == 0) p.rstd_x[row] = (float)r;
     c *= r;
   }
@@ -207,13 +221,13 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
     unpack_bf16x8(pv[i], w);
     unpack_bf16x8(gv[i], g);
     unpack_bf16x8(rv[i], r);
-    uint32_t pmax = 0;
+    float size = 0.f;   // (their sum says as much as their largest, and shows a NaN)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       prod[e] = x[e] * w[e] * g[e];
-      pmax = umax(pmax, abs_bits(prod[e]));
+      size += fabsf(prod[e]);
     }
-    if (__builtin_expect((pmax - kExactLo < kExactHi - kExactLo) | (i * nt + tid >= nv), 1)) {
+    if (__builtin_expect(((size >= 0x1p-97f) & (size < 0x1p100f)) | (i * nt + tid >= nv), 1)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[e] = (float)fma((double)prod[e], c, (double)r[e]);
     } else {
@@ -230,7 +244,7 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 // in every format, 70-75 us against 73-84.)
 template <int FMT, int V, typename P>
 __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) {
-  constexpr bool BLOCK = std::is_same_v<P, SandwichParams>;
+  constexpr bool BLOCK = P::BLOCK;
   __shared__ double red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3, kb_n = p.k >> 7;
@@ -244,10 +258,16 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) 
     if (j < nv) {
       hv[i] = reinterpret_cast<const v4i*>(p.x)[base + j];
       if (p.residual) rv[i] = reinterpret_cast<const v4i*>(p.residual)[base + j];
-      wv[i] = reinterpret_cast<const v4i*>(p.weight)[j];
+      if (!BLOCK) wv[i] = reinterpret_cast<const v4i*>(p.weight)[j];
     }
   }
-  if constexpr (BLOCK) block_output<V>(p, row, hv, rv);
+  if constexpr (BLOCK) {
+    block_output<V>(p, row, hv, rv);
+    // (read during the sum that follows: for three rows on a CU there are no registers before)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i * nt + tid < nv) wv[i] = reinterpret_cast<const v4i*>(p.weight)[i * nt + tid];
+  }
   double ss = 0;   // (the squares of bf16 numbers are exact in fp64, and its range holds them)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -268,7 +288,8 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) 
   }
   // the sum and r in 64 bits: a code near a border follows y = (h * weight) * r, whose first
   // product is exact (two bf16 values)
-  const double r64 = 1.0 / sqrt(block_sum(ss, red) * p.inv_k + (double)p.eps);
+  const double mean = block_sum(ss, red) * p.inv_k + (double)p.eps;
+  const double r64 = BLOCK ? rsqrt64(mean) : 1.0 / sqrt(mean);
   const float r = (float)r64;
   const TwoFloats r2 = {r, (float)(r64 - (double)r)};
   // the products that the two numbers serve (none where r is one number, or subnormal)
@@ -568,9 +589,11 @@ struct SandwichBackParams {
 // both gradients behind it: dgate = scale * post_weight * S, and dpost_weight adds up scale *
 // gate * S.  A gate's sum that lies in one workgroup is final; the first and the last gate of
 // a workgroup may go on in its neighbours, and leave as its partial rows 0 and 1 (0 where
-// the two are one).
-template <int V, bool AHEAD>
+// the two are one).  Rows of up to 8192 read the next row's dy and h ahead and keep the weights;
+// longer ones have no registers for either.
+template <int V>
 __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBackParams p) {
+  constexpr bool AHEAD = V <= 2, KEEP = V <= 2;
   __shared__ float red[2][2][NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3;
@@ -588,18 +611,28 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
     o[1] = v4f{v[4], v[5], v[6], v[7]};
   };
   float dw[V][8], dpw[V][8], sum[V][8];
-  v4i wv[V], pv[V], gv[V], dyn[V], hn[V];
+  v4i dyn[V], hn[V], wk[KEEP ? V : 1], pk[KEEP ? V : 1], gk[KEEP ? V : 1];
+  int gate = -1;
+  // the weights and the present gate: kept in registers, or read where they are used
+  auto read_weight = [&](int i) { return at(p.weight, 0, i); };
+  auto read_post = [&](int i) { return p.post_weight ? at(p.post_weight, 0, i) : one; };
+  auto read_gate = [&](int i) { return p.gate ? at(p.gate, gate, i) : one; };
+  auto weight_of = [&](int i) { return KEEP ? wk[KEEP ? i : 0] : read_weight(i); };
+  auto post_of = [&](int i) { return KEEP ? pk[KEEP ? i : 0] : read_post(i); };
+  auto gate_of = [&](int i) { return KEEP ? gk[KEEP ? i : 0] : read_gate(i); };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    wv[i] = at(p.weight, 0, i);
-    pv[i] = p.post_weight ? at(p.post_weight, 0, i) : one;
-    gv[i] = one;
+    if constexpr (KEEP) {
+      wk[i] = read_weight(i);
+      pk[i] = read_post(i);
+      gk[i] = one;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = dpw[i][e] = sum[i][e] = 0.f;
   }
   const int row0 = blockIdx.x * p.rows, row1 = min(p.m, row0 + p.rows);
   const int first_gate = row0 / p.gate_rows;
-  int gate = -1, gate_end = row0, turn = 0;
+  int gate_end = row0, turn = 0;
   float rn = 0.f;
   auto load_next = [&](int r) {
     rn = p.rstd[r];
@@ -617,8 +650,8 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float g[8], w[8], o[8];
-      unpack_bf16x8(gv[i], g);
-      unpack_bf16x8(pv[i], w);
+      unpack_bf16x8(gate_of(i), g);
+      unpack_bf16x8(post_of(i), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float t = p.scale * sum[i][e];
@@ -635,9 +668,9 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
       if (gate >= 0) end_gate();
       gate = row / p.gate_rows;
       gate_end = (int)min((long long)p.m, (long long)(gate + 1) * p.gate_rows);
-      if (p.gate) {
+      if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) gv[i] = at(p.gate, gate, i);
+        for (int i = 0; i < V; ++i) gk[i] = read_gate(i);
       }
     }
     v4i dyc[V], hc[V], dhc[V], xc[V];
@@ -656,7 +689,7 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
       float a[8], n[8], w[8];
       unpack_bf16x8(dyc[i], a);
       unpack_bf16x8(hc[i], n);
-      unpack_bf16x8(wv[i], w);
+      unpack_bf16x8(weight_of(i), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         n[e] *= r;
@@ -674,11 +707,11 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
       float a[8], n[8], w[8], d[8], x[8], g[8], pw[8];
       unpack_bf16x8(dyc[i], a);
       unpack_bf16x8(hc[i], n);
-      unpack_bf16x8(wv[i], w);
+      unpack_bf16x8(weight_of(i), w);
       unpack_bf16x8(dhc[i], d);
       unpack_bf16x8(xc[i], x);
-      unpack_bf16x8(gv[i], g);
-      unpack_bf16x8(pv[i], pw);
+      unpack_bf16x8(gate_of(i), g);
+      unpack_bf16x8(post_of(i), pw);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[e] += r * (a[e] * w[e] - n[e] * r * mean);
@@ -780,9 +813,9 @@ static bool sandwich_backward_fits(int m, int k) { return k % 128 == 0 && k <= S
 
 static hipError_t launch_sandwich_backward(const SandwichBackParams& p, int grid, hipStream_t hs) {
   const NormShape s = norm_shape(p.k);
-  if (s.v == 1) hipLaunchKernelGGL((sandwich_norm_backward_kernel<1, true>), dim3(grid), dim3(s.threads), 0, hs, p);
-  else if (s.v == 2) hipLaunchKernelGGL((sandwich_norm_backward_kernel<2, true>), dim3(grid), dim3(s.threads), 0, hs, p);
-  else hipLaunchKernelGGL((sandwich_norm_backward_kernel<4, false>), dim3(grid), dim3(s.threads), 0, hs, p);
+  if (s.v == 1) hipLaunchKernelGGL((sandwich_norm_backward_kernel<1>), dim3(grid), dim3(s.threads), 0, hs, p);
+  else if (s.v == 2) hipLaunchKernelGGL((sandwich_norm_backward_kernel<2>), dim3(grid), dim3(s.threads), 0, hs, p);
+  else hipLaunchKernelGGL((sandwich_norm_backward_kernel<4>), dim3(grid), dim3(s.threads), 0, hs, p);
   return hipGetLastError();
 }
 
