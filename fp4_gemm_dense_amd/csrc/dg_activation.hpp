@@ -72,16 +72,16 @@ __device__ __forceinline__ void activate(float (&v)[M], const Activation& a) {
   }
 }
 
-// act(u) and its derivative (ReLU's at 0: 0).
-template <int N>
+// act(u) and its derivative (ReLU's at 0: 0), of kind KIND.
+template <int KIND, int N>
 __device__ __forceinline__ void activate_both(const float (&u)[N], float (&y)[N], float (&dy)[N], const Activation& a) {
-  if (a.kind == ACT_KIND_CLAMP) {
+  if constexpr (KIND == ACT_KIND_CLAMP) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       y[e] = u[e] < a.lo ? a.lo : u[e];
       dy[e] = u[e] > a.lo || a.lo < 0.f ? 1.f : 0.f;   // (ReLU of a NaN: 0)
     }
-  } else if (a.kind == ACT_KIND_SIGMOID) {
+  } else if constexpr (KIND == ACT_KIND_SIGMOID) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const float s = act_sigmoid(u[e], a), x = __builtin_amdgcn_fmed3f(u[e], -128.f, 128.f);

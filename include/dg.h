@@ -521,9 +521,9 @@ int dg_mxfp4_linear(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, con
  *        dx = q . (w quantised along n)^T and dw = qt . (x quantised along m)^T, two dg_mxfp4_gemm_nt
  *   dbias [n] fp32, the sums over the rows of dz before it is rounded, in a fixed order; or NULL
  *   workspace  with dbias, dg_activation_backward_workspace_bytes(m, n) bytes, 16-byte aligned; may
- *        be NULL when that is 0 (up to 128 rows)
- * At least one output is given.  Requirements: m, n > 0; n % 128 == 0 (gated: n % 256 == 0) and m + 127
- *   at most 2^31 - 1 (else DG_ERR_UNSUPPORTED).  Outputs overlap nothing but as said.
+ *        be NULL when that is 0 (few rows)
+ * At least one output is given.  Requirements: m, n > 0; n % 128 == 0 (gated: n % 256 == 0), n below 2^23
+ *   and m + 127 at most 2^31 - 1 (else DG_ERR_UNSUPPORTED).  Outputs overlap nothing but as said.
  */
 int dg_activation_backward(const uint16_t* dy, const uint16_t* z, int activation, uint16_t* dz, uint8_t* q, int32_t* sf,
                            uint8_t* qt, int32_t* sft, float* dbias, int m, int n, void* workspace, size_t workspace_bytes,

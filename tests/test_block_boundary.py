@@ -135,7 +135,7 @@ def test_linear_refusals(change, status):
     (dict(m=300), 1), (dict(m=300, ws=A + 8), 1), (dict(m=300, ws=A, less=1), 1),
     (dict(dy=A + 8), 1), (dict(z=A + 8), 1), (dict(dz=A + 8), 1), (dict(q=A + 8), 1), (dict(qt=A + 8), 1), (dict(sf=A + 2), 1),
     (dict(sft=A + 2), 1), (dict(dbias=A + 8), 1),
-    (dict(n=192), 2), (dict(n=128, act=18), 2), (dict(m=0x7fffffff - 126), 2),
+    (dict(n=192), 2), (dict(n=128, act=18), 2), (dict(m=0x7fffffff - 126), 2), (dict(n=1 << 23), 2), (dict(n=(1 << 23) - 128), OK),
 ])
 def test_activation_backward_refusals(change, status):
     v = dict(dy=A, z=A, act=3, dz=A, q=A, sf=A, qt=A, sft=A, dbias=A, m=8, n=256, ws=0)
@@ -147,7 +147,8 @@ def test_activation_backward_refusals(change, status):
 
 def test_activation_backward_workspace_query():
     f = dgm.dg_activation_backward_workspace_bytes
-    assert f(0, 128) == f(8, 0) == f(8, 100) == f(128, 256) == f(0x7fffffff, 128) == 0 and f(129, 256) == 2 * 256 * 4
+    assert f(0, 128) == f(8, 0) == f(8, 100) == f(128, 256) == f(0x7fffffff, 128) == 0 and f(129, 256) == 5 * 256 * 4
+    assert f(0x7fffffff - 127, (1 << 23) - 128) <= 1 << 30
 
 
 def test_linear_binding_checks_tensors():
