@@ -26,11 +26,10 @@ struct GroupedPlan {
 };
 
 // The tile with the least estimated time.  units(tile): how many of it the call has by the host's
-// guess, and the most it can have.  A ring has to leave room for the table; tiles with K groups
-// take one unit per workgroup; the 256x256 tile runs 15-20 % behind its estimate here
-// (measured over 15 calls).
+// guess, and the most it can have; slow: how far the 256x256 tile runs behind its estimate.  A
+// ring has to leave room for the table; tiles with K groups take one unit per workgroup.
 template <typename F>
-static GroupedPlan plan_grouped(int groups, int kb, int cus, F units) {
+static GroupedPlan plan_grouped(int groups, int kb, int cus, double slow, F units) {
   const int force = mxfp4_forced();
   GroupedPlan best{2, 0};
   double best_t = 1e30;
@@ -39,7 +38,7 @@ static GroupedPlan plan_grouped(int groups, int kb, int cus, F units) {
     long long most;
     const long long guess = units(t, &most);
     if (t.lds + group_table_bytes(groups) > kLdsBytes || (t.kg > 1 && most > cus)) continue;
-    const double us = id == force ? 0.0 : mxfp4_tile_time(id, guess, kb, cus) * (t.bm == 256 ? 1.2 : 1.0);
+    const double us = id == force ? 0.0 : mxfp4_tile_time(id, guess, kb, cus) * (t.bm == 256 ? slow : 1.0);
     if (us < best_t - 1e-9) {
       best_t = us;
       best = {id, (int)std::min<long long>(most, cus)};
@@ -49,12 +48,12 @@ static GroupedPlan plan_grouped(int groups, int kb, int cus, F units) {
 }
 
 // Along M: groups of equal size, and half a tile more for each.  (8192 x 4096 x 7168 in 8 groups
-// 162 us on 128x256, 189 on 128x128, 201 on 256x256; 64 x 4096 x 7168 in 32, the weights' stream,
-// 80 on 128x256, 86 on 128x128, 80 on 64x128, and 111 by a streaming kernel of 16 columns a
-// workgroup, as the dense GEMM has for few rows; 8 rows in 8 groups 26 on 64x128 with two K
-// groups, 34 streaming.)
+// 161 us on 128x256, 189 on 128x128, 177 on 256x256, whose tiles are the more often half empty; 64 x
+// 4096 x 7168 in 32, the weights' stream, 80 on 128x256, 86 on 128x128, 80 on 64x128, and 111 by a
+// streaming kernel of 16 columns a workgroup, as the dense GEMM has for few rows; 8 rows in 8
+// groups 26 on 64x128 with two K groups, 34 streaming.)
 static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
-  return plan_grouped(groups, k / 128, cus, [=](const Mxfp4TileInfo& t, long long* most) {
+  return plan_grouped(groups, k / 128, cus, 1.2, [=](const Mxfp4TileInfo& t, long long* most) {
     const long long tiles_n = (n + t.bn - 1) / t.bn;
     const int with_rows = std::min(m, groups);
     *most = ((long long)m / t.bm + with_rows) * tiles_n;
@@ -63,9 +62,10 @@ static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
   });
 }
 
-// Along K: every group that has rows has the same tiles.
+// Along K: every group that has rows has the same tiles.  (16384 rows in 8 groups, 4096 x 7168, 335
+// us on 256x256, 362 on 128x256, 429 on 128x128; 4000 rows, 4096 x 2048, 46, 49 and 57.)
 static GroupedPlan plan_kgroup(int m, int n, int kb, int groups, int cus) {
-  return plan_grouped(groups, std::max(1, kb / groups), cus, [=](const Mxfp4TileInfo& t, long long* most) {
+  return plan_grouped(groups, std::max(1, kb / groups), cus, 1.0, [=](const Mxfp4TileInfo& t, long long* most) {
     return *most = (long long)((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * groups;
   });
 }

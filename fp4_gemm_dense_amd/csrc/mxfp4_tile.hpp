@@ -290,6 +290,13 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
 
   // the lane, for terms formed where they are used
   auto lane_here = [&]() -> int {
+    if constexpr (T::ONE && GROUPED) {
+      // (formed anew each time: the builtin's value would be kept, in memory, and its reload
+      // waits for every copy in flight)
+      int ln;
+      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(ln));
+      return ln;
+    }
     return opaque(T::ONE ? (int)__builtin_amdgcn_mbcnt_hi(-1, __builtin_amdgcn_mbcnt_lo(-1, 0)) : lane);
   };
 
@@ -512,10 +519,23 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
 
   v4i af[2][MT], bf[NT];
   uint32_t sa[2][MT], sb[NT];   // scale words; the byte is taken at use
+  // The 256x256 tile's grouped kinds hold more than the dense one, whose registers are all taken:
+  // they form the addresses of a stage's K block 1 and of B's scale words (row * 4, from the
+  // fragments' row * 128) where they are used.  (With three registers in memory, reloaded in every
+  // stage, 16384 rows along K in 8 groups, 4096 x 7168, took 382 us, 335 so.)
+  constexpr bool FORM = T::ONE && GROUPED;
+  auto sb_at = [&]() {
+    return FORM ? ((uint32_t)opaque((int)b_rd) >> 5 & ~3u) + (T::OFF_SB - T::OFF_B / 32) : sb_rd;
+  };
+  auto of_half = [&](uint32_t x, auto half_tag) -> uint32_t {
+    constexpr uint32_t flip = decltype(half_tag)::value * 64u;
+    if constexpr (FORM && flip != 0) return (uint32_t)opaque((int)x) ^ flip;
+    else return x ^ flip;
+  };
   // Reads of K block H of the slot at byte offset rd, in two sets of parts.
   auto read_a = [&](uint32_t rd, auto half_tag, auto mt_tag) {
     constexpr int H = decltype(half_tag)::value, mt = decltype(mt_tag)::value;
-    af[H][mt] = *reinterpret_cast<const v4i*>(smem + rd + (a_rd ^ (H * 64u)) + mt * 2048);
+    af[H][mt] = *reinterpret_cast<const v4i*>(smem + rd + of_half(a_rd, half_tag) + mt * 2048);
   };
   auto read_sa = [&](uint32_t rd, auto half_tag) {
     constexpr int H = decltype(half_tag)::value;
@@ -527,11 +547,12 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
   // and after the last of a half of the column blocks that half's scale words
   auto read_b = [&](uint32_t rd, auto half_tag, auto nt_tag) {
     constexpr int H = decltype(half_tag)::value, nt = decltype(nt_tag)::value, NH = NT / 2;
-    bf[nt] = *reinterpret_cast<const v4i*>(smem + rd + (b_rd ^ (H * 64u)) + (nt >> 1) * 4096 + (nt & 1) * 512);
+    bf[nt] = *reinterpret_cast<const v4i*>(smem + rd + of_half(b_rd, half_tag) + (nt >> 1) * 4096 + (nt & 1) * 512);
     if constexpr (nt % NH == NH - 1) {
+      const uint32_t at = sb_at();
 #pragma unroll
       for (int e = nt - NH + 1; e <= nt; ++e)
-        sb[e] = *reinterpret_cast<const uint32_t*>(smem + rd + sb_rd + H * (T::BN * 4) + (e >> 1) * 128 + (e & 1) * 16);
+        sb[e] = *reinterpret_cast<const uint32_t*>(smem + rd + at + H * (T::BN * 4) + (e >> 1) * 128 + (e & 1) * 16);
     }
   };
   using I0 = std::integral_constant<int, 0>;
