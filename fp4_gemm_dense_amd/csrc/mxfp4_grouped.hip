@@ -63,9 +63,10 @@ static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
 }
 
 // Along K: every group that has rows has the same tiles.  (16384 rows in 8 groups, 4096 x 7168, 335
-// us on 256x256, 362 on 128x256, 429 on 128x128; 4000 rows, 4096 x 2048, 46, 49 and 57.)
+// us on 256x256, 362 on 128x256, 429 on 128x128; 4000 rows, 4096 x 2048, 46, 49 and 57; 1000 rows
+// in 32, 4096 x 7168, which writes D alone, 455, 506 and 597.)
 static GroupedPlan plan_kgroup(int m, int n, int kb, int groups, int cus) {
-  return plan_grouped(groups, std::max(1, kb / groups), cus, 1.0, [=](const Mxfp4TileInfo& t, long long* most) {
+  return plan_grouped(groups, std::max(1, kb / groups), cus, 0.95, [=](const Mxfp4TileInfo& t, long long* most) {
     return *most = (long long)((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * groups;
   });
 }

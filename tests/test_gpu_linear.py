@@ -325,3 +325,67 @@ def test_training_step_gradients(dg):
         # E2M1 steps are a sixth of the block's largest value at most: an operand is off by some 10 % of itself at
         # random, their product's sum by 15 % of its size
         assert np.linalg.norm(v - ref) < 0.25 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("m,n,k", [(70, 288, 4096), (300, 544, 1152), (20, 96, 512)])
+def test_graph_replays_match_eager(dg, m, n, k):
+    """Forward (a plan with partial tiles among them) and backward captured on a side stream: every replay on new inputs,
+    with eager calls between that use workspaces of their own, gives the eager results."""
+    n = n // 32 * 32
+    a, sa, b, sb, bias, _ = case(m, m, n, k, True, False, True)
+    ta, tsa, tb, tsb = (torch.from_numpy(v).cuda() for v in (a, sa, b, sb))
+    nb = (n + 255) // 256 * 256                                       # the backward pass's columns
+    zb, dy = dev(bf(1, m, nb, scale=2.0)), dev(bf(2, m, nb // 2))
+    tbias, res = dev(bias), dev(bf(3, m, n // 2))
+    new = lambda *sh, dt=torch.bfloat16: torch.empty(*sh, dtype=dt, device="cuda")   # noqa: E731
+    ws = new(max(1, dg.dg_mxfp4_gemm_workspace_bytes(m, n, k)), dt=torch.uint8)
+    ws2 = new(max(1, dg.dg_activation_backward_workspace_bytes(m, nb)), dt=torch.uint8)
+    mb = (m + 127) // 128
+    d, z = new(m, n // 2), new(m, n)
+    q, sf, qt, sft, dbias = (new(m, nb // 2, dt=torch.uint8), new(nb // 128, m, dt=torch.int32), new(nb, mb * 64, dt=torch.uint8),
+                             new(mb, nb, dt=torch.int32), new(nb, dt=torch.float32))
+    outs = (d, z, q, sf, qt, sft, dbias)
+    act = dg.ACT_GELU_TANH | dg.ACT_GATED
+
+    def step():
+        dg.dg_mxfp4_linear(ta, tsa, tb, tsb, tbias, act, res, z, d, ws)
+        dg.dg_activation_backward(dy, zb, act, None, q, sf, qt, sft, dbias, ws2)
+
+    step()
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for rep in range(4):
+        ta.copy_(torch.from_numpy(np.roll(a, rep + 1, axis=0)))
+        dy.mul_(-0.5)
+        want_d, want_z = dg.mxfp4_linear(ta, tsa, tb, tsb, tbias, act, res, pre_activation=True)
+        want = (want_d, want_z, *dg.activation_backward(dy, zb, act))
+        for t in outs:
+            t.view(torch.uint8).fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (t, v) in enumerate(zip(outs, want)):
+            assert torch.equal(t.view(torch.uint8), v.view(torch.uint8)), f"replay {rep}, output {i}"
+
+
+def test_calls_on_two_streams(dg):
+    """Calls in flight together on two streams, each with the workspace that the wrapper makes: what they give alone."""
+    sets = []
+    for seed, (m, n, k) in enumerate([(70, 544, 4096), (300, 1088, 1152)]):
+        a, sa, b, sb, bias, _ = case(seed, m, n, k, True, False, True)
+        t = [torch.from_numpy(v).cuda() for v in (a, sa, b, sb)] + [dev(bias), dg.ACT_SILU | dg.ACT_GATED]
+        zb, dy = dev(bf(seed, m, 512)), dev(bf(seed + 9, m, 256))
+        call = lambda t=t, zb=zb, dy=dy: (dg.mxfp4_linear(*t), *dg.activation_backward(dy, zb, dg.ACT_GELU | dg.ACT_GATED))   # noqa: E731
+        sets.append((call, call()))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [[], []]
+    for _ in range(8):
+        for i, (call, _) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    for (_, want), many in zip(sets, got):
+        for one in many:
+            assert all(torch.equal(w.view(torch.uint8), g.view(torch.uint8)) for w, g in zip(want, one))

@@ -188,8 +188,9 @@ def test_many_groups(dg):
     check_m(dg, a, sa, b, sb, ms, exact=True)
     kb = dg.dg_mxfp4_ragged_blocks(m, 1024)
     check_k(dg, *integers(rng, 16, kb * 128), *integers(rng, 32, kb * 128), ms, exact=True)
-    x, x64 = to_dev(values(2, m, 128), torch.bfloat16)
-    check_quantize(dg, x, x64, ms)
+    for dtype in (torch.bfloat16, torch.float32):
+        x, x64 = to_dev(values(2, m, 128), dtype)
+        check_quantize(dg, x, x64, ms)
 
 
 def test_nan_scales_stay_in_their_rows(dg):
