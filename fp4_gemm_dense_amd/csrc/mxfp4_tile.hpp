@@ -234,6 +234,22 @@ __device__ __forceinline__ void build_groups(const int32_t* ms, int groups, int 
   }
 }
 
+// The same with a third count, MOST where first is 2.
+template <int LESS, int MORE, int MOST>
+__device__ __forceinline__ void wait_vmcnt_first(int first) {
+  static_assert(LESS <= MORE && MORE <= MOST && MOST < 64, "vmcnt");
+  asm volatile(
+      "s_cmp_gt_i32 %0, 1\n\t"
+      "s_cbranch_scc1 .Lmost%=\n\t"
+      "s_cmp_lg_u32 %0, 0\n\t"
+      "s_cbranch_scc1 .Lmore%=\n\t"
+      "s_waitcnt vmcnt(%1)\n"
+      ".Lmore%=:\n\t"
+      "s_waitcnt vmcnt(%2)\n"
+      ".Lmost%=:\n\t"
+      "s_waitcnt vmcnt(%3)" ::"s"(first), "n"(LESS), "n"(MORE), "n"(MOST) : "memory", "scc");
+}
+
 // The arguments, all read here: left to where each is first used, the reads wait for one
 // another (96 x 24576 x 1536 9.2 us, 9.0 with them together).
 __device__ __forceinline__ void read_arguments(const Mxfp4Params& p) {   // (of every kind)
@@ -612,7 +628,10 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
         wait_lgkmcnt0();
         // (a gated lane's eight outputs come of two such pairs of column blocks)
         constexpr int more = (R - 2) * T::LPS, stores = T::KG > 1 ? 0 : KIND == MX_GATED && W == 8 ? T::NSTORE / 2 : T::NSTORE;
-        if constexpr (T::ONE) wait_vmcnt_first<more, more + T::LATE + stores>(first);
+        // (with z, first is 2: its stores are younger than the copies, too)
+        constexpr int z_stores = KIND == MX_GATED && W == 8 ? T::NSTORE : T::NSTORE * (KIND == MX_GATED ? 2 : 1);
+        if constexpr (T::ONE && LINEAR) wait_vmcnt_first<more, more + T::LATE + stores, more + T::LATE + stores + z_stores>(first);
+        else if constexpr (T::ONE) wait_vmcnt_first<more, more + T::LATE + stores>(first);
         else wait_vmcnt<more + (FIRST ? stores : 0)>();
         block_barrier();
         read_sa(nx, I0{});
@@ -647,6 +666,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
     const int S = ((cur.nkb + 1) / 2 + T::KG - 1) / T::KG;   // stages of this group
     int s = 0, first = 1;
     if constexpr (T::ONE) {
+      // (of the unit before: a whole tile with z, or a slice, which has as many stores as z and D)
+      if constexpr (LINEAR) first = p.z ? 2 : 1;
       asm volatile("" : "+s"(first));   // (the first stage is not peeled off the loop)
     } else {
       stage(std::true_type{}, 0);
@@ -714,13 +735,14 @@ __global__ void __launch_bounds__(T::THREADS, 1) mxfp4_tile_kernel(P p) {
       const LinearOut<KIND == MX_GATED, W> out(p);
       using Vec = typename LinearOut<KIND == MX_GATED, W>::Vec;
       // items of a lane's W outputs, their residual read PRE items ahead (a load behind a store is
-      // waited for with it; the 256x256 tile has registers for four)
+      // waited for with it; the 256x256 tile has registers for four, gated for two: with four, seven
+      // others were in memory, and their reloads waited for the stores)
       constexpr int ITEMS = KIND == MX_GATED && W == 8 ? NT / 4 : NT / 2, STEP = NT / 2 / ITEMS;
       const int c0 = wave_n * NT * 16 + (ln >> 4) * 8;   // the tile's column of item 0
       auto column = [&](int i) { return KIND == MX_GATED ? gated_output<W>(cur.n0 + c0 + i * STEP * 32) : cur.n0 + c0 + i * 32; };
       auto row_of = [&](int mt) { return cur.m0 + wave_m * MT * 16 + mt * 16 + (ln & 15); };
       const int cols = KIND == MX_GATED ? N >> 1 : N;
-      constexpr int ALL = MT * ITEMS, PRE = ALL < 4 ? ALL : 4;
+      constexpr int ALL = MT * ITEMS, PRE = T::ONE && KIND == MX_GATED ? 2 : ALL < 4 ? ALL : 4;
       Vec cv[PRE];
       auto read_c = [&](auto item_tag) {
         constexpr int mt = decltype(item_tag)::value / ITEMS, i = decltype(item_tag)::value % ITEMS;
