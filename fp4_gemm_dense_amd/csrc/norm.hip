@@ -98,6 +98,27 @@ __device__ __forceinline__ F block_sum(F v, F* red) {
   return s;
 }
 
+// The same with the waves' sums added by 16 lanes at a time: fewer registers (8192 x 7168 with
+// UE8M0 scales: 82 a thread, and two rows on a CU, with block_sum).
+__device__ __forceinline__ double block_sum_lanes(double v, double* red) {
+  v += lane_swap<1>(v);
+  v += lane_swap<2>(v);
+  v += lane_swap<4>(v);
+  v += lane_swap<8>(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  const int waves = blockDim.x >> 6, at = threadIdx.x & 15;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = at < waves ? red[at] : 0.0;
+  s += lane_swap<1>(s);
+  s += lane_swap<2>(s);
+  s += lane_swap<4>(s);
+  s += lane_swap<8>(s);
+  return s;
+}
+
 // 1 / sqrt(v), v > 0 within fp64's normal range (infinity: 0): the hardware's estimate, good to some
 // 2^-26, and two Newton steps, whose rounding leaves 2^-51.  (sqrt and a division are three times as
 // long a chain.)
@@ -210,7 +231,7 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
     }
-    const double r = rsqrt64(block_sum(ss, red) * p.inv_k + (double)p.eps);
+    const double r = rsqrt64(block_sum_lanes(ss, red) * p.inv_k + (double)p.eps);
     if (p.rstd_x && tid == 0) p.rstd_x[row] = (float)r;
     c *= r;
   }
@@ -288,7 +309,7 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) 
   }
   // the sum and r in 64 bits: a code near a border follows y = (h * weight) * r, whose first
   // product is exact (two bf16 values)
-  const double mean = block_sum(ss, red) * p.inv_k + (double)p.eps;
+  const double mean = (BLOCK ? block_sum_lanes(ss, red) : block_sum(ss, red)) * p.inv_k + (double)p.eps;
   const double r64 = BLOCK ? rsqrt64(mean) : 1.0 / sqrt(mean);
   const float r = (float)r64;
   const TwoFloats r2 = {r, (float)(r64 - (double)r)};
