@@ -231,6 +231,10 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
     }
+    if constexpr (V == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) asm volatile("" : "+v"(xv[i]));   // (unpacked again below, too)
+    }
     const double r = rsqrt64(block_sum_lanes(ss, red) * p.inv_k + (double)p.eps);
     if (p.rstd_x && tid == 0) p.rstd_x[row] = (float)r;
     c *= r;
@@ -306,6 +310,12 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) 
     if (p.h && j < nv) reinterpret_cast<v4i*>(p.h)[base + j] = hv[i];
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
+  }
+  if constexpr (BLOCK && V == 4) {
+    // (unpacked again below: their fp64 values would be kept for the rows that need them, and
+    // others in memory: 4096 x 16384 110 us, 103 so; shorter rows have the registers)
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" : "+v"(hv[i]));
   }
   // the sum and r in 64 bits: a code near a border follows y = (h * weight) * r, whose first
   // product is exact (two bf16 values)
