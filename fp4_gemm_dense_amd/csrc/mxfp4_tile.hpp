@@ -3,6 +3,8 @@
 // plan of a dense call.
 #pragma once
 
+#include <atomic>
+
 #include "dg_activation.hpp"
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
@@ -965,16 +967,28 @@ inline size_t group_table_bytes(int groups) { return (size_t)(2 * groups + 1) * 
   X(6, 2, 2, 2, 2, 4, 2)  \
   X(7, 4, 4, 2, 2, 2, 2)
 
+// Raises kernel f's limit of dynamic LDS on the current device, once for each (done: their bits).
+static hipError_t allow_lds(const void* f, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);   // (the entry points refuse device 64 and beyond)
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  const hipError_t set = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (set == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return set;
+}
+
 template <typename P>
 static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t stream, size_t table_bytes = 0) {
   switch (id) {
 #define X(i, MT, NT, WM, WN, R, KG)                                                                               \
   case i: {                                                                                                       \
     using T = MxTile<MT, NT, WM, WN, R, KG>;                                                                      \
-    static const hipError_t attr =                                                                                \
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T, P>),                              \
-                            hipFuncAttributeMaxDynamicSharedMemorySize,                                           \
-                            P::KIND >= MX_RAGGED ? kLdsBytes : P::KIND == MX_DENSE ? T::LDS : T::LDS + T::BIAS);  \
+    static std::atomic<uint64_t> allowed{0};                                                                      \
+    const hipError_t attr =                                                                                       \
+        allow_lds(reinterpret_cast<const void*>(&mxfp4_tile_kernel<T, P>),                                        \
+                  P::KIND >= MX_RAGGED ? kLdsBytes : P::KIND == MX_DENSE ? T::LDS : T::LDS + T::BIAS, allowed);   \
     if (attr != hipSuccess) return attr;                                                                          \
     const size_t lds = T::LDS + (P::KIND == MX_LINEAR || P::KIND == MX_GATED ? T::BIAS : table_bytes);           \
     hipLaunchKernelGGL((mxfp4_tile_kernel<T, P>), dim3(grid), dim3(T::THREADS), lds, stream, p);                  \
