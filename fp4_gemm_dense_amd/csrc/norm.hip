@@ -205,8 +205,9 @@ __device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, d
 }
 
 // h of the norms around a block, in place of x in xv; rv holds the residual.  x * post_weight
-// * gate is exact in fp32 (three bf16 numbers) wherever it keeps to fp32's range; the product
-// with scale * rx and the residual's addition are one fp64 step, so that h is the bf16 rounding
+// * gate is exact in fp32 (three bf16 numbers) wherever it keeps to fp32's normal range (below it
+// beside larger ones of a vector it is rounded to a multiple of 2^-149; a vector of such alone,
+// or beyond the range, goes by fp64); the product with scale * rx and the residual's addition are one fp64 step, so that h is the bf16 rounding
 // of its fp32 one whatever the order of the row's sum.
 template <int V>
 __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v4i (&xv)[V], const v4i (&rv)[V]) {

@@ -591,7 +591,8 @@ size_t dg_add_rms_norm_backward_workspace_bytes(int m, int k);
  *   h  = bf16(residual + scale * gate * (x * rx * post_weight))
  *   r  = 1 / sqrt(mean(h^2) + eps),  y = h * r * weight
  * and y is quantised as by dg_add_rms_norm (formats, layouts and exactness are its).  h is
- * rounded to fp32 and then to bf16 from a sum in fp64.
+ * rounded to fp32 and then to bf16 from a sum in fp64 (x * post_weight and its product with gate
+ * may be rounded to multiples of 2^-149 where they are below fp32's normal range).
  *   x           [m, k] bf16, the block's output; residual [m, k] bf16
  *   post_weight [k] bf16, or NULL: the block's output is not normed (x * rx * post_weight is x)
  *   gate        [ceil(m / gate_rows), k] bf16, or NULL (1): row i takes gate row i / gate_rows
