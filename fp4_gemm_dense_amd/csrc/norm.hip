@@ -33,7 +33,7 @@
 namespace dg {
 
 struct NormParams {
-  static constexpr bool BLOCK = false;
+  static constexpr bool BLOCK = false, TIGHT = false;
   const uint16_t* x;
   const uint16_t* residual;
   const uint16_t* weight;
@@ -54,6 +54,10 @@ struct SandwichParams : NormParams {
   float* rstd_x;
   int gate_rows;
   double scale;
+};
+// The same on fewer registers: four rows of 4097 to 7168 on a CU (launch_sandwich).
+struct SandwichTightParams : SandwichParams {
+  static constexpr bool TIGHT = true;
 };
 
 // A row is spread over a workgroup of 64 .. 1024 threads (whole waves), V vectors of 8
@@ -205,12 +209,13 @@ __device__ __forceinline__ uint32_t y_by_fp64(const v4i& h, const v4i& weight, d
 }
 
 // h of the norms around a block, in place of x in xv; rv holds the residual.  x * post_weight
-// * gate is exact in fp32 (three bf16 numbers) wherever it keeps to fp32's normal range (below it
-// beside larger ones of a vector it is rounded to a multiple of 2^-149; a vector of such alone,
-// or beyond the range, goes by fp64); the product with scale * rx and the residual's addition are one fp64 step, so that h is the bf16 rounding
-// of its fp32 one whatever the order of the row's sum.
-template <int V>
-__device__ __forceinline__ void block_output(const SandwichParams& p, int row, v4i (&xv)[V], const v4i (&rv)[V]) {
+// * gate is exact in fp32 (three bf16 numbers) wherever it keeps to fp32's normal range (below
+// it, beside larger ones of a vector, it is rounded to a multiple of 2^-149; a vector of such
+// alone, or beyond the range, goes by fp64).  The product with scale * rx and the residual's
+// addition are one fp64 step, so that the order of the row's sum does not show in h but for
+// values within some 2^-50 of an fp32 midpoint.
+template <int V, typename P>
+__device__ __forceinline__ void block_output(const P& p, int row, v4i (&xv)[V], const v4i (&rv)[V]) {
   __shared__ double red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x, nv = p.k >> 3;
   v4i pv[V], gv[V];
@@ -232,7 +237,7 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
     }
-    if constexpr (V == 4) {
+    if constexpr (V == 4 || P::TIGHT) {
 #pragma unroll
       for (int i = 0; i < V; ++i) asm volatile("" : "+v"(xv[i]));   // (unpacked again below, too)
     }
@@ -269,7 +274,8 @@ __device__ __forceinline__ void block_output(const SandwichParams& p, int row, v
 // against 2 to 8 persistent workgroups per CU: one row was the fastest at 8192 x 7168
 // in every format, 70-75 us against 73-84.)
 template <int FMT, int V, typename P>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) {
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512) __attribute__((amdgpu_waves_per_eu(P::TIGHT ? 7 : 1)))
+add_rms_norm_kernel(P p) {
   constexpr bool BLOCK = P::BLOCK;
   __shared__ double red[NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -312,9 +318,9 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) add_rms_norm_kernel(P p) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fma((double)a[e], (double)a[e], ss);
   }
-  if constexpr (BLOCK && V == 4) {
+  if constexpr (BLOCK && (V == 4 || P::TIGHT)) {
     // (unpacked again below: their fp64 values would be kept for the rows that need them, and
-    // others in memory: 4096 x 16384 110 us, 103 so; shorter rows have the registers)
+    // others in memory: 4096 x 16384 110 us, 103 so)
 #pragma unroll
     for (int i = 0; i < V; ++i) asm volatile("" : "+v"(hv[i]));
   }
@@ -815,9 +821,13 @@ static int norm_parts(int m, int k) {
 template <int FMT, typename P>
 static hipError_t launch_norm(const P& p, hipStream_t hs) {
   const NormShape s = norm_shape(p.k);
-  if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
-  else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
-  else hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 4, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  if constexpr (P::TIGHT) {
+    hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  } else {
+    if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+    else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+    else hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 4, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+  }
   return hipGetLastError();
 }
 
@@ -894,6 +904,15 @@ static int launch_norm_format(const P& p, int format, void* stream) {
   return e == hipSuccess ? DG_OK : DG_ERR_HIP;
 }
 
+// Rows of 4097 to 7168 (five to seven waves), where they fill the chip, take four to a CU, on 72
+// registers: 8192 x 7168 with fp32 scales 100 -> 97 us, UE8M0 96 -> 93.5, MXFP4 93 -> 90.5.  Three
+// of eight waves fit either way (4096 x 8192 52.2, 52.9 so: the values are unpacked twice), and
+// shorter rows are more without (4096 x 4096 29.0, 30.2 so).
+static int launch_sandwich(const SandwichParams& p, int format, void* stream) {
+  if (p.k > 4096 && p.k <= 7168 && p.m >= 2048) return launch_norm_format(SandwichTightParams{p}, format, stream);
+  return launch_norm_format(p, format, stream);
+}
+
 extern "C" {
 
 int dg_add_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h, void* q,
@@ -915,7 +934,7 @@ int dg_sandwich_norm(const uint16_t* x, const uint16_t* residual, const uint16_t
     if (misaligned(post_weight, 16) || misaligned(gate, 16) || misaligned(rstd_x, 4)) return DG_ERR_INVALID_ARG;
     const SandwichParams p{{x, residual, weight, h, q, sf, rstd, m, k, eps, 1.0 / k}, post_weight, gate, rstd_x, gate_rows, scale};
     const int st = norm_arguments(p, format);
-    return st != DG_OK ? st : launch_norm_format(p, format, stream);
+    return st != DG_OK ? st : launch_sandwich(p, format, stream);
   } catch (...) {
     return DG_ERR_HIP;
   }

@@ -59,12 +59,21 @@ def run(dgm, x, res, pw, gate, w, fmt, gate_rows, scale, eps=1e-6, inplace=None)
     return (q.cpu().numpy(), sf.cpu().numpy(), bits(h), rstd.cpu().numpy().astype(np.float64)), rstd_x.cpu().numpy().astype(np.float64)
 
 
-def check(got, rstd_x, x, res, pw, gate, w, fmt, gate_rows, scale, eps=1e-6):
+def check(got, rstd_x, x, res, pw, gate, w, fmt, gate_rows, scale, eps=1e-6, fp64=False):
+    """fp64: h is anything between the roundings of values 2^-48 of the magnitudes in it below and above the oracle's."""
     m, k = x.shape
     f = [None if v is None else bf16_bits_to_f64(v) for v in (x, res, pw)]
     h, rx = X.sandwich_norm(*f, by_row(gate, gate_rows, m), scale, eps)
     want = bf16_of_fp32(h)
     bad = got[2] != want
+    if fp64:
+        # Where the residual cancels the branch but for the roundings on the way (scale 0.7: 0.7 * 0.2734375 - 0.19140625 is
+        # some 10^-17), h is what they leave.  The oracle rounds three products, 1/rms (a sum of k squares in pairs, a
+        # root and a division: 2^-49 at most here) and the sum; the kernel c = scale * rx (rx within 2^-49) and one fma:
+        # together below 2^-48 of |residual| + |branch|, and both roundings behind it keep the order.
+        off = 2.0 ** -48 * (np.abs(f[1]) + np.abs(h - f[1]))
+        lo, hi, is_ = (bf16_bits_to_f64(v) for v in (bf16_of_fp32(h - off), bf16_of_fp32(h + off), got[2]))
+        bad &= ~((lo <= is_) & (is_ <= hi))
     assert not bad.any(), f"h: {bad.sum()} differ, first at {np.argwhere(bad)[0]}"
     if pw is not None:
         assert (np.abs(rstd_x - rx) <= 2 * U * rx).all(), "rstd_x"
@@ -122,6 +131,28 @@ def test_sandwich_in_place(dg, which):
     a = inputs(11, 7, 1280, 3)
     got, rx = run(dg, *a, MX, 3, 0.5, inplace=which)
     check(got, rx, *a, MX, 3, 0.5)
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
+@pytest.mark.parametrize("m,k,gate_rows,post", [(2048, 4224, 700, True), (2065, 7168, 1, True), (2100, 8192, 2100, False)])
+def test_sandwich_long_rows_many(dg, m, k, gate_rows, post, fmt):
+    """Many long rows run on fewer registers: the rows of two halves, bit for bit, and the oracle's on some."""
+    a = inputs(m, m, k, gate_rows, post)
+    a[0][7], a[1][7] = 0, 0                       # eps alone decides
+    a[0][40], a[1][40] = a[0][40] & 0x87ff, 0     # far below 1: products of fp64
+    a[0][m - 1, 5] = 0x7fc0
+    got, rx = run(dg, *a, fmt, gate_rows, 0.7)
+    half = -(-m // 2 // gate_rows) * gate_rows if gate_rows <= m // 2 else m // 2 + 1
+    for lo, hi in ((0, half), (half, m)):
+        gate = a[3] if gate_rows >= m else a[3][lo // gate_rows:]
+        part, prx = run(dg, a[0][lo:hi], a[1][lo:hi], a[2], gate[:-(-(hi - lo) // gate_rows)], a[4], fmt, gate_rows, 0.7)
+        assert np.array_equal(prx.view(np.int64), rx[lo:hi].view(np.int64)) or not post
+        for i, (g, w) in enumerate(zip(got, part)):
+            g = g[:, lo:hi] if i == 1 and fmt != UE8M0 else g[lo:hi]
+            assert np.array_equal(np.ascontiguousarray(g).view(np.uint8), np.ascontiguousarray(w).view(np.uint8)), i
+    few = [v[:48] for v in a[:2]] + [a[2], a[3][:-(-48 // gate_rows)], a[4]]
+    sf = got[1][:, :48] if fmt != UE8M0 else got[1][:48]
+    check((got[0][:48], sf, got[2][:48], got[3][:48]), rx[:48], *few, fmt, gate_rows, 0.7, fp64=True)
 
 
 def test_sandwich_wrapper_matches_the_plain_norm(dg):
