@@ -7,7 +7,10 @@
 // that dz stores; the sums take the unrounded ones.
 //
 // Bound: HBM.  An element of dz costs 2 bytes of z and 2 of dy (gated: 1) of reading and
-// 17/32 of writing per direction.
+// 17/32 of writing per direction.  Measured (one MI355X, both directions and dbias): 4096 x 16384
+// gated with SiLU 82 us (floor at a copy's 5.1 TB/s 53), SiLU alone 91 (66), the identity 83; 2001 x
+// 4096 GELU 15.4 and 4.6 of the sums (8.1: 512 tiles on 256 CUs, whose reads, arithmetic and writes follow
+// one another); 130 x 4096 gated 6.8 + 2.7.  Of the first, 9 us are dbias and 15 the columns.
 #include <algorithm>
 
 #include "../../include/dg.h"

@@ -6,6 +6,13 @@
 // on the fp32 accumulators where they are (after the K groups' sums have met, or in the reduce
 // of a plan split along K), so neither u nor act(u) goes to memory between the two.  act reads
 // the unrounded u, whether or not z is stored: the same d either way.
+//
+// Bound: as the dense GEMM, and the epilogue behind a unit's last product, which nothing
+// overlaps but the next unit's copies.  Measured (one MI355X; in brackets the dense GEMM, whose D
+// is [m, n]): 4096 x 16384 x 7168 gated with SiLU 232-239 us (225-233), with z 278 (237-244: z is 134 MB
+// more); 4096 x 7168 x 16384 with residual 247 (235); 4096 x 24576 x 1536 NONE 107 (98), ReLU 112-119,
+// gated SiLU with z 128, GELU 150-160 (its polynomial for 128 values of a lane in a unit); 2001 x 4096 x
+// 7168 GELU with residual and z 41 (35); 1 x 4096 x 7168 6.6 (6.1).
 #include <algorithm>
 
 #include "../../include/dg.h"
