@@ -61,7 +61,7 @@ namespace dg {
 
 static const Mxfp4TileInfo kMxTiles[] = {
 #define X(id, MT, NT, WM, WN, R, KG) {MxTile<MT, NT, WM, WN, R, KG>::BM, MxTile<MT, NT, WM, WN, R, KG>::BN, KG, MxTile<MT, NT, WM, WN, R, KG>::LDS, NT < 4},
-    DG_MXFP4_TILES(X)
+    DG_MXFP4_TILES(X) DG_MXFP4_GROUPED_TILES(X)
 #undef X
 };
 
@@ -110,9 +110,10 @@ int mxfp4_forced() {
 }
 
 // Of each tile: a stage of 256 values of K, and a unit's fixed share, in microseconds.
-static constexpr double kStage[] = {1.85, 1.12, 0.76, 0.69, 0.57, 0.81, 0.52, 1.05};
-static constexpr double kUnit[] = {4.5, 2.0, 1.0, 1.0, 1.8, 1.9, 1.6, 2.5};
-static_assert(sizeof(kStage) / sizeof(kStage[0]) == kMxTileCount && sizeof(kMxTiles) / sizeof(kMxTiles[0]) == kMxTileCount, "tiles");
+static constexpr double kStage[] = {1.85, 1.12, 0.76, 0.69, 0.57, 0.81, 0.52, 1.05, 1.45};
+static constexpr double kUnit[] = {4.5, 2.0, 1.0, 1.0, 1.8, 1.9, 1.6, 2.5, 3.3};
+static_assert(sizeof(kStage) / sizeof(kStage[0]) == kMxGroupedTileCount && sizeof(kMxTiles) / sizeof(kMxTiles[0]) == kMxGroupedTileCount,
+              "tiles");
 
 double mxfp4_tile_time(int id, long long units, int kb, int cus) {
   const int kg = kMxTiles[id].kg, whole = ((kb + 1) / 2 + kg - 1) / kg;

@@ -13,8 +13,7 @@
 //
 // Bound: with few rows the stream of the weights (64 rows over 32 experts of 4096 x 7168 80 us: 403 MB
 // at 5.0 TB/s); with many the schedule, as the dense GEMM, and the groups' last tiles (8192 rows over 8
-// 161-178 us, 2.7-3.0 PFLOP/s, matrix cores 34 % busy; 4000 rows over 8 of 4096 x 2048 41, 2.3 rounds
-// of units); along K the stores of D (4000 rows in 8 groups of 4096 x 2048 46-51, 134 MB of D).
+// 144-150 us, 3.2-3.3 PFLOP/s; 4000 rows over 8 of 4096 x 2048 34, 1.6 rounds of units); along K the stores of D (4000 rows in 8 groups of 4096 x 2048 46-51, 134 MB of D).
 #include <algorithm>
 
 #include "../../include/dg.h"
@@ -38,7 +37,7 @@ static GroupedPlan plan_grouped(int groups, int kb, int cus, double slow, F unit
   const int force = mxfp4_forced();
   GroupedPlan best{2, 0};
   double best_t = 1e30;
-  for (int id = 0; id < kMxTileCount; ++id) {
+  for (int id = 0; id < kMxGroupedTileCount; ++id) {
     const Mxfp4TileInfo t = mxfp4_tile_info(id);
     long long most;
     const long long guess = units(t, &most);
@@ -53,12 +52,14 @@ static GroupedPlan plan_grouped(int groups, int kb, int cus, double slow, F unit
 }
 
 // Along M: groups of equal size, and half a tile more for each.  (8192 x 4096 x 7168 in 8 groups
-// 161 us on 128x256, 189 on 128x128, 177 on 256x256, whose tiles are the more often half empty; 64 x
+// 144 us on 192x256, 161 on 128x256, 176 on 256x256, 187 on 128x128: 3 rounds of units, 5, 3 and 9; 3901
+// x 2048 x 4096 in 16 31 on 192x256, 38 on the best other.  The tile taken is on average 2 % behind the
+// best of 80 shapes with 4 to 64 groups of like and unlike sizes, at worst 26 %; 64 x
 // 4096 x 7168 in 32, the weights' stream, 80 on 128x256, 86 on 128x128, 80 on 64x128, and 111 by a
 // streaming kernel of 16 columns a workgroup, as the dense GEMM has for few rows; 8 rows in 8
 // groups 26 on 64x128 with two K groups, 34 streaming.)
 static GroupedPlan plan_ragged(int m, int n, int k, int groups, int cus) {
-  return plan_grouped(groups, k / 128, cus, 1.2, [=](const Mxfp4TileInfo& t, long long* most) {
+  return plan_grouped(groups, k / 128, cus, 1.05, [=](const Mxfp4TileInfo& t, long long* most) {
     const long long tiles_n = (n + t.bn - 1) / t.bn;
     const int with_rows = std::min(m, groups);
     *most = ((long long)m / t.bm + with_rows) * tiles_n;

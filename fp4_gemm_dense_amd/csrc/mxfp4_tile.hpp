@@ -966,6 +966,8 @@ inline size_t group_table_bytes(int groups) { return (size_t)(2 * groups + 1) * 
   X(5, 3, 4, 2, 2, 2, 2)  \
   X(6, 2, 2, 2, 2, 4, 2)  \
   X(7, 4, 4, 2, 2, 2, 2)
+// and of the grouped kinds alone (whose rounds it fills better: mxfp4_grouped.hip)
+#define DG_MXFP4_GROUPED_TILES(X) X(8, 3, 8, 4, 2, 2, 1)
 
 // Raises kernel f's limit of dynamic LDS on the current device, once for each (done: their bits).
 static hipError_t allow_lds(const void* f, int bytes, std::atomic<uint64_t>& done) {
@@ -995,6 +997,10 @@ static hipError_t launch_mxfp4_tile(const P& p, int id, int grid, hipStream_t st
     return hipGetLastError();                                                                                     \
   }
     DG_MXFP4_TILES(X)
+  default:
+    if constexpr (P::KIND >= MX_RAGGED) {
+      switch (id) { DG_MXFP4_GROUPED_TILES(X) }
+    }
 #undef X
   }
   return hipErrorInvalidValue;
@@ -1031,7 +1037,7 @@ struct Mxfp4TileInfo {
   bool narrow;   // its waves have fewer than 64 columns
 };
 Mxfp4TileInfo mxfp4_tile_info(int id);
-constexpr int kMxTileCount = 8, kMxSkinnyIdBase = 100;
+constexpr int kMxTileCount = 8, kMxGroupedTileCount = 9, kMxSkinnyIdBase = 100;
 int mxfp4_forced();   // the kernel that DG_FORCE_MXFP4 pins (kMxSkinnyIdBase and up: a streaming one), or -1
 // Estimated microseconds of `units` whole tiles of kb K blocks each.
 double mxfp4_tile_time(int id, long long units, int kb, int cus);

@@ -67,7 +67,7 @@ def test_m_grouped_sizes(dg, sizes, tail):
     check_m(dg, a, sa, b, sb, sizes)
 
 
-@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7, 8])
 def test_m_grouped_every_kernel(dg, kernel, monkeypatch):
     """Each tile pinned, on all CUs and on eight (several tiles of several groups per workgroup, odd and even counts of K
     blocks, fewer than the ring's slots too); exact integers."""
@@ -164,7 +164,7 @@ def test_k_grouped_sizes(dg, sizes):
     check_k(dg, *rand_mx(rng, m, kb * 128), *rand_mx(rng, n, kb * 128), sizes)
 
 
-@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3, 4, 5, 6, 7, 8])
 def test_k_grouped_every_kernel(dg, kernel, monkeypatch):
     monkeypatch.setenv("DG_FORCE_MXFP4", str(kernel))
     for sizes in ([300, 0, 70, 1], [5, 129, 0, 0, 1300, 256, 2]):
