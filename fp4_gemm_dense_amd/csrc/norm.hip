@@ -25,7 +25,7 @@
 // Around a block, with its own norm and a gate: forward 8192 x 7168 90.5 us MXFP4, 93.5 UE8M0, 97 fp32
 // scales (4.3-4.5 TB/s; without the gate 89, without the post-norm 77: two sums over a row, one
 // after the other, and fp64 for each value of h), 3 x 7168 4.8; backward, 12 bytes per element, 4096 x
-// 7168 77 us and 6 in the second kernel (4.3 TB/s), 4096 x 16384 254 (floor 157: one row on a CU), 130 x
+// 7168 77 us and 6 in the second kernel (4.3 TB/s), 4096 x 16384 233 (floor 157: one row on a CU), 130 x
 // 2048 5.8 + 3.6.
 #include <algorithm>
 #include <cmath>
@@ -632,11 +632,13 @@ struct SandwichBackParams {
 // both gradients behind it: dgate = scale * post_weight * S, and dpost_weight adds up scale *
 // gate * S.  A gate's sum that lies in one workgroup is final; the first and the last gate of
 // a workgroup may go on in its neighbours, and leave as its partial rows 0 and 1 (0 where
-// the two are one).  Rows of up to 8192 read the next row's dy and h ahead and keep the weights;
-// longer ones have no registers for either.
-template <int V>
-__global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBackParams p) {
-  constexpr bool AHEAD = V <= 2, KEEP = V <= 2;
+// the two are one).  Rows of up to 8192 read the next row's dy and h ahead and keep the weights.
+// Longer ones (WIDE) take up to 1024 threads, twice the waves with half the registers each, which
+// hold neither: 4096 x 16384 233 us, 2048 x 9216 81, with four vectors a thread 255 and 96 (and
+// with the weights' addresses kept, 31 registers in memory for these 25, 238 and 83).
+template <int V, int THREADS = 512>
+__global__ void __launch_bounds__(THREADS) sandwich_norm_backward_kernel(SandwichBackParams p) {
+  constexpr bool WIDE = THREADS == 1024, AHEAD = !WIDE, KEEP = !WIDE;
   __shared__ float red[2][2][NORM_MAX_WAVES];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.k >> 3;
@@ -647,7 +649,8 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
     return j < nv ? reinterpret_cast<const v4i*>(t)[(size_t)row * nv + j] : none;
   };
   auto store = [&](float* t, int i, const float (&v)[8]) {
-    const int j = i * nt + tid;
+    int j = i * nt + tid;
+    if constexpr (WIDE) asm volatile("" : "+v"(j));
     if (j >= nv) return;
     v4f* o = reinterpret_cast<v4f*>(t + (size_t)j * 8);
     o[0] = v4f{v[0], v[1], v[2], v[3]};
@@ -657,9 +660,15 @@ __global__ void __launch_bounds__(512) sandwich_norm_backward_kernel(SandwichBac
   v4i dyn[V], hn[V], wk[KEEP ? V : 1], pk[KEEP ? V : 1], gk[KEEP ? V : 1];
   int gate = -1;
   // the weights and the present gate: kept in registers, or read where they are used
-  auto read_weight = [&](int i) { return at(p.weight, 0, i); };
-  auto read_post = [&](int i) { return p.post_weight ? at(p.post_weight, 0, i) : one; };
-  auto read_gate = [&](int i) { return p.gate ? at(p.gate, gate, i) : one; };
+  auto vector = [&](const uint16_t* t, int i) -> v4i {
+    if constexpr (!WIDE) return at(t, 0, i);
+    int o = (i * nt + tid) * 16;
+    asm volatile("" : "+v"(o));   // (read here, not ahead of the rows, and its address formed here)
+    return dg_raw_buffer_load_v4i32(make_buffer_rsrc(t, (uint32_t)p.k * 2u), o, 0, 0);
+  };
+  auto read_weight = [&](int i) { return vector(p.weight, i); };
+  auto read_post = [&](int i) { return p.post_weight ? vector(p.post_weight, i) : one; };
+  auto read_gate = [&](int i) { return p.gate ? vector(p.gate + (size_t)gate * p.k, i) : one; };
   auto weight_of = [&](int i) { return KEEP ? wk[KEEP ? i : 0] : read_weight(i); };
   auto post_of = [&](int i) { return KEEP ? pk[KEEP ? i : 0] : read_post(i); };
   auto gate_of = [&](int i) { return KEEP ? gk[KEEP ? i : 0] : read_gate(i); };
@@ -862,7 +871,7 @@ static hipError_t launch_sandwich_backward(const SandwichBackParams& p, int grid
   const NormShape s = norm_shape(p.k);
   if (s.v == 1) hipLaunchKernelGGL((sandwich_norm_backward_kernel<1>), dim3(grid), dim3(s.threads), 0, hs, p);
   else if (s.v == 2) hipLaunchKernelGGL((sandwich_norm_backward_kernel<2>), dim3(grid), dim3(s.threads), 0, hs, p);
-  else hipLaunchKernelGGL((sandwich_norm_backward_kernel<4>), dim3(grid), dim3(s.threads), 0, hs, p);
+  else hipLaunchKernelGGL((sandwich_norm_backward_kernel<2, 1024>), dim3(grid), dim3((p.k / 16 + 63) / 64 * 64), 0, hs, p);
   return hipGetLastError();
 }
 
