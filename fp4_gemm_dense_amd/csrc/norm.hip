@@ -60,7 +60,7 @@ struct SandwichParams : NormParams {
   int gate_rows;
   double scale;
 };
-// The same on fewer registers: four rows of 4097 to 7168 on a CU (launch_sandwich).
+// The same with two vectors a thread on fewer registers (launch_sandwich).
 struct SandwichTightParams : SandwichParams {
   static constexpr bool TIGHT = true;
 };
@@ -279,7 +279,7 @@ __device__ __forceinline__ void block_output(const P& p, int row, v4i (&xv)[V], 
 // against 2 to 8 persistent workgroups per CU: one row was the fastest at 8192 x 7168
 // in every format, 70-75 us against 73-84.)
 template <int FMT, int V, typename P>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) __attribute__((amdgpu_waves_per_eu(P::TIGHT ? 7 : 1)))
+__global__ void __launch_bounds__(V == 4 || P::TIGHT ? 1024 : 512) __attribute__((amdgpu_waves_per_eu(P::TIGHT ? 7 : 1)))
 add_rms_norm_kernel(P p) {
   constexpr bool BLOCK = P::BLOCK;
   __shared__ double red[NORM_MAX_WAVES];
@@ -836,7 +836,7 @@ template <int FMT, typename P>
 static hipError_t launch_norm(const P& p, hipStream_t hs) {
   const NormShape s = norm_shape(p.k);
   if constexpr (P::TIGHT) {
-    hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
+    hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3((p.k / 16 + 63) / 64 * 64), 0, hs, p);
   } else {
     if (s.v == 1) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 1, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
     else if (s.v == 2) hipLaunchKernelGGL((add_rms_norm_kernel<FMT, 2, P>), dim3(p.m), dim3(s.threads), 0, hs, p);
@@ -921,9 +921,12 @@ static int launch_norm_format(const P& p, int format, void* stream) {
 // Rows of 4097 to 7168 (five to seven waves), where they fill the chip, take four to a CU, on 72
 // registers: 8192 x 7168 with fp32 scales 100 -> 97 us, UE8M0 96 -> 93.5, MXFP4 93 -> 90.5.  Three
 // of eight waves fit either way (4096 x 8192 52.2, 52.9 so: the values are unpacked twice), and
-// shorter rows are more without (4096 x 4096 29.0, 30.2 so).
+// shorter rows are more without (4096 x 4096 29.0, 30.2 so).  Rows of 8193 to 12288 take two vectors
+// of up to 768 threads where the plain norm has four of half as many: as many rows on a CU
+// with twice the waves (2048 x 9216 47.7 -> 38.2, 4096 x 12288 101.5 -> 78.6; 4096 x 14336 106, 114 so, 4096 x
+// 16384, one row on a CU then, 105, 130 so).
 static int launch_sandwich(const SandwichParams& p, int format, void* stream) {
-  if (p.k > 4096 && p.k <= 7168 && p.m >= 2048) return launch_norm_format(SandwichTightParams{p}, format, stream);
+  if ((p.k > 4096 && p.k <= 7168 && p.m >= 2048) || (p.k > 8192 && p.k <= 12288)) return launch_norm_format(SandwichTightParams{p}, format, stream);
   return launch_norm_format(p, format, stream);
 }
 

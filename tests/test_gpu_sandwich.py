@@ -134,9 +134,10 @@ def test_sandwich_in_place(dg, which):
 
 
 @pytest.mark.parametrize("fmt", [F32, UE8M0, MX])
-@pytest.mark.parametrize("m,k,gate_rows,post", [(2048, 4224, 700, True), (2065, 7168, 1, True), (2100, 8192, 2100, False)])
+@pytest.mark.parametrize("m,k,gate_rows,post", [(2048, 4224, 700, True), (2065, 7168, 1, True), (2100, 8192, 2100, False),
+                                                (100, 8320, 7, True), (64, 12288, 64, True), (90, 11008, 1, False)])
 def test_sandwich_long_rows_many(dg, m, k, gate_rows, post, fmt):
-    """Many long rows run on fewer registers: the rows of two halves, bit for bit, and the oracle's on some."""
+    """Long rows, and many of them, run on other kernels: the rows of two halves, bit for bit, and the oracle's on some."""
     a = inputs(m, m, k, gate_rows, post)
     a[0][7], a[1][7] = 0, 0                       # eps alone decides
     a[0][40], a[1][40] = a[0][40] & 0x87ff, 0     # far below 1: products of fp64
