@@ -150,19 +150,19 @@ __device__ __forceinline__ void quantize_tile_columns(QuantTile<T>& l, int rows,
       if constexpr (sizeof(T) == 2) {
         uint32_t e[32];   // rows b*32 .. of columns c2 (low half) and c2 + 1
         us2 am = us2{0, 0};
-    #pragma unroll
+#pragma unroll
         for (int r = 0; r < 32; ++r) {
           e[r] = *reinterpret_cast<const uint32_t*>(&l.tile[b * 32 + r][c2]);
           am = us2max(am, us2abs((int)e[r]));
         }
-    #pragma unroll
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
           byte[h] = ue8m0_byte<false>((uint32_t)(h ? am.y : am.x) << 16);
           const float scale = ue8m0_value(byte[h]);
-    #pragma unroll
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
             v4i pr;   // eight rows of the column
-    #pragma unroll
+#pragma unroll
             for (int j = 0; j < 4; ++j)
               pr[j] = (int)__builtin_amdgcn_perm(e[8 * q + 2 * j + 1], e[8 * q + 2 * j], h ? 0x07060302u : 0x05040100u);
             w[h][q] = byte[h] == 255u ? 0 : (int)e2m1x8(pr, scale);
@@ -171,7 +171,7 @@ __device__ __forceinline__ void quantize_tile_columns(QuantTile<T>& l, int rows,
       } else {
         float e[2][32];
         uint32_t am[2] = {0, 0};
-    #pragma unroll
+#pragma unroll
         for (int r = 0; r < 32; ++r) {
           const float2 f = *reinterpret_cast<const float2*>(&l.tile[b * 32 + r][c2]);
           e[0][r] = f.x;
@@ -179,14 +179,14 @@ __device__ __forceinline__ void quantize_tile_columns(QuantTile<T>& l, int rows,
           am[0] = umax(am[0], abs_bits(f.x));
           am[1] = umax(am[1], abs_bits(f.y));
         }
-    #pragma unroll
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
           byte[h] = ue8m0_byte<false>(am[h]);
           const float scale = ue8m0_value(byte[h]);
-    #pragma unroll
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
             float o[8];
-    #pragma unroll
+#pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = e[h][8 * q + j];
             w[h][q] = byte[h] == 255u ? 0 : (int)e2m1x8(o, scale);
           }
