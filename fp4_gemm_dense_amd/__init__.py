@@ -714,11 +714,14 @@ def dg_add_rms_norm_backward(dy, dh, h, weight, rstd, dx, dweight, workspace=Non
 
 
 def _gate_shape(gate, gate_rows, m, k):
+    """The gate's shape, and gate_rows as the C call takes it: an int there, so that m stands for every number beyond
+    (their low 32 bits would be another number of gate rows)."""
     if gate is None:
-        return None
+        return None, 1
     if gate_rows < 1:
         raise ValueError(f"gate_rows: expected 1 or more, got {gate_rows}")
-    return ((m + gate_rows - 1) // gate_rows, k)
+    gate_rows = min(gate_rows, max(m, 1))
+    return ((m + gate_rows - 1) // gate_rows, k), gate_rows
 
 
 def dg_sandwich_norm(x, residual, post_weight, gate, weight, h, q, sf, quant_format, rstd_x=None, rstd=None, gate_rows=1,
@@ -729,7 +732,7 @@ def dg_sandwich_norm(x, residual, post_weight, gate, weight, h, q, sf, quant_for
     m, k = x.shape
     if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
         raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
-    shape, dev, gshape = (m, k), x.get_device(), _gate_shape(gate, gate_rows, m, k)
+    shape, dev, (gshape, gate_rows) = (m, k), x.get_device(), _gate_shape(gate, gate_rows, m, k)
     sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
     _call("dg_sandwich_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
           _arg(post_weight, _BF, (k,), dev, "post_weight"), _arg(gate, _BF, gshape, dev, "gate"),
@@ -749,7 +752,7 @@ def dg_sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rstd_x, r
     (see include/dg.h); dh may be None, post_weight, rstd_x and dpost_weight together, and gate and dgate.  workspace:
     uint8 device tensor of at least dg_sandwich_norm_backward_workspace_bytes(...) bytes."""
     m, k = dy.shape
-    shape, dev, gshape = (m, k), dy.get_device(), _gate_shape(gate, gate_rows, m, k)
+    shape, dev, (gshape, gate_rows) = (m, k), dy.get_device(), _gate_shape(gate, gate_rows, m, k)
     nbytes = workspace.numel()
     _call("dg_sandwich_norm_backward", dev, _arg(dy, _BF, shape, dev, "dy"), _arg(dh, _BF, shape, dev, "dh"),
           _arg(x, _BF, shape, dev, "x"), _arg(h, _BF, shape, dev, "h"), _arg(post_weight, _BF, (k,), dev, "post_weight"),
@@ -997,8 +1000,8 @@ def sandwich_norm(x, residual, post_weight, gate, weight, scale=1.0, gate_rows=N
     [ceil(m / gate_rows), k] (gate_rows None: one row for all rows of x), or None; post_weight None: x is not normed, and
     rstd_x None."""
     m, k = x.shape
-    gate_rows = max(m, 1) if gate_rows is None else gate_rows
-    shape, index, dev, gshape = (m, k), x.get_device(), x.device, _gate_shape(gate, gate_rows, m, k)
+    shape, index, dev = (m, k), x.get_device(), x.device
+    gshape, gate_rows = _gate_shape(gate, max(m, 1) if gate_rows is None else gate_rows, m, k)
     ins = (_arg(x, _BF, shape, index, "x"), _req_given(residual, _BF, shape, index, "residual"),
            _arg(post_weight, _BF, (k,), index, "post_weight"), _arg(gate, _BF, gshape, index, "gate"),
            _req_given(weight, _BF, (k,), index, "weight"))
@@ -1018,8 +1021,8 @@ def sandwich_norm_backward(dy, dh, x, h, post_weight, gate, weight, rstd_x, rstd
     """(dx, dresidual, dweight, dpost_weight, dgate) of sandwich_norm: dx and dresidual bf16, the others fp32
     (dpost_weight and dgate None where post_weight and gate are)."""
     m, k = dy.shape
-    gate_rows = max(m, 1) if gate_rows is None else gate_rows
-    shape, index, dev, gshape = (m, k), dy.get_device(), dy.device, _gate_shape(gate, gate_rows, m, k)
+    shape, index, dev = (m, k), dy.get_device(), dy.device
+    gshape, gate_rows = _gate_shape(gate, max(m, 1) if gate_rows is None else gate_rows, m, k)
     ins = (_arg(dy, _BF, shape, index, "dy"), _arg(dh, _BF, shape, index, "dh"), _req_given(x, _BF, shape, index, "x"),
            _req_given(h, _BF, shape, index, "h"), _arg(post_weight, _BF, (k,), index, "post_weight"),
            _arg(gate, _BF, gshape, index, "gate"), _req_given(weight, _BF, (k,), index, "weight"),
