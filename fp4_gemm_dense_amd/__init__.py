@@ -680,13 +680,17 @@ def dg_activation_backward(dy, z, activation, dz=None, q=None, sf=None, qt=None,
           _arg(dbias, _F32S, (n,), index, "dbias"), m, n, _arg(workspace, _U8S, (nbytes,), index, "workspace"), nbytes)
 
 
+def _check_format(quant_format):
+    if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
+        raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
+
+
 def dg_add_rms_norm(x, residual, weight, h, q, sf, eps, quant_format, rstd=None):
     """h = x + residual; q, sf = quantised h / rms(h) * weight (see include/dg.h).  x, residual, h [m, k] bf16 (residual
     and h may be None), weight [k]; q [m, k] uint8 and sf [k/128, m] fp32 (QUANT_E4M3_F32) or [m, ceil(k/512)] int32
     (QUANT_E4M3_UE8M0), or q [m, k/2] and sf [k/128, m] int32 (QUANT_MXFP4); rstd [m] fp32 or None."""
     m, k = x.shape
-    if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
-        raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
+    _check_format(quant_format)
     shape, dev = (m, k), x.get_device()
     sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
     _call("dg_add_rms_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
@@ -730,8 +734,7 @@ def dg_sandwich_norm(x, residual, post_weight, gate, weight, h, q, sf, quant_for
     x, residual, h [m, k] bf16; post_weight, weight [k] and gate [ceil(m / gate_rows), k] bf16 (post_weight and gate may
     be None); q, sf as dg_add_rms_norm; rstd_x, rstd [m] fp32 or None."""
     m, k = x.shape
-    if quant_format not in (QUANT_E4M3_F32, QUANT_E4M3_UE8M0, QUANT_MXFP4):
-        raise ValueError(f"quant_format: expected QUANT_E4M3_F32, QUANT_E4M3_UE8M0 or QUANT_MXFP4, got {quant_format}")
+    _check_format(quant_format)
     shape, dev, (gshape, gate_rows) = (m, k), x.get_device(), _gate_shape(gate, gate_rows, m, k)
     sf_shape = (m, _kw(k)) if quant_format == QUANT_E4M3_UE8M0 else (k // 128, m)
     _call("dg_sandwich_norm", dev, _arg(x, _BF, shape, dev, "x"), _arg(residual, _BF, shape, dev, "residual"),
@@ -961,6 +964,7 @@ def add_rms_norm(x, residual, weight, eps=1e-6, quant_format=QUANT_E4M3_F32):
     """(q, sf, h, rstd): the quantised norm of h = x + residual (residual None: h is x itself), with h and
     rstd = 1 / rms(h) for the residual stream and the backward pass."""
     m, k = x.shape
+    _check_format(quant_format)
     shape, index, dev = (m, k), x.get_device(), x.device
     xp, rp = _arg(x, _BF, shape, index, "x"), _arg(residual, _BF, shape, index, "residual")
     wp = _arg(weight, _BF, (k,), index, "weight")
@@ -1000,6 +1004,7 @@ def sandwich_norm(x, residual, post_weight, gate, weight, scale=1.0, gate_rows=N
     [ceil(m / gate_rows), k] (gate_rows None: one row for all rows of x), or None; post_weight None: x is not normed, and
     rstd_x None."""
     m, k = x.shape
+    _check_format(quant_format)
     shape, index, dev = (m, k), x.get_device(), x.device
     gshape, gate_rows = _gate_shape(gate, max(m, 1) if gate_rows is None else gate_rows, m, k)
     ins = (_arg(x, _BF, shape, index, "x"), _req_given(residual, _BF, shape, index, "residual"),

@@ -48,3 +48,14 @@ def test_one_gate_for_all_rows(calls, gate_rows):
     for name, args in calls:
         got = ctypes.c_int(args[GATE_ROWS[name]]).value
         assert got >= m, f"{name}: {got}"
+
+
+@pytest.mark.parametrize("fmt", [-1, 3, 1 << 32, (1 << 32) + 1, (1 << 32) + 2])
+def test_unknown_formats_are_refused(calls, fmt):
+    """Also those whose low 32 bits are a format's: codes and scales would be another format's than the tensors say."""
+    x, w = torch.zeros(8, 512, dtype=torch.bfloat16), torch.zeros(512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="quant_format: expected"):
+        dgm.sandwich_norm(x, x, None, None, w, quant_format=fmt)
+    with pytest.raises(ValueError, match="quant_format: expected"):
+        dgm.add_rms_norm(x, x, w, quant_format=fmt)
+    assert not calls
