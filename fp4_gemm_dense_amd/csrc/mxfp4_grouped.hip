@@ -15,6 +15,8 @@
 // at 5.0 TB/s); with many the schedule, as the dense GEMM, and the groups' last tiles (8192 rows over 8
 // 144-150 us, 3.2-3.3 PFLOP/s; 4000 rows over 8 of 4096 x 2048 34, 1.6 rounds of units); along K the stores of D (4000 rows in 8 groups of 4096 x 2048 46-51, 134 MB of D).
 #include <algorithm>
+#include <cstdio>
+#include <cstdlib>
 
 #include "../../include/dg.h"
 #include "mxfp4_tile.hpp"
@@ -27,6 +29,7 @@ using KGroupParams = Mxfp4GroupedParams<MX_KGROUP>;
 
 struct GroupedPlan {
   int tile, grid;
+  long long most;   // tiles that the call can have
 };
 
 // The tile with the least estimated time.  units(tile): how many of it the call has by the host's
@@ -35,7 +38,7 @@ struct GroupedPlan {
 template <typename F>
 static GroupedPlan plan_grouped(int groups, int kb, int cus, double slow, F units) {
   const int force = mxfp4_forced();
-  GroupedPlan best{2, 0};
+  GroupedPlan best{2, 0, 0};
   double best_t = 1e30;
   for (int id = 0; id < kMxGroupedTileCount; ++id) {
     const Mxfp4TileInfo t = mxfp4_tile_info(id);
@@ -45,7 +48,7 @@ static GroupedPlan plan_grouped(int groups, int kb, int cus, double slow, F unit
     const double us = id == force ? 0.0 : mxfp4_tile_time(id, guess, kb, cus) * (t.bm == 256 ? slow : 1.0);
     if (us < best_t - 1e-9) {
       best_t = us;
-      best = {id, (int)std::min<long long>(most, cus)};
+      best = {id, (int)std::min<long long>(most, cus), most};
     }
   }
   return best;
@@ -75,6 +78,15 @@ static GroupedPlan plan_kgroup(int m, int n, int kb, int groups, int cus) {
   return plan_grouped(groups, std::max(1, kb / groups), cus, 0.95, [=](const Mxfp4TileInfo& t, long long* most) {
     return *most = (long long)((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn) * groups;
   });
+}
+
+// (with DG_LOG=1)
+static void log_grouped_plan(const char* call, int m, int n, int k, int groups, const GroupedPlan& pl) {
+  const char* log = std::getenv("DG_LOG");
+  if (!log || log[0] != '1') return;
+  const Mxfp4TileInfo t = mxfp4_tile_info(pl.tile);
+  std::fprintf(stderr, "[dg] %s m=%d n=%d k=%d groups=%d -> tile %dx%d, %d K group%s, at most %lld tiles, %d workgroups\n", call, m, n, k,
+               groups, t.bm, t.bn, t.kg, t.kg > 1 ? "s" : "", pl.most, pl.grid);
 }
 
 template <typename P>
@@ -182,6 +194,7 @@ int dg_m_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, con
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
     const GroupedPlan pl = plan_ragged(m, n, k, num_groups, dg_get_num_cus());
+    log_grouped_plan("m_grouped_mxfp4_gemm_nt_ragged", m, n, k, num_groups, pl);
     const RaggedParams p = grouped_params<RaggedParams>(a, a_sf, b, b_sf, d, m, n, k, mxfp4_tile_info(pl.tile), ms, num_groups);
     hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     const hipError_t e = launch_mxfp4_tile(p, pl.tile, pl.grid, hs, group_table_bytes(num_groups));
@@ -203,6 +216,7 @@ int dg_k_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, con
     DeviceInfo di = current_device_info();
     if (!di.ok) return DG_ERR_NO_DEVICE;
     const GroupedPlan pl = plan_kgroup(m, n, k / 128, num_groups, dg_get_num_cus());
+    log_grouped_plan("k_grouped_mxfp4_gemm_nt_ragged", m, n, k, num_groups, pl);
     const KGroupParams p = grouped_params<KGroupParams>(a, a_sf, b, b_sf, d, m, n, k, mxfp4_tile_info(pl.tile), ms, num_groups);
     const hipError_t e = launch_mxfp4_tile(p, pl.tile, pl.grid, reinterpret_cast<hipStream_t>(stream), group_table_bytes(num_groups));
     return e == hipSuccess ? DG_OK : DG_ERR_HIP;
