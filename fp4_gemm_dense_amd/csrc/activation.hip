@@ -8,9 +8,10 @@
 //
 // Bound: HBM.  An element of dz costs 2 bytes of z and 2 of dy (gated: 1) of reading and
 // 17/32 of writing per direction.  Measured (one MI355X, both directions and dbias): 4096 x 16384
-// gated with SiLU 82 us (floor at a copy's 5.1 TB/s 53), SiLU alone 91 (66), the identity 83; 2001 x
+// gated with SiLU 78-82 us (floor at a copy's 5.1 TB/s 53), SiLU alone 87-91 (66), the identity 83; 2001 x
 // 4096 GELU 15.4 and 4.6 of the sums (8.1: 512 tiles on 256 CUs, whose reads, arithmetic and writes follow
-// one another); 130 x 4096 gated 6.8 + 2.7.  Of the first, 9 us are dbias and 15 the columns.
+// one another); 130 x 4096 gated 6.8 + 2.7.  Of the first, 9 us are dbias and 15 the columns.  (The 128-row
+// gated kernel has 164 registers: one workgroup on a CU.  The ungated one has 115, the 32-row ones up to 99: two.)
 #include <algorithm>
 
 #include "../../include/dg.h"
@@ -176,8 +177,11 @@ __global__ void __launch_bounds__(256) activation_dbias_kernel(const float* part
 
 // Row tiles of 128, or of 32 where those serve a quarter of the chip's 256 CUs or fewer (130 x 4096
 // gated 14.0 -> 11.6 us, 500 x 2048 13.1 -> 12.2), except where the partial rows would then need a
-// launch that they do not need now (128 x 8192 9.2, 11.8 with 32), in chunks that give every
-// CU two workgroups.  (Functions of the sizes alone, so that the order of the sums is, too.)
+// launch that they do not need now (128 x 8192 9.2, 11.8 with 32), in chunks of as many tiles as give
+// at most two workgroups to each of 256 CUs (one chunk where a row of tiles alone has more).  A chunk is
+// a whole number of tiles, so that sizes just past an even share have far fewer workgroups (GELU 2048 x
+// 4096 512, 18.3 us, 2049 x 4096 288, 21.5; SiLU 4096 x 32768 512, 173 us, 4096 x 32896 257, 256).
+// (Functions of the sizes alone, so that the order of the sums is, too.)
 struct ActPlan {
   int rows, per, chunks, sums;   // sums: the chunks that hold rows (the last block of 128 is filled up)
 };

@@ -8,9 +8,11 @@
 //   erf      u * Phi(u), Phi the normal distribution: GELU
 // Phi comes from its tail, Phi(-a) = exp(-a^2 / 2) Q(a) for a >= 0, Q = t P(t) with t = 1 / (1 + 0.31 a): the
 // form of Hastings' approximations (Approximations for Digital Computers, 1955), with P fitted here to Q
-// itself, so that the tail keeps its relative error: 4.5e-7 of Q in fp32, and a^2 2^-24 from the exponent.
-// w beyond +-128 is held there (exp is 0 or infinity long before).  A NaN stays one; u = -infinity
-// gives NaN except in ReLU, since 0 times infinity is none.
+// itself, so that the tail keeps its relative error: measured against erfc in fp64 at 4 million a, 5e-7 of Q
+// (its two fp32 roundings among it), 5.3e-7 of the tail up to a = 1, 9e-7 up to 4, and a^2 2^-24 from the
+// exponent beyond, to 12.9, where exp leaves fp32's range.
+// w beyond +-128 is held there (exp is 0 or infinity long before).  A NaN stays one.  u = -infinity
+// stays in the identity, gives 0 in ReLU and NaN in the others, since 0 times infinity is none.
 #pragma once
 
 #include "dg_device.hpp"

@@ -9,9 +9,10 @@
 //
 // Bound: as the dense GEMM, and the epilogue behind a unit's last product, which nothing
 // overlaps but the next unit's copies.  Measured (one MI355X; in brackets the dense GEMM, whose D
-// is [m, n]): 4096 x 16384 x 7168 gated with SiLU 232-239 us (225-233), with z 278 (237-244: z is 134 MB
-// more); 4096 x 7168 x 16384 with residual 247 (235); 4096 x 24576 x 1536 without 107 (98), SiLU 119-126,
-// gated SiLU with z 128, GELU 150-160 (its polynomial for 128 values of a lane in a unit); 2001 x 4096 x
+// is [m, n]): 4096 x 16384 x 7168 gated with SiLU 229 us (225), with z, 134 MB more, 241, and in
+// passes one upon another, at the clock that power then leaves, 248-258 and 261-272 (230-257); 4096 x
+// 7168 x 16384 with residual 247 (235); 4096 x 24576 x 1536 without 107 (98), SiLU 119-126, gated
+// SiLU with z 128, GELU 150-160 (its polynomial for 128 values of a lane in a unit); 2001 x 4096 x
 // 7168 GELU with residual and z 41 (35); 1 x 4096 x 7168 6.6 (6.1).
 #include <algorithm>
 

@@ -926,7 +926,8 @@ static int launch_norm_format(const P& p, int format, void* stream) {
 // with twice the waves (2048 x 9216 47.7 -> 38.2, 4096 x 12288 101.5 -> 78.6; 4096 x 14336 106, 114 so, 4096 x
 // 16384, one row on a CU then, 105, 130 so).
 static int launch_sandwich(const SandwichParams& p, int format, void* stream) {
-  if ((p.k > 4096 && p.k <= 7168 && p.m >= 2048) || (p.k > 8192 && p.k <= 12288)) return launch_norm_format(SandwichTightParams{p}, format, stream);
+  if ((p.k > 4096 && p.k <= 7168 && p.m >= 2048) || (p.k > 8192 && p.k <= 12288))
+    return launch_norm_format(SandwichTightParams{p}, format, stream);
   return launch_norm_format(p, format, stream);
 }
 

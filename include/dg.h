@@ -446,7 +446,8 @@ size_t dg_mxfp4_gemm_workspace_bytes(int m, int n, int k, int num_cus);
  *   b    [num_groups, n, k/2], b_sf [num_groups, k/128, n]   (dg_quantize_mxfp4's q and sf; its
  *        qt and sft, with the weights' n and k changed about, for the input's gradient)
  *   d    [m, n] bf16
- * Requirements: as dg_mxfp4_gemm_nt's (b: per group); num_groups <= 1024, else DG_ERR_UNSUPPORTED.
+ * Requirements: as dg_mxfp4_gemm_nt's (b: per group; m > 0 here, too: a layer without any rows makes no call);
+ *   num_groups <= 1024, else DG_ERR_UNSUPPORTED.
  */
 int dg_m_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, const int32_t* b_sf,
                                       const int32_t* ms, uint16_t* d, int m, int n, int k, int num_groups, void* stream);
@@ -461,8 +462,8 @@ int dg_m_grouped_mxfp4_gemm_nt_ragged(const uint8_t* a, const int32_t* a_sf, con
  *          group's are not written
  *   qt     [k, 64 B]     E2M1 pairs along the rows
  *   sft    [B, k]        int32; blocks behind the last group's are not written (in qt neither)
- * Values, exponents and rounding as dg_quantize_mxfp4.  Requirements: k % 128 == 0, m + 127 at most
- * 2^31 - 1, num_groups <= 1024 (else DG_ERR_UNSUPPORTED).
+ * Values, exponents and rounding as dg_quantize_mxfp4.  Requirements: num_groups, m, k > 0; k % 128 == 0,
+ * m + 127 at most 2^31 - 1, num_groups <= 1024 (else DG_ERR_UNSUPPORTED).
  */
 int dg_quantize_mxfp4_ragged(const void* x, int x_type, const int32_t* ms, uint8_t* q, int32_t* sf, uint8_t* qt, int32_t* sft,
                              int m, int k, int num_groups, void* stream);
@@ -512,7 +513,8 @@ int dg_mxfp4_linear(const uint8_t* a, const int32_t* a_sf, const uint8_t* b, con
  * itself), as the operands that they read.
  *   dz[i][j] = dy[i][j] * act'(z[i][j]), and gated, with g = z[i][j] and p = z[i][n/2 + j],
  *   dz[i][j] = dy[i][j] * p * act'(g),  dz[i][n/2 + j] = dy[i][j] * act(g)
- * (ReLU's derivative at 0 is 0), rounded to bf16.
+ * in fp32 and from the left (a dy * p past its range is an infinity, and NaN times a slope of 0), rounded to bf16.
+ * ReLU's derivative is 0 at 0 and for a NaN; the other activations' pass a NaN on (none: 1).
  *   dy   [m, n] bf16 (gated: [m, n/2])
  *   z    [m, n] bf16 from the forward pass; may be NULL with DG_ACT_NONE (ungated)
  *   dz   [m, n] bf16, or NULL (may be z, or ungated dy, itself)
@@ -667,7 +669,8 @@ int dg_get_num_cus(void);
  * over the workgroups, and for K >= 3584 applies the same split rule to their
  * count on the device (a second kernel then sums the split tiles).  For it this
  * function reports the tile shape and splits = 1.
- * Exposed so callers can log the choice (DG_LOG=1 prints it on every call).
+ * Exposed so callers can log the choice (DG_LOG=1 prints it on every call, those of the
+ * MXFP4 products included).
  */
 typedef struct dg_plan {
   int block_m;

@@ -72,3 +72,17 @@ def test_gradients_are_the_products_of_their_operands(dg, m, n, k, act, gated):
     ref = X.linear_epilogue_backward(bf16_bits_to_f64(dy), bf16_bits_to_f64(bits(z)), act, gated)
     for v in (X.dequant_mxfp4(q.cpu().numpy(), sf.cpu().numpy()), X.dequant_mxfp4(qt.cpu().numpy(), sft.cpu().numpy())[:, :m].T):
         assert np.linalg.norm(v - ref) < 0.2 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("act,want", [("none", 1.0), ("relu", 0.0), ("silu", np.nan), ("gelu", np.nan), ("gelu_tanh", np.nan)])
+def test_slopes_of_a_nan(dg, act, want):
+    """As include/dg.h has them; a gated layer's other half takes act(NaN), which is a NaN in all of them."""
+    z = bf(1, 1, 512)
+    z[0, 7] = 0x7fc0
+    z[0, 256:] = 0x3f80
+    one = np.full((1, 256), 0x3f80, np.uint16)
+    got = dg.activation_backward(dev(one), dev(z[:, :256].copy()), ACTS[act])[4].cpu().numpy()
+    assert np.array_equal(got[7], want, equal_nan=True) and np.isfinite(np.delete(got, 7)).all()
+    got = dg.activation_backward(dev(one), dev(z), ACTS[act] | GATED)[4].cpu().numpy()
+    assert np.array_equal(got[7], want, equal_nan=True) and np.isnan(got[256 + 7])
+    assert np.isfinite(np.delete(got, (7, 256 + 7))).all()
